@@ -358,6 +358,104 @@ int mok_quantize_mxfp8_f32(const float* src, int64_t rows, int32_t K, uint8_t* c
 int mok_quantize_mxfp4_f32(const float* src, int64_t rows, int32_t K, uint8_t* codes,
                            uint8_t* scales, void* stream);
 
+/* ---------------------------------------------------------------- balance loss of the router
+ * The load-balancing loss of a batch or of packed sequences, with the experts' counts, and its
+ * gradient for the logits. Sequence s holds the tokens [seq_offsets[s], seq_offsets[s+1]), n_s of
+ * them; seq_offsets NULL means one sequence over all T tokens (then n_seq must be 1).
+ *   p[t,e] = softmax(logits[t,:])_e
+ *   c[s,e] = picks of expert e by the tokens of s (topk_idx entries outside [0, E) count nowhere)
+ *   f[s,e] = E c[s,e] / (k n_s)      P[s,e] = (1 / n_s) sum_{t in s} p[t,e]
+ *   loss   = (alpha / n_seq) sum_s sum_e f[s,e] P[s,e]
+ *   dlogits[t,e] = dloss (alpha / (n_seq n_s)) p[t,e] (f[s,e] - sum_e' f[s,e'] p[t,e'])
+ * (the counts are piecewise constant: the gradient goes through P). An empty sequence adds
+ * nothing and counts in n_seq. A token of no sequence adds nothing, and its dlogits row is zero;
+ * what its logits and picks hold is not looked at. A logit of -inf has probability 0; a row of
+ * nothing but -inf has no probabilities and a zero gradient (its picks still count). NaN and
+ * +inf logits make their row's probabilities NaN.
+ *
+ *   logits [T, E] float32, topk_idx [T, k] int32, seq_offsets [n_seq + 1] int32, nondecreasing
+ *   (device; values outside [0, T] are taken as the nearer end)
+ *   loss [1] float32, counts [n_seq, E] int32, mean_prob [n_seq, E] float32 (P): outputs
+ *   dloss [1] float32 (device): the upstream gradient; counts: the forward's
+ *   dlogits [T, E] float32, overwritten; must not overlap logits
+ * Requires 1 <= k <= E <= 1024, k <= 64, 1 <= n_seq <= 65535, 0 <= T, T k < 2^31. T == 0 gives a
+ * zero loss. Softmax and sums in float32 or wider; no float atomics: bit-identical reruns.
+ * ws: device scratch of mok_balance_loss_workspace_bytes(...) bytes, 8-byte aligned; nothing in
+ * it is needed after the call's own work. */
+int mok_balance_loss_workspace_bytes(int64_t T, int32_t E, int32_t n_seq, size_t* bytes);
+int mok_balance_loss(const float* logits, const int32_t* topk_idx, int64_t T, int32_t E, int32_t k,
+                     const int32_t* seq_offsets, int32_t n_seq, float alpha, float* loss,
+                     int32_t* counts, float* mean_prob, void* ws, size_t ws_bytes, void* stream);
+int mok_balance_loss_backward(const float* logits, const int32_t* counts, int64_t T, int32_t E,
+                              int32_t k, const int32_t* seq_offsets, int32_t n_seq, float alpha,
+                              const float* dloss, float* dlogits, void* stream);
+
+/* ---------------------------------------------------------------- residual RMS norm
+ * Residual addition and root-mean-square norm of rows, and the backward.
+ *   h = x + residual, rounded to the storage type (residual NULL: h = x)
+ *   rstd[t] = 1 / sqrt(mean_i h[t,i]^2 + eps),   y[t,i] = h[t,i] rstd[t] weight[i]
+ * Outputs, each NULL where not wanted (one at least is): h [rows, d] and y [rows, d] in the
+ * storage type, rstd [rows] float32, and y in MXFP8 (both or none): codes [rows, d] E4M3 and
+ * scales [rows, d / 32] E8M0 in the layout and by the rules of mok_quantize_mxfp8_f32, from the
+ * float32 y. A 32-value block of y with an infinity or a NaN is all NaN (codes 0x7F, scale 0xFF).
+ * x, residual, weight [d]: float32 or bf16 (io_dtype). h may be x or residual, and y may be x or
+ * residual where h is not the same one; other overlaps are not allowed. d >= 1, d % 32 == 0 with
+ * codes, d <= 2^24; rows < 2^31; eps >= 0. Rows of d % 8 == 0, d <= 16384, with 16-byte aligned
+ * pointers are read once; others take a slower form.
+ *
+ * Backward, g = dy weight, n = h rstd:
+ *   dx[t,i] = rstd[t] (g[t,i] - n[t,i] mean_j(g[t,j] n[t,j])) + dh[t,i]
+ *   dweight[i] = sum_t dy[t,i] n[t,i]
+ * h, rstd: the forward's. dh [rows, d]: the gradient that reaches h from the residual stream
+ * (NULL: none). dx is the gradient of both x and residual. dx [rows, d] in the storage type; it
+ * may be dy or dh. dweight [d] float32, overwritten (zeros with rows == 0), NULL: not wanted (then
+ * ws may be NULL). No atomics: bit-identical reruns. ws: device scratch, 16-byte aligned. */
+int mok_rmsnorm(const void* x, const void* residual, const void* weight, int64_t rows, int32_t d,
+                int32_t io_dtype, float eps, void* h, float* rstd, void* y, uint8_t* codes,
+                uint8_t* scales, void* stream);
+int mok_rmsnorm_backward_workspace_bytes(int64_t rows, int32_t d, size_t* bytes);
+int mok_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const void* weight,
+                         const void* dh, int64_t rows, int32_t d, int32_t io_dtype, void* dx,
+                         float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- router backward
+ * Gradients through mok_route to its input and weight, with the picks held fixed: from dtopk_w
+ * [T, k] (mok_moe_backward's, the gradient of the routing weights) and, where given, dlogits
+ * [T, E] (mok_balance_loss_backward's):
+ *   dl[t,e] = dlogits[t,e] + sum_{j: topk_idx[t,j] = e} w[t,j] (dw[t,j] - sum_i w[t,i] dw[t,i])
+ *   dx[t,i] = dx_in[t,i] + sum_e dl[t,e] w_router[e,i]
+ *   dw_router[e,i] = sum_t dl[t,e] x[t,i]
+ * x [T, d], w_router [E, d], dx_in [T, d] (NULL: none; the experts' share of the layer's dx), dx
+ * [T, d]: float32 or bf16 (io_dtype); topk_idx [T, k] int32, topk_w, dtopk_w [T, k] and dlogits
+ * (NULL: none) float32; dw_router [E, d] float32, overwritten (zeros with T == 0). dx or dw_router
+ * may be NULL where not wanted. Picks outside [0, E) take no part; an expert named twice adds up.
+ * dx may be dx_in, and overlaps nothing else. Sums in float32 (bf16 operands enter as they are,
+ * dl with at least 16 significant bits for dx and 24 for dw_router); each output is rounded once;
+ * no atomics: bit-identical reruns. Sizes as mok_route, d <= 2^24, T k < 2^31.
+ * ws: device scratch of mok_route_backward_workspace_bytes(...) bytes, 16-byte aligned; needed for
+ * dw_router only. */
+int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t io_dtype,
+                                       size_t* bytes);
+int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_idx,
+                       const float* topk_w, const float* dtopk_w, const float* dlogits,
+                       const void* dx_in, int64_t T, int32_t d, int32_t E, int32_t k,
+                       int32_t io_dtype, void* dx, float* dw_router, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/* ---------------------------------------------------------------- microscaled product
+ * C[m,n] = sum_k A[m,k] B[n,k] of operands in the mok_quantize_mx* layouts: codes [rows, K]
+ * (MXFP8) or [rows, K/2] (MXFP4), E8M0 scales [rows, K/32]; a_dtype and b_dtype are MOK_MXFP8 or
+ * MOK_MXFP4, in any combination. c [M, N] bf16 or float32 (out_dtype: MOK_BF16, MOK_FP32), rounded
+ * once from float32 sums. K % 32 == 0, 32 <= K <= 2^22; M, N >= 0, < 2^31 (and fewer than 2^23
+ * tiles). Codes and c start on 16 bytes. A scale of 0xFF (NaN) or a NaN code makes what it enters
+ * NaN. ws: device scratch of mok_mx_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned (0 bytes:
+ * may be NULL). Bit-identical reruns. */
+int mok_mx_gemm_workspace_bytes(int64_t M, int64_t N, int32_t K, size_t* bytes);
+int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype,
+                const uint8_t* b_codes, const uint8_t* b_scales, int32_t b_dtype, int64_t M,
+                int64_t N, int32_t K, int32_t out_dtype, void* c, void* ws, size_t ws_bytes,
+                void* stream);
+
 /* ---------------------------------------------------------------- device error word
  * The persistent work loop bounds every wait; a wait that runs out sets a nonzero error word
  * in the workspace and the loop exits. This SYNCHRONOUS call waits for `stream`, then reads

@@ -35,7 +35,11 @@ EXPORTS = ["mok_status_string", "mok_version", "mok_route", "mok_topk",
            "mok_moe_forward", "mok_moe_workspace_region", "mok_moe_backward",
            "mok_moe_backward_workspace_bytes", "mok_moe_backward_error", "mok_pull_gather",
            "mok_push_dispatch", "mok_quantize_mxfp8", "mok_quantize_mxfp4",
-           "mok_quantize_mxfp8_f32", "mok_quantize_mxfp4_f32", "mok_get_device_error"]
+           "mok_quantize_mxfp8_f32", "mok_quantize_mxfp4_f32", "mok_get_device_error",
+           "mok_balance_loss_workspace_bytes", "mok_balance_loss", "mok_balance_loss_backward",
+           "mok_rmsnorm", "mok_rmsnorm_backward_workspace_bytes", "mok_rmsnorm_backward",
+           "mok_route_backward_workspace_bytes", "mok_route_backward",
+           "mok_mx_gemm_workspace_bytes", "mok_mx_gemm"]
 
 
 class MokError(RuntimeError):
@@ -113,6 +117,17 @@ _lib.mok_quantize_mxfp4_f32.argtypes = [_P, _I64, _I32, _P, _P, _P]
 _lib.mok_pull_gather.argtypes = [_P, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _P]
 _lib.mok_push_dispatch.argtypes = [_P, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I64, _P, _P, _P,
                                    _P]
+_F32 = ctypes.c_float
+_lib.mok_balance_loss_workspace_bytes.argtypes = [_I64, _I32, _I32, ctypes.POINTER(_SZ)]
+_lib.mok_balance_loss.argtypes = [_P, _P, _I64, _I32, _I32, _P, _I32, _F32, _P, _P, _P, _P, _SZ, _P]
+_lib.mok_balance_loss_backward.argtypes = [_P, _P, _I64, _I32, _I32, _P, _I32, _F32, _P, _P, _P]
+_lib.mok_rmsnorm.argtypes = [_P, _P, _P, _I64, _I32, _I32, _F32, _P, _P, _P, _P, _P, _P]
+_lib.mok_rmsnorm_backward_workspace_bytes.argtypes = [_I64, _I32, ctypes.POINTER(_SZ)]
+_lib.mok_rmsnorm_backward.argtypes = [_P, _P, _P, _P, _P, _I64, _I32, _I32, _P, _P, _P, _SZ, _P]
+_lib.mok_route_backward_workspace_bytes.argtypes = [_I64, _I32, _I32, _I32, ctypes.POINTER(_SZ)]
+_lib.mok_route_backward.argtypes = [_P] * 7 + [_I64] + [_I32] * 4 + [_P, _P, _P, _SZ, _P]
+_lib.mok_mx_gemm_workspace_bytes.argtypes = [_I64, _I64, _I32, ctypes.POINTER(_SZ)]
+_lib.mok_mx_gemm.argtypes = [_P, _P, _I32, _P, _P, _I32, _I64, _I64, _I32, _I32, _P, _P, _SZ, _P]
 _lib.mok_get_device_error.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32), _P]
 for _n in EXPORTS:
     if _n not in ("mok_status_string", "mok_version"):
@@ -262,6 +277,204 @@ def mok_get_device_error(workspace, stream=None) -> int:
     _check("mok_get_device_error", _lib.mok_get_device_error(_ptr(workspace), ctypes.byref(err),
                                                              _stream(stream)))
     return err.value
+
+
+# ------------------------------------------------------- operators around the layer
+#
+# These check what they marshal: a tensor of another type or shape, a strided one, or one on
+# another device than the first raises MokError (MOK_EINVAL) before anything is enqueued. The work
+# goes to the tensors' own device: its current stream, or `stream`, which must belong to it.
+
+class _Args:
+    """Checks the tensors of one call and holds the device they share."""
+
+    def __init__(self, fn: str):
+        self.fn, self.dev = fn, None
+
+    def bad(self):
+        raise MokError(self.fn, MOK_EINVAL)
+
+    def __call__(self, t, dtype, shape=None):
+        """Pointer of t: contiguous, on the call's GPU, of this dtype and shape (None: any)."""
+        if t is None:
+            return None
+        dev = t.get_device()
+        if self.dev is None:
+            self.dev = dev
+        if (dev != self.dev or dev < 0 or t.dtype is not dtype or not t.is_contiguous()
+                or (shape is not None and t.shape != shape)):
+            self.bad()
+        return t.data_ptr()
+
+    def scratch(self, ws):
+        """(pointer, bytes) of a workspace tensor of any dtype."""
+        if ws is None:
+            return None, 0
+        if ws.get_device() != self.dev or not ws.is_contiguous():
+            self.bad()
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
+    def run(self, f, *args, stream=None):
+        import torch
+        if self.dev == torch.cuda.current_device():
+            _check(self.fn, f(*args, _stream(stream)))
+        else:
+            with torch.cuda.device(self.dev):
+                _check(self.fn, f(*args, _stream(stream)))
+
+
+def _io_of(a: _Args, t) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return MOK_BF16
+    if t.dtype is not torch.float32:
+        a.bad()
+    return MOK_FP32
+
+
+def mok_balance_loss_workspace_bytes(T: int, E: int, n_seq: int = 1) -> int:
+    out = _SZ(0)
+    _check("mok_balance_loss_workspace_bytes",
+           _lib.mok_balance_loss_workspace_bytes(T, E, n_seq, ctypes.byref(out)))
+    return out.value
+
+
+def mok_balance_loss(logits, topk_idx, alpha: float, loss, counts, mean_prob, ws, *,
+                     seq_offsets=None, stream=None) -> None:
+    """Balance loss of logits [T, E] float32 and picks [T, k] int32: loss [1], counts [S, E] int32
+    and mean probabilities [S, E] float32 of the S packed sequences of seq_offsets [S + 1] int32
+    (None: one sequence). ws: mok_balance_loss_workspace_bytes(T, E, S) bytes."""
+    import torch
+    a = _Args("mok_balance_loss")
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        a.bad()
+    (T, E), k = logits.shape, topk_idx.shape[1]
+    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    f32, i32 = torch.float32, torch.int32
+    args = (a(logits, f32), a(topk_idx, i32, (T, k)), T, E, k, a(seq_offsets, i32, (S + 1,)), S,
+            alpha, a(loss, f32, (1,)), a(counts, i32, (S, E)), a(mean_prob, f32, (S, E)))
+    a.run(_lib.mok_balance_loss, *args, *a.scratch(ws), stream=stream)
+
+
+def mok_balance_loss_backward(logits, counts, k: int, alpha: float, dloss, dlogits, *,
+                              seq_offsets=None, stream=None) -> None:
+    """Gradient of mok_balance_loss for the logits: dlogits [T, E] float32 (overwritten), with the
+    forward's counts and the upstream gradient dloss [1] (both on the device)."""
+    import torch
+    a = _Args("mok_balance_loss_backward")
+    if logits.dim() != 2:
+        a.bad()
+    T, E = logits.shape
+    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    f32, i32 = torch.float32, torch.int32
+    args = (a(logits, f32), a(counts, i32, (S, E)), T, E, k, a(seq_offsets, i32, (S + 1,)), S,
+            alpha, a(dloss, f32, (1,)), a(dlogits, f32, (T, E)))
+    a.run(_lib.mok_balance_loss_backward, *args, stream=stream)
+
+
+def mok_rmsnorm(x, weight, eps: float, *, residual=None, h=None, rstd=None, y=None, codes=None,
+                scales=None, stream=None) -> None:
+    """h = x + residual, y = h / rms(h) * weight for rows x [T, d] float32 or bf16. Outputs, those
+    that are given: h, y [T, d], rstd [T] float32, y in MXFP8 as codes [T, d] and scales
+    [T, d / 32] uint8."""
+    import torch
+    a = _Args("mok_rmsnorm")
+    if x.dim() != 2:
+        a.bad()
+    (T, d), t, u8 = x.shape, x.dtype, torch.uint8
+    io = _io_of(a, x)
+    args = (a(x, t), a(residual, t, (T, d)), a(weight, t, (d,)), T, d, io, eps, a(h, t, (T, d)),
+            a(rstd, torch.float32, (T,)), a(y, t, (T, d)), a(codes, u8, (T, d)),
+            a(scales, u8, (T, d // 32)))
+    a.run(_lib.mok_rmsnorm, *args, stream=stream)
+
+
+def mok_rmsnorm_backward_workspace_bytes(T: int, d: int) -> int:
+    out = _SZ(0)
+    _check("mok_rmsnorm_backward_workspace_bytes",
+           _lib.mok_rmsnorm_backward_workspace_bytes(T, d, ctypes.byref(out)))
+    return out.value
+
+
+def mok_rmsnorm_backward(dy, h, rstd, weight, dx, dweight=None, ws=None, *, dh=None,
+                         stream=None) -> None:
+    """Backward of mok_rmsnorm: dx [T, d] (the gradient of x and of residual; dh: what reaches h
+    from the residual stream) and dweight [d] float32 (with ws of
+    mok_rmsnorm_backward_workspace_bytes(T, d) bytes)."""
+    import torch
+    a = _Args("mok_rmsnorm_backward")
+    if dy.dim() != 2:
+        a.bad()
+    (T, d), t, f32 = dy.shape, dy.dtype, torch.float32
+    io = _io_of(a, dy)
+    args = (a(dy, t), a(h, t, (T, d)), a(rstd, f32, (T,)), a(weight, t, (d,)), a(dh, t, (T, d)),
+            T, d, io, a(dx, t, (T, d)), a(dweight, f32, (d,)))
+    a.run(_lib.mok_rmsnorm_backward, *args, *a.scratch(ws), stream=stream)
+
+
+def mok_route_backward_workspace_bytes(T: int, d: int, E: int, dtype) -> int:
+    import torch
+    out = _SZ(0)
+    io = {torch.float32: MOK_FP32, torch.bfloat16: MOK_BF16}.get(dtype, -1)
+    _check("mok_route_backward_workspace_bytes",
+           _lib.mok_route_backward_workspace_bytes(T, d, E, io, ctypes.byref(out)))
+    return out.value
+
+
+def mok_route_backward(x, w_router, topk_idx, topk_w, dtopk_w, dx=None, dw_router=None, ws=None, *,
+                       dlogits=None, dx_in=None, stream=None) -> None:
+    """Gradients through mok_route with the picks held fixed: dx [T, d] (dx_in added) and
+    dw_router [E, d] float32 (with ws of mok_route_backward_workspace_bytes(T, d, E, x.dtype)
+    bytes), from dtopk_w [T, k] and, where given, dlogits [T, E]."""
+    import torch
+    a = _Args("mok_route_backward")
+    if x.dim() != 2 or w_router.dim() != 2 or topk_idx.dim() != 2:
+        a.bad()
+    (T, d), E, k = x.shape, w_router.shape[0], topk_idx.shape[1]
+    t, f32 = x.dtype, torch.float32
+    io = _io_of(a, x)
+    args = (a(x, t), a(w_router, t, (E, d)), a(topk_idx, torch.int32, (T, k)),
+            a(topk_w, f32, (T, k)), a(dtopk_w, f32, (T, k)), a(dlogits, f32, (T, E)),
+            a(dx_in, t, (T, d)), T, d, E, k, io, a(dx, t, (T, d)), a(dw_router, f32, (E, d)))
+    a.run(_lib.mok_route_backward, *args, *a.scratch(ws), stream=stream)
+
+
+def mok_mx_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    out = _SZ(0)
+    _check("mok_mx_gemm_workspace_bytes",
+           _lib.mok_mx_gemm_workspace_bytes(M, N, K, ctypes.byref(out)))
+    return out.value
+
+
+def mok_mx_gemm(a_codes, a_scales, b_codes, b_scales, c, ws=None, *, stream=None) -> None:
+    """c [M, N] (bf16 or float32) = A B^T of quantised rows: codes [rows, K] (MXFP8) or
+    [rows, K / 2] (MXFP4) and scales [rows, K / 32], all uint8, as
+    mok_quantize_mxfp8 / mok_quantize_mxfp4 write them; the format of each operand is
+    read from its shapes. ws: mok_mx_gemm_workspace_bytes(M, N, K) bytes."""
+    import torch
+    a = _Args("mok_mx_gemm")
+    if a_scales.dim() != 2 or b_scales.dim() != 2 or a_codes.dim() != 2 or b_codes.dim() != 2:
+        a.bad()
+    M, N, K, u8 = a_scales.shape[0], b_scales.shape[0], 32 * a_scales.shape[1], torch.uint8
+
+    def fmt(codes):
+        if codes.shape[1] == K:
+            return MOK_MXFP8
+        if 2 * codes.shape[1] != K:
+            a.bad()
+        return MOK_MXFP4
+
+    fa, fb = fmt(a_codes), fmt(b_codes)
+    if c.dtype is torch.bfloat16:
+        out = MOK_BF16
+    elif c.dtype is torch.float32:
+        out = MOK_FP32
+    else:
+        a.bad()
+    args = (a(a_codes, u8, (M, a_codes.shape[1])), a(a_scales, u8), fa,
+            a(b_codes, u8, (N, b_codes.shape[1])), a(b_scales, u8, (N, K // 32)), fb, M, N, K, out,
+            a(c, c.dtype, (M, N)))
+    a.run(_lib.mok_mx_gemm, *args, *a.scratch(ws), stream=stream)
 
 
 # ------------------------------------------------------------------------ layer helper

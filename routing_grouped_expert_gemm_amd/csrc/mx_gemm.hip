@@ -1,0 +1,500 @@
+// Product of two microscaled operands: C[m,n] = sum_k A[m,k] B[n,k], A [M, K] and B [N, K] in
+// MXFP8 (E4M3) or MXFP4 (E2M1), one E8M0 scale per 32 values along K, both in the layout that the
+// mok_quantize_mx* entry points write (row-major codes and scales); C in bf16 or float32.
+//
+// Everything runs on the scaled MFMA 32x32x64, which takes the codes and the scales as they are
+// and accumulates in float32. Its operands: a lane (h, r) = (lane / 32, lane % 32) carries row r
+// and the scale of the instruction's 32-value block h. An E2M1 lane holds block h's 16 code
+// bytes; an E4M3 lane holds 16 of the 32 values of block 0 (its half h) and 16 of block 1. K may
+// be permuted freely as long as both operands agree, so the instructions of a step of 256 values
+// pair block s with block 4 + s (s = 0 .. 3): lane half h then needs the scales 4 h .. 4 h + 3 of
+// its row, one aligned word, and instruction s picks byte s of it (op_sel).
+// B is the first operand, so a lane's accumulators hold 4 consecutive columns of C's row r.
+//
+// Two forms:
+//  k_mx_tile  LDS tiles, for many rows: bound by the MFMA rate and its LDS feeding.
+//  k_mx_rows  up to 64 rows (single tokens and small batches): bound by streaming B once.
+#include <algorithm>
+#include <utility>
+
+#include "device_common.h"
+#include "launch.h"
+#include "lds_dma.h"
+#include "mok.h"
+
+namespace mok {
+namespace {
+
+constexpr int F8 = 0, F4 = 4;                     // the MFMA's operand format codes
+
+template <int F> constexpr int code_bytes(int n) { return F == F8 ? n : n / 2; }
+
+struct MxArgs {
+  const uint8_t *a, *as, *b, *bs;
+  void* c;                 // bf16 or float32 [M, N]; partial sums: float32 [splits, M, N]
+  int M, N, K;
+  int out_f32;
+  int tiles_m, tiles_n;
+  int splits;              // K ranges (grid z of k_mx_tile)
+  int steps_per_split;
+};
+
+template <int N, class F, int... I>
+MOK_DEV void static_for_(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F> MOK_DEV void static_for(F&& f) {
+  static_for_<N>(f, std::make_integer_sequence<int, N>{});
+}
+
+// A lane's operand of one MFMA: 16 bytes (E2M1) or 32 (E4M3).
+template <int F> struct Frag {
+  uint4 q[F == F8 ? 2 : 1];
+  MOK_DEV void zero() {
+    q[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (F == F8) q[1] = make_uint4(0, 0, 0, 0);
+  }
+  MOK_DEV i32x8_t regs() const {
+    i32x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
+    v[0] = q[0].x; v[1] = q[0].y; v[2] = q[0].z; v[3] = q[0].w;
+    if constexpr (F == F8) { v[4] = q[1].x; v[5] = q[1].y; v[6] = q[1].z; v[7] = q[1].w; }
+    return v;
+  }
+};
+
+template <int FA, int FB, int SEL>
+MOK_DEV f32x16_t mfma(const Frag<FB>& b, const Frag<FA>& a, f32x16_t acc, uint32_t bsc,
+                      uint32_t asc) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.regs(), a.regs(), acc, FB, FA, SEL,
+                                                         (int)bsc, SEL, (int)asc);
+}
+
+// A 4-byte word at any address.
+MOK_DEV uint32_t load_word(const uint8_t* p) {
+  uint32_t v;
+  __builtin_memcpy(&v, p, 4);
+  return v;
+}
+// The scales of blocks b0 .. b0 + 3 of a row of n blocks: past the row, the last one's (their
+// codes are taken as zero).
+MOK_DEV uint32_t scales_at(const uint8_t* row, int b0, int n) {
+  if (b0 + 4 <= n) return load_word(row + b0);
+  uint32_t v = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v |= (uint32_t)row[min(b0 + i, n - 1)] << (8 * i);
+  return v;
+}
+
+// 4 consecutive columns n .. n + 3 of row m of C.
+MOK_DEV void store4(const MxArgs& p, void* c, bool f32, int m, int n, float4 v) {
+  if (m >= p.M || n >= p.N) return;
+  const int64_t at = (int64_t)m * p.N + n;
+  if (p.N % 4 == 0) {
+    if (f32) *(float4*)((float*)c + at) = v;
+    else *(uint2*)((bf16_t*)c + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  } else {
+    const float q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < p.N) {
+        if (f32) ((float*)c)[at + i] = q[i];
+        else ((bf16_t*)c)[at + i] = f32_to_bf16(q[i]);
+      }
+  }
+}
+
+// ------------------------------------------------------------------------- few rows
+// A workgroup computes 32 columns (rows of B) x 32 MT rows; its KS waves take every KS-th step
+// of 256 along K, straight from memory into registers, and add their sums through LDS in wave
+// order. B is read once over the grid.
+constexpr int KS = 8;
+
+template <int FA, int FB, int MT>
+__global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
+  __shared__ float4 red[KS][MT][4][64];
+  const int lane = lane_id(), w = uniform(threadIdx.x >> 6), h = lane >> 5, r = lane & 31;
+  const int n0 = blockIdx.x * 32, m0 = blockIdx.y * 32 * MT;
+  const int KB = p.K / 32;
+  const int64_t rb = min(n0 + r, p.N - 1);
+  const uint8_t* b = p.b + rb * code_bytes<FB>(p.K);
+  const uint8_t* bs = p.bs + rb * KB;
+  const uint8_t *a[MT], *as[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t ra = min(m0 + 32 * i + r, p.M - 1);
+    a[i] = p.a + ra * code_bytes<FA>(p.K);
+    as[i] = p.as + ra * KB;
+  }
+  f32x16_t acc[MT] = {};
+  // this lane's part of the MFMA of blocks b0 + s and b0 + 4 + s
+  auto frag = [&](auto f, const uint8_t* row, int b0, int s) {
+    Frag<f()> v;
+    const int blk = b0 + 4 * h + s;
+    if constexpr (f() == F4) {
+      v.q[0] = *(const uint4*)(row + 16 * min(blk, KB - 1));
+      if (blk >= KB) v.zero();
+    } else {
+      const int x0 = b0 + s, x1 = b0 + 4 + s;
+      v.q[0] = *(const uint4*)(row + 32 * min(x0, KB - 1) + 16 * h);
+      v.q[1] = *(const uint4*)(row + 32 * min(x1, KB - 1) + 16 * h);
+      if (x0 >= KB) v.q[0] = make_uint4(0, 0, 0, 0);
+      if (x1 >= KB) v.q[1] = make_uint4(0, 0, 0, 0);
+    }
+    return v;
+  };
+  std::integral_constant<int, FA> fa;
+  std::integral_constant<int, FB> fb;
+  for (int b0 = 8 * w; b0 < KB; b0 += 8 * KS) {
+    Frag<FB> vb[4];
+    Frag<FA> va[MT][4];
+    uint32_t sb = scales_at(bs, b0 + 4 * h, KB), sa[MT];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) vb[s] = frag(fb, b, b0, s);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      sa[i] = scales_at(as[i], b0 + 4 * h, KB);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) va[i][s] = frag(fa, a[i], b0, s);
+    }
+    static_for<4>([&](auto s) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i] = mfma<FA, FB, s()>(vb[s()], va[i][s()], acc[i], sb, sa[i]);
+    });
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      red[w][i][q][lane] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2],
+                                       acc[i][4 * q + 3]);
+  __syncthreads();
+  for (int t = threadIdx.x; t < 256 * MT; t += 64 * KS) {
+    const int l = t & 63, q = (t >> 6) & 3, i = t >> 8;
+    float4 v = red[0][i][q][l];
+#pragma unroll
+    for (int k = 1; k < KS; ++k) {
+      const float4 x = red[k][i][q][l];
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    store4(p, p.c, p.out_f32, m0 + 32 * i + (l & 31), n0 + 8 * q + 4 * (l >> 5), v);
+  }
+}
+
+// ------------------------------------------------------------------------- LDS tiles
+// BM x BN tiles, 4 waves (2 x 2) of BM/2 x BN/2. K steps of KT values go to one of two LDS
+// buffers by LDS-DMA (16-byte chunks; chunk c of row r at slot c ^ swz(r), so that the 16 rows
+// that a quarter of a wave reads at one chunk hit distinct banks). A step's last sub-step follows
+// the barrier that publishes the next step's buffer: its MFMAs cover the next step's first LDS
+// reads, and the DMA of the step after that is issued among them.
+template <int FA_, int FB_, int BM_, int BN_>
+struct Tile {
+  static constexpr int FA = FA_, FB = FB_, BM = BM_, BN = BN_;
+  static constexpr int KT = FA == F4 && FB == F4 ? 256 : 128;
+  static constexpr int SUB = KT / 64;
+  static constexpr int FM = BM / 64, FN = BN / 64;
+  static constexpr int RBA = code_bytes<FA>(KT), RBB = code_bytes<FB>(KT);   // bytes of a row
+  static constexpr int QA = BM * RBA / 4096, QB = BN * RBB / 4096;   // DMA instructions a wave
+  static constexpr int LDS = 2 * (BM * RBA + BN * RBB);
+};
+
+template <int RB> MOK_DEV constexpr int swz(int r) {
+  return RB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
+
+template <class C>
+__global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
+  constexpr int FA = C::FA, FB = C::FB, FM = C::FM, FN = C::FN, SUB = C::SUB, KT = C::KT;
+  __shared__ uint4 lds_a[2][C::BM * C::RBA / 16], lds_b[2][C::BN * C::RBB / 16];
+  const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
+  const int wm = wid >> 1, wn = wid & 1, h = lane >> 5, r = lane & 31;
+  // XCD x takes consecutive tiles, 8 M tiles deep, so that its L2 holds their operands
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int per = (tiles + 7) / 8;
+  const int tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (tile >= tiles || (int)(blockIdx.x >> 3) >= per) return;
+  const int band = tile / (8 * p.tiles_n), in = tile % (8 * p.tiles_n);
+  const int bh = min(8, p.tiles_m - 8 * band);
+  const int m0 = (8 * band + in % bh) * C::BM, n0 = in / bh * C::BN;
+  const int KB = p.K / 32;
+  const int step0 = blockIdx.z * p.steps_per_split;
+  const int nk = min(p.steps_per_split, (p.K + KT - 1) / KT - step0);
+  const int64_t lda = code_bytes<FA>(p.K), ldb = code_bytes<FB>(p.K);
+
+  // DMA instruction q of this wave: rows (q, wave) of an operand tile
+  auto dma = [&](auto RB_, auto Q_, const uint8_t* base, int64_t ld, int row0, int rows, int kt,
+                 int q, const uint4* buf) {
+    constexpr int RB = RB_(), Q = Q_(), CH = RB / 16, RPI = 64 / CH;
+    const int row = (wid * Q + q) * RPI + lane / CH;
+    const int rr = min(row0 + row, rows - 1) - row0;        // rows past the operand: its last
+    int byte = kt * RB + ((lane % CH) ^ swz<RB>(row)) * 16;
+    byte = min(byte, (int)ld - 16);                         // chunks past K: the row's last
+    dma_b128(uniform_ptr(base + row0 * ld), (uint32_t)(rr * ld + byte),
+             uniform(lds_addr(buf)) + (wid * Q + q) * 1024);
+  };
+  auto issue = [&](int kt, int q) {
+    __builtin_amdgcn_sched_barrier(0);
+    const int buf = kt & 1, g = step0 + kt;
+    if (q < C::QA)
+      dma(std::integral_constant<int, C::RBA>{}, std::integral_constant<int, C::QA>{}, p.a, lda, m0,
+          p.M, g, q, lds_a[buf]);
+    else
+      dma(std::integral_constant<int, C::RBB>{}, std::integral_constant<int, C::QB>{}, p.b, ldb, n0,
+          p.N, g, q - C::QA, lds_b[buf]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // scale words of step kt of this lane's rows: KT 256: byte s is sub-step s's; KT 128: byte 2 s
+  const uint8_t *as[FM], *bs[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+    as[i] = p.as + (int64_t)min(m0 + wm * (C::BM / 2) + 32 * i + r, p.M - 1) * KB;
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    bs[j] = p.bs + (int64_t)min(n0 + wn * (C::BN / 2) + 32 * j + r, p.N - 1) * KB;
+  auto scale = [&](const uint8_t* row, int kt) {
+    const int b0 = (step0 + kt) * (KT / 32);
+    if constexpr (KT == 256) return scales_at(row, b0 + 4 * h, KB);
+    else return scales_at(row, b0, KB) >> (8 * h);
+  };
+  uint32_t asc[FM], bsc[FN], asc_n[FM], bsc_n[FN];
+  auto load_scales = [&](int kt) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) asc_n[i] = scale(as[i], kt);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bsc_n[j] = scale(bs[j], kt);
+  };
+  Frag<FA> fa[2][FM];
+  Frag<FB> fb[2][FN];
+  // block pairs of sub-step s: (s, 4 + s) of 8 blocks (KT 256) or (2 s, 2 s + 1) of 4 (KT 128)
+  auto blk = [](int s, int x) { return KT == 256 ? 4 * x + s : 2 * s + x; };
+  auto read = [&](auto f, auto RB_, const uint4* buf, int row, int kt, int s) {
+    constexpr int RB = RB_(), CH = RB / 16;
+    Frag<f()> v;
+    const uint4* base = buf + row * CH;
+    const int left = KB - (step0 + kt) * (KT / 32);         // blocks from this step on
+    if constexpr (f() == F4) {
+      v.q[0] = base[blk(s, h) ^ swz<RB>(row)];
+      if (left < KT / 32 && blk(s, h) >= left) v.zero();
+    } else {
+      v.q[0] = base[(2 * blk(s, 0) + h) ^ swz<RB>(row)];
+      v.q[1] = base[(2 * blk(s, 1) + h) ^ swz<RB>(row)];
+      if (left < KT / 32) {
+        if (blk(s, 0) >= left) v.q[0] = make_uint4(0, 0, 0, 0);
+        if (blk(s, 1) >= left) v.q[1] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    return v;
+  };
+  auto frags = [&](int kt, int s, int f) {
+    const uint4 *A = lds_a[kt & 1], *B = lds_b[kt & 1];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      fb[f][j] = read(std::integral_constant<int, FB>{}, std::integral_constant<int, C::RBB>{}, B,
+                      wn * (C::BN / 2) + 32 * j + r, kt, s);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      fa[f][i] = read(std::integral_constant<int, FA>{}, std::integral_constant<int, C::RBA>{}, A,
+                      wm * (C::BM / 2) + 32 * i + r, kt, s);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  f32x16_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  constexpr int NQ = C::QA + C::QB, NM = FM * FN;
+  auto mfmas = [&](auto s, auto&& after) {
+    constexpr int SEL = KT == 256 ? s() : 2 * s(), F = s() & 1;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        acc[i][j] = mfma<FA, FB, SEL>(fb[F][j], fa[F][i], acc[i][j], bsc[j], asc[i]);
+        after(i * FN + j);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) asc[i] = asc_n[i];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bsc[j] = bsc_n[j];
+  };
+  // every wave's DMA and scales issued so far have landed and its LDS reads are back
+  auto publish = [&]() {
+    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+    lds_barrier();
+  };
+
+  for (int q = 0; q < NQ; ++q) issue(0, q);
+  load_scales(0);
+  publish();
+  take_scales();
+  if (nk > 1) {
+    for (int q = 0; q < NQ; ++q) issue(1, q);
+    load_scales(1);
+  }
+  frags(0, 0, 0);
+  for (int kt = 0; kt < nk; ++kt) {
+    static_for<SUB - 1>([&](auto s) {
+      mfmas(s, [&](int n) {
+        if (n == NM / 2 - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          frags(kt, s() + 1, (s() + 1) & 1);
+        }
+      });
+    });
+    publish();                          // step kt + 1 has landed; all reads of kt are back
+    const bool more = kt + 1 < nk, dma_more = kt + 2 < nk;
+    mfmas(std::integral_constant<int, SUB - 1>{}, [&](int n) {
+      if (n == NM / 2 - 1 && more) {
+        __builtin_amdgcn_sched_barrier(0);
+        frags(kt + 1, 0, 0);
+      }
+      if (dma_more) {
+#pragma unroll
+        for (int q = n * NQ / NM; q < (n + 1) * NQ / NM; ++q) issue(kt + 2, q);
+      }
+    });
+    if (more) take_scales();
+    if (dma_more) load_scales(kt + 2);
+  }
+  void* c = p.c;
+  bool f32 = p.out_f32;
+  if (p.splits > 1) {
+    c = (float*)p.c + (int64_t)blockIdx.z * p.M * p.N;
+    f32 = true;
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        store4(p, c, f32, m0 + wm * (C::BM / 2) + 32 * i + r,
+               n0 + wn * (C::BN / 2) + 32 * j + 8 * q + 4 * h,
+               make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                           acc[i][j][4 * q + 3]));
+}
+
+// C = the K ranges' partial sums in ascending order.
+__global__ __launch_bounds__(256) void k_mx_join(const float* __restrict__ part, int splits,
+                                                 int64_t elems, int f32, void* c) {
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < elems;
+       i += (int64_t)gridDim.x * 256) {
+    float v = 0.0f;
+#pragma unroll 4
+    for (int q = 0; q < splits; ++q) v += part[q * elems + i];
+    if (f32) ((float*)c)[i] = v;
+    else ((bf16_t*)c)[i] = f32_to_bf16(v);
+  }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int kRowsMax = 64;      // rows up to which k_mx_rows streams B
+
+// The tiling of a product, from its sizes alone.
+struct Plan {
+  bool rows;               // k_mx_rows
+  int tile;                // 256 or 128
+  int splits;
+};
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  Plan t;
+  t.rows = M <= kRowsMax;
+  t.tile = cdiv(M, 256) * cdiv(N, 256) >= 192 ? 256 : 128;
+  const int64_t tiles = cdiv(M, t.tile) * cdiv(N, t.tile), steps = cdiv(K, 256);
+  t.splits = t.rows || tiles >= 128 ? 1
+                                    : (int)std::max<int64_t>(1, std::min(256 / tiles, steps / 4));
+  return t;
+}
+
+template <int FA, int FB>
+hipError_t run_mx(MxArgs p, const Plan& t, float* part, void* c, hipStream_t s) {
+  if (t.rows) {
+    p.c = c;
+    const dim3 grid((unsigned)cdiv(p.N, 32), 1);
+    if (p.M <= 32)
+      launch_k(k_mx_rows<FA, FB, 1>, grid, dim3(64 * KS), 0, s, nullptr, nullptr, p);
+    else
+      launch_k(k_mx_rows<FA, FB, 2>, grid, dim3(64 * KS), 0, s, nullptr, nullptr, p);
+    return hipGetLastError();
+  }
+  p.tiles_m = (int)cdiv(p.M, t.tile);
+  p.tiles_n = (int)cdiv(p.N, t.tile);
+  constexpr int KT = Tile<FA, FB, 128, 128>::KT;
+  const int64_t steps = cdiv(p.K, KT);
+  p.steps_per_split = (int)cdiv(steps, t.splits);
+  p.splits = (int)cdiv(steps, p.steps_per_split);       // every range has a step
+  p.c = p.splits > 1 ? part : c;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  const dim3 grid((unsigned)(8 * cdiv(tiles, 8)), 1, p.splits);
+  if (t.tile == 256)
+    launch_k(k_mx_tile<Tile<FA, FB, 256, 256>>, grid, dim3(256), 0, s, nullptr, nullptr, p);
+  else
+    launch_k(k_mx_tile<Tile<FA, FB, 128, 128>>, grid, dim3(256), 0, s, nullptr, nullptr, p);
+  if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+  if (p.splits > 1) {
+    const int64_t elems = (int64_t)p.M * p.N;
+    launch_k(k_mx_join, dim3((unsigned)std::min<int64_t>(cdiv(elems, 256), 8192)), dim3(256), 0, s,
+             nullptr, nullptr, (const float*)part, p.splits, elems, p.out_f32, c);
+  }
+  return hipGetLastError();
+}
+
+int mx_check(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 32 || K % 32 || K > (1 << 22)) return MOK_EINVAL;
+  if (M >= (int64_t)1 << 31 || N >= (int64_t)1 << 31) return MOK_EINVAL;
+  return MOK_OK;
+}
+
+}  // namespace
+}  // namespace mok
+
+using namespace mok;
+
+extern "C" {
+
+int mok_mx_gemm_workspace_bytes(int64_t M, int64_t N, int32_t K, size_t* bytes) {
+  if (!bytes || mx_check(M, N, K) != MOK_OK) return MOK_EINVAL;
+  *bytes = 0;
+  if (M == 0 || N == 0) return MOK_OK;
+  const Plan t = plan_of(M, N, K);
+  if (t.splits > 1) *bytes = (size_t)t.splits * M * N * sizeof(float);
+  return MOK_OK;
+}
+
+int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype,
+                const uint8_t* b_codes, const uint8_t* b_scales, int32_t b_dtype, int64_t M,
+                int64_t N, int32_t K, int32_t out_dtype, void* c, void* ws, size_t ws_bytes,
+                void* stream) {
+  const int st = mx_check(M, N, K);
+  if (st != MOK_OK) return st;
+  if ((a_dtype != MOK_MXFP8 && a_dtype != MOK_MXFP4) || (b_dtype != MOK_MXFP8 && b_dtype != MOK_MXFP4))
+    return MOK_EINVAL;
+  if (out_dtype != MOK_FP32 && out_dtype != MOK_BF16) return MOK_EINVAL;
+  if (M == 0 || N == 0) return MOK_OK;
+  if (!a_codes || !a_scales || !b_codes || !b_scales || !c) return MOK_EINVAL;
+  if ((uintptr_t)a_codes % 16 || (uintptr_t)b_codes % 16 || (uintptr_t)c % 16) return MOK_EINVAL;
+  const Plan t = plan_of(M, N, K);
+  // a launch counts its threads in 32 bits
+  if (cdiv(M, t.tile) * cdiv(N, t.tile) >= (int64_t)1 << 23) return MOK_EUNSUPPORTED;
+  size_t need = 0;
+  mok_mx_gemm_workspace_bytes(M, N, K, &need);
+  if (need && (!ws || ws_bytes < need || (uintptr_t)ws % 16)) return MOK_EWORKSPACE;
+  MxArgs p = {};
+  p.a = a_codes; p.as = a_scales; p.b = b_codes; p.bs = b_scales;
+  p.M = (int)M; p.N = (int)N; p.K = K;
+  p.out_f32 = out_dtype == MOK_FP32;
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e;
+  if (a_dtype == MOK_MXFP4 && b_dtype == MOK_MXFP4) e = run_mx<F4, F4>(p, t, (float*)ws, c, s);
+  else if (a_dtype == MOK_MXFP8 && b_dtype == MOK_MXFP4) e = run_mx<F8, F4>(p, t, (float*)ws, c, s);
+  else if (a_dtype == MOK_MXFP4) e = run_mx<F4, F8>(p, t, (float*)ws, c, s);
+  else e = run_mx<F8, F8>(p, t, (float*)ws, c, s);
+  return e == hipSuccess ? MOK_OK : MOK_EHIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,468 @@
+// Residual addition + root-mean-square norm, with an output in the storage type, in MXFP8, or
+// both, and the norm's backward.
+//
+//   h = x + residual (rounded to the storage type: the residual stream)
+//   rstd[t] = 1 / sqrt(mean_i h[t,i]^2 + eps)          y[t,i] = h[t,i] rstd[t] weight[i]
+//   backward, g = dy weight, n = h rstd:
+//   dx[t,i] = rstd (g[t,i] - n[t,i] mean_j(g[t,j] n[t,j])) + dh[t,i]
+//   dweight[i] = sum_t dy[t,i] n[t,i]
+//
+// The norm reads h as it is stored, so the backward, which is given the stored h, differentiates
+// exactly the function that the forward computed. Everything between the loads and the stores is
+// float32; each output is rounded once. MXFP8 codes come from the float32 y (not from a rounded
+// one), by the rules of mok_quantize_mxfp8_f32.
+//
+// HBM streams: a row stays in registers between its sum of squares and its output, so each input
+// is read once and each output written once. TPR threads hold a row in NC pieces of 8 values.
+#include <algorithm>
+
+#include "device_common.h"
+#include "launch.h"
+#include "mok.h"
+
+namespace mok {
+namespace {
+
+constexpr int NORM_NT = 256;
+
+template <class T> struct Piece;             // 8 consecutive values
+template <> struct Piece<bf16_t> {
+  MOK_DEV static void load(const bf16_t* p, float (&v)[8]) {
+    const uint4 q = *(const uint4*)p;
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  MOK_DEV static void store(bf16_t* p, const float (&v)[8]) {
+    *(uint4*)p = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+};
+template <> struct Piece<float> {
+  MOK_DEV static void load(const float* p, float (&v)[8]) {
+    const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  MOK_DEV static void store(float* p, const float (&v)[8]) {
+    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+
+template <class T> MOK_DEV float as_stored(float v);     // v rounded to the storage type
+template <> MOK_DEV float as_stored<float>(float v) { return v; }
+template <> MOK_DEV float as_stored<bf16_t>(float v) { return bf16_to_f32(f32_to_bf16(v)); }
+
+// Sum over the row's TPR threads, the same value in each (xor order within a wave, then the
+// waves in ascending order). slot: LDS words of this call, one per wave; two calls in a row use
+// two slots, so one barrier each is enough.
+template <int TPR>
+MOK_DEV float row_total(float v, float* slot) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, kWave);
+  if constexpr (TPR > 64) {
+    if (lane_id() == 0) slot[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = slot[0];
+#pragma unroll
+    for (int w = 1; w < TPR / 64; ++w) v += slot[w];
+  }
+  return v;
+}
+
+// The 8 E4M3 codes of a lane's piece and its 32-value block's scale byte (the aligned quad of
+// lanes holds the block). A block with an infinity or a NaN is NaN: code 0x7F, scale 0xFF.
+MOK_DEV uint2 mx8_codes(const float (&v)[8], uint8_t* scale) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bad |= !(fabsf(v[i]) < INFINITY);
+  int b = bad;
+  b |= __shfl_xor(b, 1, kWave);
+  b |= __shfl_xor(b, 2, kWave);
+  int s;
+  uint2 c = quantize_quad8_f32(v, &s);
+  if (b) {
+    c = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    s = 128;
+  }
+  *scale = (uint8_t)(s + 127);
+  return c;
+}
+
+// A workgroup of max(TPR, 256) threads holds 256 / TPR rows (at least one). res, h_out, rstd, y,
+// codes (with scales): NULL where not wanted.
+template <class T, int TPR, int NC>
+__global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm(
+    const T* x, const T* res, const T* __restrict__ weight, int64_t rows, int d, float eps,
+    T* h_out, float* __restrict__ rstd_out, T* y, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+  constexpr int NT = TPR > NORM_NT ? TPR : NORM_NT, RPB = NT / TPR;
+  __shared__ float sh[NT / 64];
+  const int l = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const bool live = row < rows;
+  const int64_t at = row * d;
+  float h[NC][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int n = 0; n < NC; ++n) {
+    const int c = (n * TPR + l) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[n][i] = 0.0f;
+    if (live && c < d) {
+      Piece<T>::load(x + at + c, h[n]);
+      if (res) {
+        float r[8];
+        Piece<T>::load(res + at + c, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[n][i] = as_stored<T>(h[n][i] + r[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NC; ++n) {
+    const int c = (n * TPR + l) * 8;
+    if (h_out && live && c < d) Piece<T>::store(h_out + at + c, h[n]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += h[n][i] * h[n][i];
+  }
+  ss = row_total<TPR>(ss, sh);
+  const float rstd = 1.0f / sqrtf(ss / (float)d + eps);
+  if (rstd_out && live && l == 0) rstd_out[row] = rstd;
+#pragma unroll
+  for (int n = 0; n < NC; ++n) {
+    const int c = (n * TPR + l) * 8;
+    const bool ok = live && c < d;
+    float w[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8];
+    if (ok) Piece<T>::load(weight + c, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = h[n][i] * rstd * w[i];
+    if (y && ok) Piece<T>::store(y + at + c, v);
+    if (codes) {                   // d % 32 == 0: a quad's four lanes are all inside the row
+      uint8_t s;
+      const uint2 q = mx8_codes(v, &s);
+      if (ok) {
+        *(uint2*)(codes + at + c) = q;
+        if ((l & 3) == 0) scales[(at + c) >> 5] = s;
+      }
+    }
+  }
+}
+
+// Any d and alignment: one workgroup a row, one value a thread and step (one 32-value block a
+// thread for the codes). The second pass reads back what the first stored in h_out.
+template <class T>
+__global__ __launch_bounds__(NORM_NT) void k_rmsnorm_any(
+    const T* x, const T* res, const T* weight, int64_t rows, int d, float eps, T* h_out,
+    float* rstd_out, T* y, uint8_t* codes, uint8_t* scales) {
+  __shared__ float sh[NORM_NT / 64];
+  const int64_t row = blockIdx.x, at = row * d;
+  auto sum_at = [&](int i) {
+    const float v = load_as_f32(x + at + i);
+    return res ? as_stored<T>(v + load_as_f32(res + at + i)) : v;
+  };
+  float ss = 0.0f;
+  for (int i = threadIdx.x; i < d; i += NORM_NT) {
+    const float v = sum_at(i);
+    if (h_out) h_out[at + i] = f32_to<T>(v);
+    ss += v * v;
+  }
+  ss = row_total<NORM_NT>(ss, sh);
+  __syncthreads();                 // the row's h is written: other threads read it below
+  const float rstd = 1.0f / sqrtf(ss / (float)d + eps);
+  if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
+  auto y_at = [&](int i) {
+    const float v = h_out ? load_as_f32(h_out + at + i) : sum_at(i);
+    return v * rstd * load_as_f32(weight + i);
+  };
+  if (codes) {
+    for (int b = threadIdx.x; b < d / 32; b += NORM_NT) {
+      float amax = 0.0f;
+      bool bad = false;
+      for (int i = 0; i < 32; ++i) {
+        const float v = fabsf(y_at(32 * b + i));
+        bad |= !(v < INFINITY);
+        amax = fmaxf(amax, v);
+      }
+      const int s = mx_shared_exp(amax);
+      for (int i = 0; i < 32; ++i)
+        codes[at + 32 * b + i] = bad ? 0x7F : (uint8_t)e4m3_encode(y_at(32 * b + i), s);
+      scales[(at >> 5) + b] = bad ? 0xFF : (uint8_t)(s + 127);
+    }
+    __syncthreads();               // y may be x: its first write follows the codes' last read
+  }
+  if (y)
+    for (int i = threadIdx.x; i < d; i += NORM_NT) y[at + i] = f32_to<T>(y_at(i));
+}
+
+// Backward over rows blockIdx.x * RPB + ..., stepping by the whole grid: dweight's sums stay in
+// registers from row to row. part [gridDim.x, d]: this workgroup's share of dweight (NULL: none).
+template <class T, int TPR, int NC>
+__global__ __launch_bounds__(NORM_NT) void k_rmsnorm_bwd(
+    const T* dy, const T* __restrict__ h, const float* __restrict__ rstd,
+    const T* __restrict__ weight, const T* dh, int64_t rows, int d, T* dx,
+    float* __restrict__ part) {
+  constexpr int RPB = NORM_NT / TPR;
+  __shared__ float sh[2][NORM_NT / 64];
+  __shared__ float fold[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NC * 8 : 1];
+  const int l = threadIdx.x % TPR, r = threadIdx.x / TPR;
+  float w[NC][8], acc[NC][8];
+#pragma unroll
+  for (int n = 0; n < NC; ++n) {
+    const int c = (n * TPR + l) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[n][i] = acc[n][i] = 0.0f;
+    if (c < d) Piece<T>::load(weight + c, w[n]);
+  }
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = r0 + r, at = row * d;
+    const bool live = row < rows;
+    const float rs = live ? rstd[row] : 0.0f;
+    float n_[NC][8], g[NC][8], dot = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      const int c = (n * TPR + l) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n_[n][i] = g[n][i] = 0.0f;
+      if (live && c < d) {
+        Piece<T>::load(h + at + c, n_[n]);
+        Piece<T>::load(dy + at + c, g[n]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n_[n][i] *= rs;
+        acc[n][i] += g[n][i] * n_[n][i];
+        g[n][i] *= w[n][i];
+        dot += g[n][i] * n_[n][i];
+      }
+    dot = row_total<TPR>(dot, sh[turn]) / (float)d;
+    turn ^= 1;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      const int c = (n * TPR + l) * 8;
+      if (live && c < d) {
+        float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (dh) Piece<T>::load(dh + at + c, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += rs * (g[n][i] - n_[n][i] * dot);
+        Piece<T>::store(dx + at + c, o);
+      }
+    }
+  }
+  if (!part) return;
+  float* out = part + (int64_t)blockIdx.x * d;
+  if constexpr (RPB == 1) {
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      const int c = (n * TPR + l) * 8;
+      if (c < d) Piece<float>::store(out + c, acc[n]);
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < NC; ++n) Piece<float>::store(&fold[r][(n * TPR + l) * 8], acc[n]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += NORM_NT) {
+      float v = fold[0][c];
+#pragma unroll
+      for (int q = 1; q < RPB; ++q) v += fold[q][c];
+      out[c] = v;
+    }
+  }
+}
+
+// Any d and alignment, first launch: workgroup (x, y) sums dweight's columns 256 x .. over the
+// rows y, y + gridDim.y, ... It runs before dx is written, which may lie where dy does.
+template <class T>
+__global__ __launch_bounds__(NORM_NT) void k_rmsnorm_dw_any(const T* dy, const T* h,
+                                                            const float* rstd, int64_t rows, int d,
+                                                            float* part) {
+  const int c = blockIdx.x * NORM_NT + threadIdx.x;
+  if (c >= d) return;
+  float v = 0.0f;
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y)
+    v += load_as_f32(dy + row * d + c) * (load_as_f32(h + row * d + c) * rstd[row]);
+  part[(int64_t)blockIdx.y * d + c] = v;
+}
+
+template <class T>
+__global__ __launch_bounds__(NORM_NT) void k_rmsnorm_bwd_any(const T* dy, const T* h,
+                                                             const float* rstd, const T* weight,
+                                                             const T* dh, int d, T* dx) {
+  __shared__ float sh[NORM_NT / 64];
+  const int64_t row = blockIdx.x, at = row * d;
+  const float rs = rstd[row];
+  float dot = 0.0f;
+  for (int i = threadIdx.x; i < d; i += NORM_NT)
+    dot += load_as_f32(dy + at + i) * load_as_f32(weight + i) * (load_as_f32(h + at + i) * rs);
+  dot = row_total<NORM_NT>(dot, sh) / (float)d;
+  for (int i = threadIdx.x; i < d; i += NORM_NT) {
+    const float g = load_as_f32(dy + at + i) * load_as_f32(weight + i);
+    const float o = rs * (g - load_as_f32(h + at + i) * rs * dot);
+    dx[at + i] = f32_to<T>(o + (dh ? load_as_f32(dh + at + i) : 0.0f));
+  }
+}
+
+// out[c] = sum of part[0 .. n)[c] : 16 waves a workgroup over 64 columns, each its rows in
+// ascending order, then the waves in ascending order. n == 0 writes zeros.
+__global__ __launch_bounds__(1024) void k_column_sum(const float* __restrict__ part, int n, int d,
+                                                     float* __restrict__ out) {
+  __shared__ float sh[16][64];
+  const int lane = lane_id(), g = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  float v = 0.0f;
+  if (c < d)
+    for (int i = g; i < n; i += 16) v += part[(int64_t)i * d + c];
+  sh[g][lane] = v;
+  __syncthreads();
+  if (g == 0 && c < d) {
+#pragma unroll
+    for (int q = 1; q < 16; ++q) v += sh[q][lane];
+    out[c] = v;
+  }
+}
+
+// Workgroups of the backward that keep a share of dweight each.
+int bwd_blocks(int64_t rows) { return (int)std::max<int64_t>(1, std::min<int64_t>(rows, 512)); }
+
+// Rows of one launch that takes a workgroup a row: a launch counts its threads in 32 bits.
+constexpr int64_t kMaxLaunchRows = (int64_t)1 << 21;
+
+bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+template <class T>
+hipError_t run_norm(const T* x, const T* res, const T* weight, int64_t rows, int d, float eps,
+                    T* h, float* rstd, T* y, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  const bool vec = d % 8 == 0 && d <= 16384 && al16(x) && al16(res) && al16(weight) && al16(h) &&
+                   al16(y) && (uintptr_t)codes % 8 == 0;
+  if (rows > kMaxLaunchRows) {
+    const int64_t n = kMaxLaunchRows, o = n * d;
+    const hipError_t e = run_norm(x, res, weight, n, d, eps, h, rstd, y, codes, scales, s);
+    if (e != hipSuccess) return e;
+    auto skip = [](auto* p, int64_t k) { return p ? p + k : p; };
+    return run_norm(x + o, skip(res, o), weight, rows - n, d, eps, skip(h, o), skip(rstd, n),
+                    skip(y, o), skip(codes, o), skip(scales, o / 32), s);
+  }
+  auto go = [&](auto TPR, auto NC) {
+    constexpr int nt = TPR() > NORM_NT ? TPR() : NORM_NT, rpb = nt / TPR();
+    launch_k(k_rmsnorm<T, TPR(), NC()>, dim3((unsigned)((rows + rpb - 1) / rpb)), dim3(nt), 0, s,
+             nullptr, nullptr, x, res, weight, rows, d, eps, h, rstd, y, codes, scales);
+  };
+  auto c = [](auto v) { return v; };
+#define MOK_NORM(TPR, NC) go(c(std::integral_constant<int, TPR>{}), c(std::integral_constant<int, NC>{}))
+  if (!vec)
+    launch_k(k_rmsnorm_any<T>, dim3((unsigned)rows), dim3(NORM_NT), 0, s, nullptr, nullptr, x, res,
+             weight, rows, d, eps, h, rstd, y, codes, scales);
+  else if (d <= 512) MOK_NORM(64, 1);
+  else if (d <= 1024) MOK_NORM(64, 2);
+  else if (d <= 2048) MOK_NORM(64, 4);
+  else if (d <= 4096) MOK_NORM(256, 2);
+  else if (d <= 8192) MOK_NORM(256, 4);
+  else MOK_NORM(1024, 2);
+#undef MOK_NORM
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t run_bwd(const T* dy, const T* h, const float* rstd, const T* weight, const T* dh,
+                   int64_t rows, int d, T* dx, float* dweight, float* part, hipStream_t s) {
+  const int blocks = bwd_blocks(rows);
+  const bool vec = d % 8 == 0 && d <= 8192 && al16(dy) && al16(h) && al16(weight) && al16(dh) &&
+                   al16(dx);
+  float* p = dweight ? part : nullptr;
+  int n_part = rows > 0 ? blocks : 0;
+  auto go = [&](auto TPR, auto NC) {
+    constexpr int rpb = NORM_NT / TPR();
+    const int grid = (int)std::min<int64_t>(dweight ? blocks : 1 << 16, (rows + rpb - 1) / rpb);
+    n_part = grid;
+    launch_k(k_rmsnorm_bwd<T, TPR(), NC()>, dim3(grid), dim3(NORM_NT), 0, s, nullptr, nullptr, dy,
+             h, rstd, weight, dh, rows, d, dx, p);
+  };
+  auto c = [](auto v) { return v; };
+#define MOK_NORM(TPR, NC) go(c(std::integral_constant<int, TPR>{}), c(std::integral_constant<int, NC>{}))
+  if (rows == 0) {
+  } else if (!vec) {
+    if (p)
+      launch_k(k_rmsnorm_dw_any<T>, dim3((d + NORM_NT - 1) / NORM_NT, blocks), dim3(NORM_NT), 0, s,
+               nullptr, nullptr, dy, h, rstd, rows, d, p);
+    for (int64_t r = 0; r < rows; r += kMaxLaunchRows) {
+      const int64_t n = std::min(rows - r, kMaxLaunchRows), o = r * d;
+      launch_k(k_rmsnorm_bwd_any<T>, dim3((unsigned)n), dim3(NORM_NT), 0, s, nullptr, nullptr,
+               dy + o, h + o, rstd + r, weight, dh ? dh + o : dh, d, dx + o);
+    }
+  } else if (d <= 512) MOK_NORM(64, 1);
+  else if (d <= 1024) MOK_NORM(64, 2);
+  else if (d <= 2048) MOK_NORM(64, 4);
+  else if (d <= 4096) MOK_NORM(256, 2);
+  else MOK_NORM(256, 4);
+#undef MOK_NORM
+  if (dweight)
+    launch_k(k_column_sum, dim3((d + 63) / 64), dim3(1024), 0, s, nullptr, nullptr,
+             (const float*)part, n_part, d, dweight);
+  return hipGetLastError();
+}
+
+int norm_check(int64_t rows, int32_t d, int32_t io_dtype) {
+  if (rows < 0 || rows >= (int64_t)1 << 31 || d < 1 || d > (1 << 24)) return MOK_EINVAL;
+  return io_dtype == MOK_FP32 || io_dtype == MOK_BF16 ? MOK_OK : MOK_EINVAL;
+}
+
+}  // namespace
+}  // namespace mok
+
+using namespace mok;
+
+extern "C" {
+
+int mok_rmsnorm(const void* x, const void* residual, const void* weight, int64_t rows, int32_t d,
+                int32_t io_dtype, float eps, void* h, float* rstd, void* y, uint8_t* codes,
+                uint8_t* scales, void* stream) {
+  const int st = norm_check(rows, d, io_dtype);
+  if (st != MOK_OK) return st;
+  if (!(eps >= 0.0f) || (codes != nullptr) != (scales != nullptr) || (codes && d % 32))
+    return MOK_EINVAL;
+  if (rows == 0) return MOK_OK;
+  if (!x || !weight || (!h && !rstd && !y && !codes)) return MOK_EINVAL;
+  hipStream_t s = (hipStream_t)stream;
+  const hipError_t e =
+      io_dtype == MOK_BF16
+          ? run_norm((const bf16_t*)x, (const bf16_t*)residual, (const bf16_t*)weight, rows, d, eps,
+                     (bf16_t*)h, rstd, (bf16_t*)y, codes, scales, s)
+          : run_norm((const float*)x, (const float*)residual, (const float*)weight, rows, d, eps,
+                     (float*)h, rstd, (float*)y, codes, scales, s);
+  return e == hipSuccess ? MOK_OK : MOK_EHIP;
+}
+
+int mok_rmsnorm_backward_workspace_bytes(int64_t rows, int32_t d, size_t* bytes) {
+  if (!bytes || norm_check(rows, d, MOK_FP32) != MOK_OK) return MOK_EINVAL;
+  *bytes = (size_t)bwd_blocks(rows) * d * sizeof(float);
+  return MOK_OK;
+}
+
+int mok_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const void* weight,
+                         const void* dh, int64_t rows, int32_t d, int32_t io_dtype, void* dx,
+                         float* dweight, void* ws, size_t ws_bytes, void* stream) {
+  const int st = norm_check(rows, d, io_dtype);
+  if (st != MOK_OK) return st;
+  if (rows > 0 && (!dy || !h || !rstd || !weight || !dx)) return MOK_EINVAL;
+  if (rows == 0 && !dweight) return MOK_OK;
+  size_t need = 0;
+  mok_rmsnorm_backward_workspace_bytes(rows, d, &need);
+  if (dweight && (!ws || ws_bytes < need || (uintptr_t)ws % 16)) return MOK_EWORKSPACE;
+  hipStream_t s = (hipStream_t)stream;
+  const hipError_t e =
+      io_dtype == MOK_BF16
+          ? run_bwd((const bf16_t*)dy, (const bf16_t*)h, rstd, (const bf16_t*)weight,
+                    (const bf16_t*)dh, rows, d, (bf16_t*)dx, dweight, (float*)ws, s)
+          : run_bwd((const float*)dy, (const float*)h, rstd, (const float*)weight, (const float*)dh,
+                    rows, d, (float*)dx, dweight, (float*)ws, s);
+  return e == hipSuccess ? MOK_OK : MOK_EHIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,167 @@
+"""Microscaled product (mok_mx_gemm) of quantised operands.
+
+Exact cases: both operands hold the E2M1 grid (multiples of 1/2 up to 6) under scales 2^-1, 1 or 2,
+so every product is a multiple of 1/16 of at most 144 and every sum of up to 7168 of them is below
+2^20: exact in float32 in any order, and the result has to be equal. General cases: sums in float32
+in any order, at most K roundings or truncations: K 2^-23 sum |a b|."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+GRID = np.array([0, .5, 1, 1.5, 2, 3, 4, 6])
+
+
+def pack4(nib):
+    return (nib[:, 0::2] | (nib[:, 1::2] << 4)).astype(np.uint8)
+
+
+def operand(rng, rows, K, fmt, scales=(126, 129)):
+    """(codes, scales, float64 values) on the E2M1 grid."""
+    nib = rng.integers(0, 16, (rows, K)).astype(np.uint8)
+    val = np.where(nib & 8, -1.0, 1.0) * GRID[nib & 7]
+    sc = rng.integers(*scales, (rows, K // 32)).astype(np.uint8)
+    if fmt == 4:
+        codes = pack4(nib)
+    else:
+        codes = torch.from_numpy(val).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    val = val.reshape(rows, -1, 32) * (2.0 ** (sc.astype(np.float64) - 127))[:, :, None]
+    return codes, sc, val.reshape(rows, K)
+
+
+def gemm(mok, a, asc, b, bsc, dtype=torch.float32, behind=0):
+    M, N, K = a.shape[0], b.shape[0], 32 * asc.shape[1]
+    t = [torch.from_numpy(np.ascontiguousarray(v)).to(DEV) for v in (a, asc, b, bsc)]
+    full = torch.full((M + behind, N), 7.0, dtype=dtype, device=DEV)
+    n = mok.mok_mx_gemm_workspace_bytes(M, N, K)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) if n else None
+    mok.mok_mx_gemm(*t, full[:M], ws)
+    torch.cuda.synchronize()
+    assert (full[M:] == 7.0).all()
+    return full[:M].cpu()
+
+
+SIZES = [(1, 1, 32), (1, 32, 64), (1, 7168, 2048), (3, 33, 96), (17, 100, 256), (32, 64, 288),
+         (33, 129, 512), (64, 31, 2080), (5, 16, 7168), (65, 65, 32), (100, 130, 64), (65, 257, 4128),
+         (128, 128, 256), (129, 127, 320), (200, 333, 1056), (100, 128, 7168), (130, 260, 2592),
+         (1000, 514, 736)]
+FMT = [(4, 4), (8, 4), (4, 8), (8, 8)]
+
+
+@pytest.mark.parametrize("fa,fb", FMT)
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_exact(M, N, K, fa, fb):
+    import routing_grouped_expert_gemm_amd as mok
+    rng = np.random.default_rng(M * 7 + N * 3 + K + fa * 100 + fb)
+    a, asc, av = operand(rng, M, K, fa)
+    b, bsc, bv = operand(rng, N, K, fb)
+    ref = torch.from_numpy(av @ bv.T)
+    got = gemm(mok, a, asc, b, bsc, behind=3)
+    assert torch.equal(got.double(), ref)
+    got = gemm(mok, a, asc, b, bsc, torch.bfloat16, behind=3)
+    assert torch.equal(got, ref.float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("fa,fb", FMT)
+def test_exact_large_tiles(fa, fb):
+    """Enough tiles for the 256 x 256 form, with ragged rows, columns and K."""
+    import routing_grouped_expert_gemm_amd as mok
+    rng = np.random.default_rng(fa * 10 + fb)
+    for M, N, K in ((3500, 3521, 416), (256 * 12 + 8, 256 * 16, 1024)):
+        a, asc, av = operand(rng, M, K, fa)
+        b, bsc, bv = operand(rng, N, K, fb)
+        ref = (torch.from_numpy(av).to(DEV) @ torch.from_numpy(bv).to(DEV).T).cpu()
+        assert torch.equal(gemm(mok, a, asc, b, bsc).double(), ref)
+
+
+@pytest.mark.parametrize("fa,fb", FMT)
+@pytest.mark.parametrize("M,N,K", [(1, 500, 1024), (60, 100, 7168), (300, 260, 2048), (70, 200, 7168)])
+def test_quantised_rows(M, N, K, fa, fb):
+    """Rows quantised by the library: the product of what the oracle says the codes stand for."""
+    import routing_grouped_expert_gemm_amd as mok
+    g = torch.Generator().manual_seed(M + N + K)
+    deq = {8: oracle.mxfp8_dequantize, 4: oracle.mxfp4_dequantize}
+    ops = []
+    for rows, f in ((M, fa), (N, fb)):
+        x = (torch.randn(rows, K, generator=g) * torch.exp(2 * torch.randn(rows, 1, generator=g))
+             ).to(torch.bfloat16).to(DEV)
+        codes = torch.empty((rows, K if f == 8 else K // 2), dtype=torch.uint8, device=DEV)
+        sc = torch.empty((rows, K // 32), dtype=torch.uint8, device=DEV)
+        (mok.mok_quantize_mxfp8 if f == 8 else mok.mok_quantize_mxfp4)(x, codes, sc)
+        torch.cuda.synchronize()
+        ops.append((codes.cpu().numpy(), sc.cpu().numpy()))
+    (a, asc), (b, bsc) = ops
+    av, bv = deq[fa](a, asc).astype(np.float64), deq[fb](b, bsc).astype(np.float64)
+    got = gemm(mok, a, asc, b, bsc).double().numpy()
+    assert (np.abs(got - av @ bv.T) <= K * 2.0 ** -23 * (np.abs(av) @ np.abs(bv).T)).all()
+    again = gemm(mok, a, asc, b, bsc).double().numpy()
+    assert np.array_equal(got, again)
+
+
+@pytest.mark.parametrize("M", [2, 100])
+def test_scale_range(M):
+    """Scales over the whole E8M0 range whose products stay normal float32 values."""
+    import routing_grouped_expert_gemm_amd as mok
+    rng = np.random.default_rng(3)
+    N, K = 40, 64
+    for sa, sb in ((1, 254), (254, 1), (60, 200), (127, 127), (20, 140)):
+        a, asc, av = operand(rng, M, K, 4, (sa, sa + 1))
+        b, bsc, bv = operand(rng, N, K, 4, (sb, sb + 1))
+        got = gemm(mok, a, asc, b, bsc).double()
+        assert torch.equal(got, torch.from_numpy(av @ bv.T))
+
+
+@pytest.mark.parametrize("M", [2, 100])
+def test_nan_codes_and_scales(M):
+    import routing_grouped_expert_gemm_amd as mok
+    rng = np.random.default_rng(4)
+    N, K = 70, 320
+    a, asc, _ = operand(rng, M, K, 8)
+    b, bsc, _ = operand(rng, N, K, 4)
+    asc[1, 9] = 0xFF
+    bsc[3, 0] = 0xFF
+    got = gemm(mok, a, asc, b, bsc)
+    nan = torch.zeros(M, N, dtype=torch.bool)
+    nan[1], nan[:, 3] = True, True
+    assert torch.equal(torch.isnan(got), nan)
+    a, asc, _ = operand(rng, M, K, 8)
+    b, bsc, _ = operand(rng, N, K, 4)
+    a[1, 319] = 0x7F
+    nan[:, 3], nan[1] = False, True
+    assert torch.equal(torch.isnan(gemm(mok, a, asc, b, bsc)), nan)
+
+
+def test_nothing_to_do():
+    import routing_grouped_expert_gemm_amd as mok
+    rng = np.random.default_rng(5)
+    a, asc, _ = operand(rng, 3, 64, 4)
+    e, esc = np.zeros((0, 32), np.uint8), np.zeros((0, 2), np.uint8)
+    assert gemm(mok, e, esc, a, asc).shape == (0, 3)
+    assert gemm(mok, a, asc, e, esc).shape == (3, 0)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (200, 300, 4096), (70, 64, 7168)])
+def test_graph_replays(M, N, K):
+    import routing_grouped_expert_gemm_amd as mok
+    rng = np.random.default_rng(6)
+    t = [torch.from_numpy(v).to(DEV) for v in operand(rng, M, K, 4)[:2] + operand(rng, N, K, 4)[:2]]
+    c = torch.empty(M, N, device=DEV)
+    n = mok.mok_mx_gemm_workspace_bytes(M, N, K)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    mok.mok_mx_gemm(*t, c, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mok.mok_mx_gemm(*t, c, ws)
+    for _ in range(4):
+        a, asc, av = operand(rng, M, K, 4)
+        t[0].copy_(torch.from_numpy(a))
+        t[1].copy_(torch.from_numpy(asc))
+        e = torch.empty_like(c)
+        mok.mok_mx_gemm(*t, e, ws)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(e, c)
