@@ -432,8 +432,7 @@ int mok_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const
  * dx may be dx_in, and overlaps nothing else. Sums in float32 (bf16 operands enter as they are,
  * dl with at least 16 significant bits for dx and 24 for dw_router); each output is rounded once;
  * no atomics: bit-identical reruns. Sizes as mok_route, d <= 2^24, T k < 2^31.
- * ws: device scratch of mok_route_backward_workspace_bytes(...) bytes, 16-byte aligned; needed for
- * dw_router only. */
+ * ws: device scratch of mok_route_backward_workspace_bytes(...) bytes, 16-byte aligned. */
 int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t io_dtype,
                                        size_t* bytes);
 int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_idx,

@@ -140,7 +140,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm(
     float w[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8];
     if (ok) Piece<T>::load(weight + c, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = h[n][i] * rstd * w[i];
+    for (int i = 0; i < 8; ++i) v[i] = h[n][i] * w[i] * rstd;   // bf16: h w is exact
     if (y && ok) Piece<T>::store(y + at + c, v);
     if (codes) {                   // d % 32 == 0: a quad's four lanes are all inside the row
       uint8_t s;
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_any(
   if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
   auto y_at = [&](int i) {
     const float v = h_out ? load_as_f32(h_out + at + i) : sum_at(i);
-    return v * rstd * load_as_f32(weight + i);
+    return v * load_as_f32(weight + i) * rstd;
   };
   if (codes) {
     for (int b = threadIdx.x; b < d / 32; b += NORM_NT) {
@@ -310,22 +310,25 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_bwd_any(const T* dy, const 
   }
 }
 
-// out[c] = sum of part[0 .. n)[c] : 16 waves a workgroup over 64 columns, each its rows in
-// ascending order, then the waves in ascending order. n == 0 writes zeros.
+// out[c] = sum of part[0 .. n)[c]: a workgroup takes 16 columns (one 64-byte segment of each row)
+// and 64 groups of rows, each group's rows in ascending order, then the groups in a fixed tree.
+// n == 0 writes zeros. (64 columns and 16 groups left 32 workgroups for 2,048 columns and took
+// 11.4 us for 512 rows of them; this took 5 us.)
 __global__ __launch_bounds__(1024) void k_column_sum(const float* __restrict__ part, int n, int d,
                                                      float* __restrict__ out) {
-  __shared__ float sh[16][64];
-  const int lane = lane_id(), g = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  __shared__ float sh[64][17];
+  const int l = threadIdx.x & 15, g = threadIdx.x >> 4, c = blockIdx.x * 16 + l;
   float v = 0.0f;
   if (c < d)
-    for (int i = g; i < n; i += 16) v += part[(int64_t)i * d + c];
-  sh[g][lane] = v;
+    for (int i = g; i < n; i += 64) v += part[(int64_t)i * d + c];
+  sh[g][l] = v;
   __syncthreads();
-  if (g == 0 && c < d) {
 #pragma unroll
-    for (int q = 1; q < 16; ++q) v += sh[q][lane];
-    out[c] = v;
+  for (int m = 32; m > 0; m >>= 1) {
+    if (g < m) sh[g][l] += sh[g + m][l];
+    __syncthreads();
   }
+  if (g == 0 && c < d) out[c] = sh[0][l];
 }
 
 // Workgroups of the backward that keep a share of dweight each.
@@ -403,7 +406,7 @@ hipError_t run_bwd(const T* dy, const T* h, const float* rstd, const T* weight, 
   else MOK_NORM(256, 4);
 #undef MOK_NORM
   if (dweight)
-    launch_k(k_column_sum, dim3((d + 63) / 64), dim3(1024), 0, s, nullptr, nullptr,
+    launch_k(k_column_sum, dim3((d + 15) / 16), dim3(1024), 0, s, nullptr, nullptr,
              (const float*)part, n_part, d, dweight);
   return hipGetLastError();
 }

@@ -6,17 +6,20 @@
 //   dW[e,i]  = sum_t dl[t,e] x[t,i]
 //
 // (w = softmax over a token's picks, so its gradient is the softmax's.) The picks are held
-// fixed. dl is never written out as a whole: a workgroup builds the part it needs in LDS from the
-// picks and the given dlogits.
+// fixed. dW's token sum is cut into ranges whose partial sums a last launch adds in order: no
+// atomics, the same bits every run. Two forms:
 //
-// This form takes any size and alignment: 64 x 64 tiles of both products on the float32 MFMA
-// (operands and sums in float32), 4 waves of 32 x 32, K steps of 32 through LDS. dW's token sum
-// is cut into ranges (one per grid z) whose partial sums a second launch adds in order: no
-// atomics, the same bits every run.
+//  k_route_bwd_any  any type, size and alignment: 64 x 64 tiles of both products on the float32
+//    MFMA (operands and sums in float32), 4 waves of 32 x 32, K steps of 32 through LDS; a
+//    workgroup builds the part of dl it needs in LDS from the picks and the given dlogits.
+//  k_route_bwd_tile  bf16 rows of d % 8 == 0: dl is written once as three bf16 planes that sum to
+//    it (8 + 8 + 8 significant bits: 24, all of float32's), and both products run on the bf16
+//    MFMA with float32 sums: dW on all three planes, dx, which is rounded to 8 bits, on two.
 #include <algorithm>
 
 #include "device_common.h"
 #include "launch.h"
+#include "lds_dma.h"
 #include "mok.h"
 
 namespace mok {
@@ -143,6 +146,266 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_any(const RbArgs a) {
   }
 }
 
+// ------------------------------------------------------------------------- bf16 planes
+// dl as bf16 planes P0 + P1 + P2 [3][Tp][EP], zero past T tokens and E experts: each plane is the
+// rounding of what the ones before leave, so the sum holds 24 bits. 8 experts a thread.
+__global__ __launch_bounds__(256) void k_route_bwd_planes(const RbArgs a, int EP, int64_t Tp,
+                                                          bf16_t* __restrict__ planes) {
+  const int per = EP / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = i / per;
+  const int e0 = (int)(i - t * per) * 8;
+  if (t >= Tp) return;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (t < a.T) {
+    if (a.dlogits) {
+      const float* q = a.dlogits + t * a.E + e0;
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        if (e0 + n < a.E) v[n] = q[n];
+    }
+    const float s = pick_dot(a, t);
+    for (int j = 0; j < a.k; ++j) {
+      const int e = a.idx[t * a.k + j];
+      const int n = e - e0;
+      if (e < a.E && n >= 0 && n < 8) {
+        const float g = a.tw[t * a.k + j] * (a.dtw[t * a.k + j] - s);
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          if (m == n) v[m] += g;
+      }
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      w[n] = pack_bf16x2(v[2 * n], v[2 * n + 1]);
+      const float lo = __uint_as_float(w[n] << 16), hi = __uint_as_float(w[n] & 0xFFFF0000u);
+      v[2 * n] = fabsf(lo) == INFINITY ? 0.0f : v[2 * n] - lo;     // an infinity stays one
+      v[2 * n + 1] = fabsf(hi) == INFINITY ? 0.0f : v[2 * n + 1] - hi;
+    }
+    *(uint4*)(planes + ((int64_t)p * Tp + t) * EP + e0) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+struct RbTile {
+  const bf16_t *x, *w, *dx_in, *planes;
+  bf16_t* dx;
+  float* dw;            // dW itself (one range) or the partial sums [ranges, E, d]
+  int64_t T, Tp;
+  int d, E, EP;
+  int tiles_d;          // tiles of 128 columns
+  int tiles_e;          // tiles of EM experts
+  int dw_blocks;        // workgroups of dW (the first ones); the rest are dx's
+  int64_t t_range;      // tokens of a dW range, a multiple of 64
+};
+
+// An operand whose K is the slow dimension, in LDS: K rows of CH 16-byte chunks, chunk c of row kr
+// at slot c ^ tswz(kr). ds_read_b64_tr_b16 turns it into K-contiguous fragments: in each group of
+// 16 lanes, lane p addresses 4 columns (4 (p % 4) further on) of K row p / 4, and lane i receives
+// column i of the 4 K rows; two reads give a lane its 8 K values. A half wave reads 4 rows x 4
+// chunks at once: the swizzle puts them on 16 distinct slots of the 64 banks.
+template <int CH> MOK_DEV constexpr int tswz(int kr) {
+  return CH == 8 ? 4 * ((kr >> 1) & 1) : 4 * (kr & 3);
+}
+template <int CH>
+MOK_DEV bf16x8_t frag_t(uint32_t tile, int blk, int s, int lane) {
+  typedef short v4i16 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4i16 lds_v4;
+  const int g = lane >> 4, p = lane & 15;
+  const int m = blk + 16 * (g & 1) + 4 * (p & 3);
+  v4i16 v[2];
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    const int kr = 16 * s + 8 * (g >> 1) + 4 * kb + (p >> 2);
+    const int off = kr * CH * 16 + (((m >> 3) ^ tswz<CH>(kr)) << 4) + (m & 7) * 2;
+    v[kb] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)(uintptr_t)(tile + off));
+  }
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Both products in one launch, so that dx's streaming runs beside dW's matrix work. 256 threads.
+//  dW: EM experts x 128 columns over a range of tokens, K steps of KT tokens: three planes and x
+//      through two LDS buffers by LDS-DMA.
+//  dx: 128 tokens x 128 columns, K steps of 64 experts: two planes (K-contiguous rows, chunk c of
+//      row r at slot c ^ (r >> 1 & 7)) and the weight's rows. The tile goes through LDS in float32,
+//      so that dx_in is read and dx written in whole row segments; dx_in is loaded before the
+//      product.
+template <int EM>
+__global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
+  constexpr int KT = EM == 64 ? 64 : 32;
+  constexpr int PB = KT * EM * 2, XB = KT * 256, WST = 3 * PB + XB;      // bytes of a dW step
+  constexpr int DST = 2 * 128 * 128 + 64 * 256;                         // bytes of a dx step
+  constexpr int DBUF = EM == 64 ? 1 : 2;                                // EP == 64: one step
+  constexpr int OLD = 132;                                              // floats of a staged row
+  constexpr int BYTES = std::max(std::max(2 * WST, DBUF * DST), 128 * OLD * 4);
+  __shared__ __align__(1024) char lds[BYTES];
+  const uint32_t lds0 = uniform(lds_addr(lds));
+  const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
+  const int h = lane >> 5, l = lane & 31;
+  // every wave's DMA has landed and its LDS reads are back
+  auto publish = [&]() {
+    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+    lds_barrier();
+  };
+  // LDS-DMA of K rows x CH chunks (row-major source, leading dimension ld): instruction q of this
+  // wave of Q; source row of K row kr: row(kr), columns past the source: the last chunk
+  auto dma_t = [&](auto CH_, int Q, int q, const bf16_t* base, int64_t ld, int c0, int cols,
+                   int last_row, uint32_t to) {
+    constexpr int CH = CH_(), RPI = 64 / CH;
+    const int kr = (wid * Q + q) * RPI + lane / CH;
+    const int c = (lane % CH) ^ tswz<CH>(kr);
+    const int col = min(c0 + 8 * c, cols - 8);
+    dma_b128(uniform_ptr(base), (uint32_t)((min(kr, last_row) * ld + col) * 2),
+             to + (wid * Q + q) * 1024);
+  };
+  if ((int)blockIdx.x < a.dw_blocks) {
+    constexpr int FE = EM == 64 ? 1 : EM == 128 ? 2 : 2, FC = EM == 64 ? 2 : EM == 128 ? 2 : 4;
+    const int b = blockIdx.x, c0 = b % a.tiles_d * 128, rest = b / a.tiles_d;
+    const int e0 = rest % a.tiles_e * EM;
+    const int64_t range = rest / a.tiles_e, tb = range * a.t_range;
+    const int64_t te = min(a.T, tb + a.t_range);
+    const int nk = te > tb ? (int)((te - tb + KT - 1) / KT) : 0;
+    // waves: EM 256: 4 x 1 of 64 experts x 128 columns; else 2 x 2
+    const int we = EM == 256 ? wid * 64 : (wid >> 1) * 32 * FE;
+    const int wc = EM == 256 ? 0 : (wid & 1) * 32 * FC;
+    auto issue = [&](int kt) {
+      const uint32_t to = lds0 + (kt & 1) * WST;
+      const int64_t t0 = tb + (int64_t)kt * KT;
+      constexpr int QP = PB / 4096, QX = XB / 4096;
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int q = 0; q < QP; ++q)
+          dma_t(std::integral_constant<int, EM / 8>{}, QP, q,
+                a.planes + ((int64_t)p * a.Tp + t0) * a.EP + e0, a.EP, 0, EM, KT - 1, to + p * PB);
+#pragma unroll
+      for (int q = 0; q < QX; ++q)
+        dma_t(std::integral_constant<int, 16>{}, QX, q, a.x + t0 * a.d, a.d, c0, a.d,
+              (int)min((int64_t)KT - 1, a.T - 1 - t0), to + 3 * PB);
+    };
+    f32x16_t acc[FE][FC] = {};
+    if (nk > 0) issue(0);
+    for (int kt = 0; kt < nk; ++kt) {
+      publish();
+      if (kt + 1 < nk) issue(kt + 1);
+      const uint32_t at = lds0 + (kt & 1) * WST;
+#pragma unroll
+      for (int s = 0; s < KT / 16; ++s) {
+        bf16x8_t fx[FC];
+#pragma unroll
+        for (int j = 0; j < FC; ++j) fx[j] = frag_t<16>(at + 3 * PB, wc + 32 * j, s, lane);
+#pragma unroll
+        for (int p = 2; p >= 0; --p)           // the smallest plane first
+#pragma unroll
+          for (int i = 0; i < FE; ++i) {
+            const bf16x8_t fp = frag_t<EM / 8>(at + p * PB, we + 32 * i, s, lane);
+#pragma unroll
+            for (int j = 0; j < FC; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fx[j], fp, acc[i][j], 0, 0, 0);
+          }
+      }
+    }
+    float* out = a.dw + range * a.E * a.d;
+#pragma unroll
+    for (int i = 0; i < FE; ++i)
+#pragma unroll
+      for (int j = 0; j < FC; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = e0 + we + 32 * i + l, c = c0 + wc + 32 * j + 8 * q + 4 * h;
+          if (e < a.E && c < a.d)
+            *(float4*)(out + (int64_t)e * a.d + c) =
+                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]);
+        }
+    return;
+  }
+  const int b = blockIdx.x - a.dw_blocks, c0 = b % a.tiles_d * 128;
+  const int64_t t0 = (int64_t)(b / a.tiles_d) * 128;
+  uint4 in[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t t = t0 + i * 16 + tid / 16;
+    const int c = c0 + tid % 16 * 8;
+    in[i] = make_uint4(0, 0, 0, 0);
+    if (a.dx_in && t < a.T && c < a.d) in[i] = *(const uint4*)(a.dx_in + t * a.d + c);
+  }
+  const int wt = (wid >> 1) * 64, wc = (wid & 1) * 64;
+  const int nk = (a.E + 63) / 64;       // every step holds an expert
+  auto issue = [&](int kt) {
+    const uint32_t to = lds0 + (kt & (DBUF - 1)) * DST;
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = (wid * 4 + q) * 8 + (lane >> 3);
+        const int c = (lane & 7) ^ ((r >> 1) & 7);
+        dma_b128(uniform_ptr(a.planes + ((int64_t)p * a.Tp + t0) * a.EP + kt * 64),
+                 (uint32_t)((r * a.EP + 8 * c) * 2), to + p * 16384 + (wid * 4 + q) * 1024);
+      }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      dma_t(std::integral_constant<int, 16>{}, 4, q, a.w + (int64_t)kt * 64 * a.d, a.d, c0, a.d,
+            min(63, a.E - 1 - kt * 64), to + 32768);
+  };
+  f32x16_t acc[2][2] = {};
+  issue(0);
+  for (int kt = 0; kt < nk; ++kt) {
+    publish();
+    if (kt + 1 < nk) issue(kt + 1);
+    const uint32_t at = lds0 + (kt & (DBUF - 1)) * DST;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      bf16x8_t fw[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) fw[j] = frag_t<16>(at + 32768, wc + 32 * j, s, lane);
+#pragma unroll
+      for (int p = 1; p >= 0; --p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = wt + 32 * i + l;
+          const int off = (int)(at - lds0) + p * 16384 + r * 128 + (((2 * s + h) ^ ((r >> 1) & 7)) << 4);
+          const bf16x8_t fp = *(const bf16x8_t*)(lds + off);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[j], fp, acc[i][j], 0, 0, 0);
+        }
+    }
+  }
+  __syncthreads();
+  float* st = (float*)lds;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(float4*)(st + (wt + 32 * i + l) * OLD + wc + 32 * j + 8 * q + 4 * h) =
+            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                        acc[i][j][4 * q + 3]);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 16 + tid / 16;
+    const int64_t t = t0 + r;
+    const int c = c0 + tid % 16 * 8;
+    if (t >= a.T || c >= a.d) continue;
+    const float* q = st + r * OLD + tid % 16 * 8;
+    const float4 u = *(const float4*)q, v = *(const float4*)(q + 4);
+    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+    const float s[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      o[n] = pack_bf16x2(__uint_as_float(w[n] << 16) + s[2 * n],
+                         __uint_as_float(w[n] & 0xFFFF0000u) + s[2 * n + 1]);
+    *(uint4*)(a.dx + t * a.d + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
 // out = the n partial sums of each element, in ascending order (n == 0: zeros).
 __global__ __launch_bounds__(256) void k_route_bwd_sum(const float* __restrict__ part, int n,
                                                        int64_t elems, float* __restrict__ out) {
@@ -157,10 +420,30 @@ __global__ __launch_bounds__(256) void k_route_bwd_sum(const float* __restrict__
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Token ranges of dW: as many as give about two workgroups a CU, each of at least 256 tokens.
+// Token ranges of dW: as many as give about two workgroups a CU, each of at least 64 tokens.
 int64_t any_ranges(int64_t T, int d, int E) {
   const int64_t tiles = cdiv(d, RB_TILE) * cdiv(E, RB_TILE);
-  return std::max<int64_t>(1, std::min(cdiv(512, tiles), cdiv(T, 256)));
+  return std::max<int64_t>(1, std::min(cdiv(512, tiles), cdiv(T, 64)));
+}
+
+// The plane form's shapes: experts padded to the tile EM, tokens to dx's tiles, dW's ranges.
+struct RbPlan {
+  int EM, EP;
+  int64_t Tp, ranges, t_range;
+  size_t planes;                      // bytes; the partial sums follow
+};
+RbPlan rb_plan(int64_t T, int d, int E) {
+  RbPlan p;
+  p.EP = (int)cdiv(E, 64) * 64;
+  if (p.EP > 64) p.EP = (int)cdiv(E, 128) * 128;
+  p.EM = p.EP == 64 ? 64 : p.EP % 256 ? 128 : 256;
+  p.Tp = cdiv(T, 128) * 128;
+  const int64_t tiles = cdiv(d, 128) * (p.EP / p.EM);
+  const int64_t n = std::max<int64_t>(1, std::min(cdiv(256, tiles), cdiv(T, 256)));
+  p.t_range = cdiv(cdiv(T, n), 64) * 64;
+  p.ranges = cdiv(T, p.t_range);
+  p.planes = (size_t)3 * p.Tp * p.EP * 2;
+  return p;
 }
 
 int rb_check(int64_t T, int32_t d, int32_t E, int32_t k, int32_t io_dtype) {
@@ -181,7 +464,12 @@ int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t 
                                        size_t* bytes) {
   if (!bytes || rb_check(T, d, E, 1, io_dtype) != MOK_OK) return MOK_EINVAL;
   const int64_t n = any_ranges(T, d, E);
-  *bytes = n > 1 ? (size_t)n * E * d * sizeof(float) : 256;
+  size_t need = n > 1 ? (size_t)n * E * d * sizeof(float) : 256;
+  if (io_dtype == MOK_BF16 && T > 0) {
+    const RbPlan p = rb_plan(T, d, E);
+    need = std::max(need, p.planes + (p.ranges > 1 ? (size_t)p.ranges * E * d * sizeof(float) : 0));
+  }
+  *bytes = need;
   return MOK_OK;
 }
 
@@ -197,7 +485,7 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
     return MOK_EINVAL;
   size_t need = 0;
   mok_route_backward_workspace_bytes(T, d, E, io_dtype, &need);
-  if (dw_router && (!ws || ws_bytes < need || (uintptr_t)ws % 16)) return MOK_EWORKSPACE;
+  if (!ws || ws_bytes < need || (uintptr_t)ws % 16) return MOK_EWORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   const int64_t elems = (int64_t)E * d;
   const unsigned sum_grid = (unsigned)std::min<int64_t>(cdiv(elems, 256), 4096);
@@ -210,6 +498,34 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
   RbArgs a;
   a.x = x; a.w = w_router; a.idx = topk_idx; a.tw = topk_w; a.dtw = dtopk_w; a.dlogits = dlogits;
   a.dx_in = dx_in; a.dx = dx; a.T = T; a.d = d; a.E = E; a.k = k;
+  auto al16 = [](const void* p) { return (uintptr_t)p % 16 == 0; };
+  if (io_dtype == MOK_BF16 && d % 8 == 0 && al16(x) && al16(w_router) && al16(dx_in) && al16(dx) &&
+      al16(dw_router)) {
+    const RbPlan p = rb_plan(T, d, E);
+    RbTile t;
+    t.x = (const bf16_t*)x; t.w = (const bf16_t*)w_router; t.dx_in = (const bf16_t*)dx_in;
+    t.planes = (const bf16_t*)ws; t.dx = (bf16_t*)dx;
+    t.dw = p.ranges > 1 ? (float*)((char*)ws + p.planes) : dw_router;
+    t.T = T; t.Tp = p.Tp; t.d = d; t.E = E; t.EP = p.EP;
+    t.tiles_d = (int)cdiv(d, 128);
+    t.tiles_e = p.EP / p.EM;
+    t.t_range = p.t_range;
+    const int64_t n_dw = dw_router ? p.ranges * t.tiles_e * t.tiles_d : 0;
+    const int64_t n = n_dw + (dx ? p.Tp / 128 * t.tiles_d : 0), n_pl = cdiv(p.Tp * (p.EP / 8), 256);
+    if (n * RB_NT >= (int64_t)1 << 32 || n_pl * 256 >= (int64_t)1 << 32) return MOK_EUNSUPPORTED;
+    t.dw_blocks = (int)n_dw;
+    launch_k(k_route_bwd_planes, dim3((unsigned)n_pl), dim3(256), 0, s, nullptr, nullptr, a, p.EP,
+             p.Tp, (bf16_t*)ws);
+    if (hipGetLastError() != hipSuccess) return MOK_EHIP;
+    auto k = p.EM == 64 ? k_route_bwd_tile<64> : p.EM == 128 ? k_route_bwd_tile<128>
+                                                           : k_route_bwd_tile<256>;
+    launch_k(k, dim3((unsigned)n), dim3(RB_NT), 0, s, nullptr, nullptr, t);
+    if (hipGetLastError() != hipSuccess) return MOK_EHIP;
+    if (dw_router && p.ranges > 1)
+      launch_k(k_route_bwd_sum, dim3(sum_grid), dim3(256), 0, s, nullptr, nullptr,
+               (const float*)t.dw, (int)p.ranges, elems, dw_router);
+    return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EHIP;
+  }
   a.tiles_d = (int)cdiv(d, RB_TILE);
   a.tiles_e = (int)cdiv(E, RB_TILE);
   a.dx_tiles = dx ? cdiv(T, RB_TILE) * a.tiles_d : 0;
