@@ -220,80 +220,145 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
   const int nk = min(p.steps_per_split, (p.K + KT - 1) / KT - step0);
   const int64_t lda = code_bytes<FA>(p.K), ldb = code_bytes<FB>(p.K);
 
-  // DMA instruction q of this wave: rows (q, wave) of an operand tile
-  auto dma = [&](auto RB_, auto Q_, const uint8_t* base, int64_t ld, int row0, int rows, int kt,
-                 int q, const uint4* buf) {
-    constexpr int RB = RB_(), Q = Q_(), CH = RB / 16, RPI = 64 / CH;
-    const int row = (wid * Q + q) * RPI + lane / CH;
-    const int rr = min(row0 + row, rows - 1) - row0;        // rows past the operand: its last
-    int byte = kt * RB + ((lane % CH) ^ swz<RB>(row)) * 16;
-    byte = min(byte, (int)ld - 16);                         // chunks past K: the row's last
-    dma_b128(uniform_ptr(base + row0 * ld), (uint32_t)(rr * ld + byte),
-             uniform(lds_addr(buf)) + (wid * Q + q) * 1024);
-  };
+  // DMA instruction q of this wave fills LDS rows (wid Q + q) RPI + lane / CH of an operand's
+  // buffer, lane % CH being the slot: its row's byte offset from the tile's first row (rows past
+  // the operand: its last) is kept; the slot's chunk alternates between two with q.
+  constexpr int CHA = C::RBA / 16, CHB = C::RBB / 16, RPA = 64 / CHA, RPB = 64 / CHB;
+  uint32_t off_a[C::QA], off_b[C::QB];
+  int ch_a[2], ch_b[2];
+#pragma unroll
+  for (int q = 0; q < C::QA; ++q) {
+    const int row = (wid * C::QA + q) * RPA + lane / CHA;
+    off_a[q] = (uint32_t)((min(m0 + row, p.M - 1) - m0) * lda);
+    if (q < 2) ch_a[q] = ((lane % CHA) ^ swz<C::RBA>(row)) * 16;
+  }
+#pragma unroll
+  for (int q = 0; q < C::QB; ++q) {
+    const int row = (wid * C::QB + q) * RPB + lane / CHB;
+    off_b[q] = (uint32_t)((min(n0 + row, p.N - 1) - n0) * ldb);
+    if (q < 2) ch_b[q] = ((lane % CHB) ^ swz<C::RBB>(row)) * 16;
+  }
+  const uint8_t* base_a = uniform_ptr(p.a + m0 * lda);
+  const uint8_t* base_b = uniform_ptr(p.b + n0 * ldb);
+  const uint32_t to_a = uniform(lds_addr(lds_a)), to_b = uniform(lds_addr(lds_b));
+  // chunks past K: the row's last (cleared in LDS before they are read)
   auto issue = [&](int kt, int q) {
     __builtin_amdgcn_sched_barrier(0);
-    const int buf = kt & 1, g = step0 + kt;
-    if (q < C::QA)
-      dma(std::integral_constant<int, C::RBA>{}, std::integral_constant<int, C::QA>{}, p.a, lda, m0,
-          p.M, g, q, lds_a[buf]);
-    else
-      dma(std::integral_constant<int, C::RBB>{}, std::integral_constant<int, C::QB>{}, p.b, ldb, n0,
-          p.N, g, q - C::QA, lds_b[buf]);
+    const int g = step0 + kt;
+    if (q < C::QA) {
+      const int ch = min(ch_a[q & 1], (int)lda - 16 - g * C::RBA);
+      dma_b128(base_a + g * C::RBA, off_a[q] + ch,
+               to_a + (kt & 1) * (C::BM * C::RBA) + (wid * C::QA + q) * 1024);
+    } else {
+      const int ch = min(ch_b[(q - C::QA) & 1], (int)ldb - 16 - g * C::RBB);
+      dma_b128(base_b + g * C::RBB, off_b[q - C::QA] + ch,
+               to_b + (kt & 1) * (C::BN * C::RBB) + (wid * C::QB + q - C::QA) * 1024);
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // scale words of step kt of this lane's rows: KT 256: byte s is sub-step s's; KT 128: byte 2 s
-  const uint8_t *as[FM], *bs[FN];
+  constexpr int NQ = C::QA + C::QB, NM = FM * FN;
+  auto issue_all = [&](int kt) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) issue(kt, q);
+  };
+  // Scale words of a step, loaded a step ahead. KT 256: lane half h takes blocks 4 h .. 4 h + 3,
+  // byte s for sub-step s; KT 128: blocks 0 .. 3, shifted by h, byte 2 s.
+  // Words past the row's end are read from its end and shifted into place (a row of fewer than
+  // 4 blocks is one step, read block by block).
+  uint32_t as[FM], bs[FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
-    as[i] = p.as + (int64_t)min(m0 + wm * (C::BM / 2) + 32 * i + r, p.M - 1) * KB;
+    as[i] = (uint32_t)(min(m0 + wm * (C::BM / 2) + 32 * i + r, p.M - 1) - m0) * KB;
 #pragma unroll
   for (int j = 0; j < FN; ++j)
-    bs[j] = p.bs + (int64_t)min(n0 + wn * (C::BN / 2) + 32 * j + r, p.N - 1) * KB;
-  auto scale = [&](const uint8_t* row, int kt) {
-    const int b0 = (step0 + kt) * (KT / 32);
-    if constexpr (KT == 256) return scales_at(row, b0 + 4 * h, KB);
-    else return scales_at(row, b0, KB) >> (8 * h);
-  };
+    bs[j] = (uint32_t)(min(n0 + wn * (C::BN / 2) + 32 * j + r, p.N - 1) - n0) * KB;
+  const uint8_t* base_as = uniform_ptr(p.as + (int64_t)m0 * KB);
+  const uint8_t* base_bs = uniform_ptr(p.bs + (int64_t)n0 * KB);
   uint32_t asc[FM], bsc[FN], asc_n[FM], bsc_n[FN];
+  int sh_n = 0;
   auto load_scales = [&](int kt) {
+    const int b0 = (step0 + kt) * (KT / 32) + (KT == 256 ? 4 * h : 0);
+    const int b = min(b0, KB - 4);
+    sh_n = min(8 * (b0 - b) + (KT == 256 ? 0 : 8 * h), 31);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) asc_n[i] = scale(as[i], kt);
+    for (int i = 0; i < FM; ++i) asc_n[i] = load_word(base_as + (as[i] + b));
 #pragma unroll
-    for (int j = 0; j < FN; ++j) bsc_n[j] = scale(bs[j], kt);
+    for (int j = 0; j < FN; ++j) bsc_n[j] = load_word(base_bs + (bs[j] + b));
+  };
+  auto load_scales_short = [&]() {
+    sh_n = KT == 256 ? 0 : 8 * h;
+    const int b0 = KT == 256 ? 4 * h : 0;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) asc_n[i] = scales_at(base_as + as[i], b0, KB);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bsc_n[j] = scales_at(base_bs + bs[j], b0, KB);
+  };
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) asc[i] = asc_n[i] >> sh_n;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bsc[j] = bsc_n[j] >> sh_n;
+  };
+  // blocks of step kt that K holds (KT / 32, fewer in a ragged last step)
+  auto left = [&](int kt) { return KB - (step0 + kt) * (KT / 32); };
+  // a ragged last step: the codes past K, which the DMA filled with the row's last chunk, are
+  // cleared where this wave's DMA put them (after it landed, before the barrier that publishes it)
+  auto clear_tail = [&](auto F_, auto RB_, auto Q_, uint4* buf, int kt) {
+    constexpr int F = F_(), RB = RB_(), Q = Q_(), CH = RB / 16, RPI = 64 / CH;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int row = (wid * Q + q) * RPI + lane / CH;
+      const int c = (lane % CH) ^ swz<RB>(row);             // the chunk at this lane's slot
+      if ((F == F8 ? c / 2 : c) >= left(kt))
+        buf[(wid * Q + q) * 64 + lane] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  // Step kt is whole in LDS: every wave's DMA and scales issued so far have landed and its LDS
+  // reads are back. LAST: kt may be the ragged last step.
+  auto publish = [&](int kt, auto LAST) {
+    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+    if constexpr (LAST()) {
+      if (left(kt) < KT / 32) {
+        clear_tail(std::integral_constant<int, FA>{}, std::integral_constant<int, C::RBA>{},
+                   std::integral_constant<int, C::QA>{}, lds_a[kt & 1], kt);
+        clear_tail(std::integral_constant<int, FB>{}, std::integral_constant<int, C::RBB>{},
+                   std::integral_constant<int, C::QB>{}, lds_b[kt & 1], kt);
+        __builtin_amdgcn_s_waitcnt(0x70);
+      }
+    }
+    lds_barrier();
   };
   Frag<FA> fa[2][FM];
   Frag<FB> fb[2][FN];
   // block pairs of sub-step s: (s, 4 + s) of 8 blocks (KT 256) or (2 s, 2 s + 1) of 4 (KT 128)
   auto blk = [](int s, int x) { return KT == 256 ? 4 * x + s : 2 * s + x; };
-  auto read = [&](auto f, auto RB_, const uint4* buf, int row, int kt, int s) {
+  auto read = [&](auto f, auto RB_, const uint4* buf, int row, int s) {
     constexpr int RB = RB_(), CH = RB / 16;
     Frag<f()> v;
     const uint4* base = buf + row * CH;
-    const int left = KB - (step0 + kt) * (KT / 32);         // blocks from this step on
     if constexpr (f() == F4) {
       v.q[0] = base[blk(s, h) ^ swz<RB>(row)];
-      if (left < KT / 32 && blk(s, h) >= left) v.zero();
     } else {
       v.q[0] = base[(2 * blk(s, 0) + h) ^ swz<RB>(row)];
       v.q[1] = base[(2 * blk(s, 1) + h) ^ swz<RB>(row)];
-      if (left < KT / 32) {
-        if (blk(s, 0) >= left) v.q[0] = make_uint4(0, 0, 0, 0);
-        if (blk(s, 1) >= left) v.q[1] = make_uint4(0, 0, 0, 0);
-      }
     }
     return v;
   };
+  // in the order in which the MFMAs first use them
   auto frags = [&](int kt, int s, int f) {
     const uint4 *A = lds_a[kt & 1], *B = lds_b[kt & 1];
+    auto a_at = [&](int i) {
+      fa[f][i] = read(std::integral_constant<int, FA>{}, std::integral_constant<int, C::RBA>{}, A,
+                      wm * (C::BM / 2) + 32 * i + r, s);
+    };
+    __builtin_amdgcn_sched_barrier(0);
+    a_at(0);
 #pragma unroll
     for (int j = 0; j < FN; ++j)
       fb[f][j] = read(std::integral_constant<int, FB>{}, std::integral_constant<int, C::RBB>{}, B,
-                      wn * (C::BN / 2) + 32 * j + r, kt, s);
+                      wn * (C::BN / 2) + 32 * j + r, s);
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-      fa[f][i] = read(std::integral_constant<int, FA>{}, std::integral_constant<int, C::RBA>{}, A,
-                      wm * (C::BM / 2) + 32 * i + r, kt, s);
+    for (int i = 1; i < FM; ++i) a_at(i);
     __builtin_amdgcn_sched_barrier(0);
   };
   f32x16_t acc[FM][FN];
@@ -303,7 +368,6 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  constexpr int NQ = C::QA + C::QB, NM = FM * FN;
   auto mfmas = [&](auto s, auto&& after) {
     constexpr int SEL = KT == 256 ? s() : 2 * s(), F = s() & 1;
 #pragma unroll
@@ -315,51 +379,42 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
       }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto take_scales = [&]() {
-#pragma unroll
-    for (int i = 0; i < FM; ++i) asc[i] = asc_n[i];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) bsc[j] = bsc_n[j];
-  };
-  // every wave's DMA and scales issued so far have landed and its LDS reads are back
-  auto publish = [&]() {
-    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
-    lds_barrier();
-  };
-
-  for (int q = 0; q < NQ; ++q) issue(0, q);
-  load_scales(0);
-  publish();
-  take_scales();
-  if (nk > 1) {
-    for (int q = 0; q < NQ; ++q) issue(1, q);
-    load_scales(1);
-  }
-  frags(0, 0, 0);
-  for (int kt = 0; kt < nk; ++kt) {
+  // One K step. MORE: a step follows (LAST: the last one); DMA: another one after that, whose
+  // loads are issued here. No branches inside: the compiler moves MFMAs past them.
+  auto step = [&](int kt, auto MORE, auto LAST, auto DMA) {
     static_for<SUB - 1>([&](auto s) {
       mfmas(s, [&](int n) {
-        if (n == NM / 2 - 1) {
-          __builtin_amdgcn_sched_barrier(0);
-          frags(kt, s() + 1, (s() + 1) & 1);
-        }
+        if (n == NM / 2 - 1) frags(kt, s() + 1, (s() + 1) & 1);
       });
     });
-    publish();                          // step kt + 1 has landed; all reads of kt are back
-    const bool more = kt + 1 < nk, dma_more = kt + 2 < nk;
+    if constexpr (MORE()) publish(kt + 1, LAST);     // and all reads of step kt are back
     mfmas(std::integral_constant<int, SUB - 1>{}, [&](int n) {
-      if (n == NM / 2 - 1 && more) {
-        __builtin_amdgcn_sched_barrier(0);
-        frags(kt + 1, 0, 0);
+      if constexpr (MORE()) {
+        if (n == NM / 2 - 1) frags(kt + 1, 0, 0);
       }
-      if (dma_more) {
+      if constexpr (DMA()) {
 #pragma unroll
         for (int q = n * NQ / NM; q < (n + 1) * NQ / NM; ++q) issue(kt + 2, q);
       }
     });
-    if (more) take_scales();
-    if (dma_more) load_scales(kt + 2);
+    if constexpr (MORE()) take_scales();
+    if constexpr (DMA()) load_scales(kt + 2);
+  };
+  constexpr std::integral_constant<bool, true> yes{};
+  constexpr std::integral_constant<bool, false> no{};
+  issue_all(0);
+  if (KB < 4) load_scales_short(); else load_scales(0);
+  publish(0, yes);
+  take_scales();
+  if (nk > 1) {
+    issue_all(1);
+    load_scales(1);
   }
+  frags(0, 0, 0);
+  int kt = 0;
+  for (; kt < nk - 2; ++kt) step(kt, yes, no, yes);
+  if (kt < nk - 1) step(kt++, yes, yes, no);
+  step(kt, no, no, no);
   void* c = p.c;
   bool f32 = p.out_f32;
   if (p.splits > 1) {
