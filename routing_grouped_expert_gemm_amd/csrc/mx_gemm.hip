@@ -181,20 +181,23 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
 }
 
 // ------------------------------------------------------------------------- LDS tiles
-// BM x BN tiles, 4 waves (2 x 2) of BM/2 x BN/2. K steps of KT values go to one of two LDS
-// buffers by LDS-DMA (16-byte chunks; chunk c of row r at slot c ^ swz(r), so that the 16 rows
-// that a quarter of a wave reads at one chunk hit distinct banks). A step's last sub-step follows
-// the barrier that publishes the next step's buffer: its MFMAs cover the next step's first LDS
-// reads, and the DMA of the step after that is issued among them.
-template <int FA_, int FB_, int BM_, int BN_>
+// BM x BN tiles, 4 waves (2 x 2) of BM/2 x BN/2. K steps of KT values go to one of ST LDS buffers
+// by LDS-DMA (16-byte chunks; chunk c of row r at slot c ^ swz(r), so that the 16 rows that a
+// quarter of a wave reads at one chunk hit distinct banks). A step's last sub-step follows the
+// barrier that publishes the next step's buffer: its MFMAs cover the next step's first LDS reads,
+// and the DMA of the step ST steps on, into the buffer just read, is issued among them.
+// 128 x 128 tiles leave room for 4 buffers: their steps are shorter than a load's way from memory.
+// AL: K % 512 == 0, so that 16-byte pieces of the scale rows are aligned and also go by DMA.
+template <int FA_, int FB_, int BM_, int BN_, bool AL_>
 struct Tile {
   static constexpr int FA = FA_, FB = FB_, BM = BM_, BN = BN_;
+  static constexpr bool AL = AL_;
   static constexpr int KT = FA == F4 && FB == F4 ? 256 : 128;
+  static constexpr int ST = AL && BM == 128 ? 4 : 2;
   static constexpr int SUB = KT / 64;
   static constexpr int FM = BM / 64, FN = BN / 64;
   static constexpr int RBA = code_bytes<FA>(KT), RBB = code_bytes<FB>(KT);   // bytes of a row
   static constexpr int QA = BM * RBA / 4096, QB = BN * RBB / 4096;   // DMA instructions a wave
-  static constexpr int LDS = 2 * (BM * RBA + BN * RBB);
 };
 
 template <int RB> MOK_DEV constexpr int swz(int r) {
@@ -204,7 +207,14 @@ template <int RB> MOK_DEV constexpr int swz(int r) {
 template <class C>
 __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
   constexpr int FA = C::FA, FB = C::FB, FM = C::FM, FN = C::FN, SUB = C::SUB, KT = C::KT;
-  __shared__ uint4 lds_a[2][C::BM * C::RBA / 16], lds_b[2][C::BN * C::RBB / 16];
+  constexpr int ST = C::ST;
+  constexpr int A_B = C::BM * C::RBA, B_B = C::BN * C::RBB, S_B = (C::BM + C::BN) * 32;   // bytes
+  __shared__ __align__(1024) char lds[ST * (A_B + B_B) + 2 * S_B];
+  char* const lds_b0 = lds + ST * A_B;
+  char* const lds_s0 = lds_b0 + ST * B_B;
+  auto buf_a = [&](int kt) { return (uint4*)(lds + kt % ST * A_B); };
+  auto buf_b = [&](int kt) { return (uint4*)(lds_b0 + kt % ST * B_B); };
+  auto buf_s = [&](int g) { return (uint32_t*)(lds_s0 + (g & 1) * S_B); };
   const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
   const int wm = wid >> 1, wn = wid & 1, h = lane >> 5, r = lane & 31;
   // XCD x takes consecutive tiles, 8 M tiles deep, so that its L2 holds their operands
@@ -240,7 +250,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
   }
   const uint8_t* base_a = uniform_ptr(p.a + m0 * lda);
   const uint8_t* base_b = uniform_ptr(p.b + n0 * ldb);
-  const uint32_t to_a = uniform(lds_addr(lds_a)), to_b = uniform(lds_addr(lds_b));
+  const uint32_t to_a = uniform(lds_addr(lds)), to_b = to_a + ST * A_B, to_s = to_b + ST * B_B;
   // chunks past K: the row's last (cleared in LDS before they are read)
   auto issue = [&](int kt, int q) {
     __builtin_amdgcn_sched_barrier(0);
@@ -248,11 +258,11 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
     if (q < C::QA) {
       const int ch = min(ch_a[q & 1], (int)lda - 16 - g * C::RBA);
       dma_b128(base_a + g * C::RBA, off_a[q] + ch,
-               to_a + (kt & 1) * (C::BM * C::RBA) + (wid * C::QA + q) * 1024);
+               to_a + kt % ST * A_B + (wid * C::QA + q) * 1024);
     } else {
       const int ch = min(ch_b[(q - C::QA) & 1], (int)ldb - 16 - g * C::RBB);
       dma_b128(base_b + g * C::RBB, off_b[q - C::QA] + ch,
-               to_b + (kt & 1) * (C::BN * C::RBB) + (wid * C::QB + q - C::QA) * 1024);
+               to_b + kt % ST * B_B + (wid * C::QB + q - C::QA) * 1024);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -261,43 +271,77 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) issue(kt, q);
   };
-  // Scale words of a step, loaded a step ahead. KT 256: lane half h takes blocks 4 h .. 4 h + 3,
-  // byte s for sub-step s; KT 128: blocks 0 .. 3, shifted by h, byte 2 s.
-  // Words past the row's end are read from its end and shifted into place (a row of fewer than
-  // 4 blocks is one step, read block by block).
-  uint32_t as[FM], bs[FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-    as[i] = (uint32_t)(min(m0 + wm * (C::BM / 2) + 32 * i + r, p.M - 1) - m0) * KB;
-#pragma unroll
-  for (int j = 0; j < FN; ++j)
-    bs[j] = (uint32_t)(min(n0 + wn * (C::BN / 2) + 32 * j + r, p.N - 1) - n0) * KB;
-  const uint8_t* base_as = uniform_ptr(p.as + (int64_t)m0 * KB);
-  const uint8_t* base_bs = uniform_ptr(p.bs + (int64_t)n0 * KB);
-  uint32_t asc[FM], bsc[FN], asc_n[FM], bsc_n[FN];
-  int sh_n = 0;
-  auto load_scales = [&](int kt) {
-    const int b0 = (step0 + kt) * (KT / 32) + (KT == 256 ? 4 * h : 0);
-    const int b = min(b0, KB - 4);
-    sh_n = min(8 * (b0 - b) + (KT == 256 ? 0 : 8 * h), 31);
-#pragma unroll
-    for (int i = 0; i < FM; ++i) asc_n[i] = load_word(base_as + (as[i] + b));
-#pragma unroll
-    for (int j = 0; j < FN; ++j) bsc_n[j] = load_word(base_bs + (bs[j] + b));
+  // Scales go through LDS in groups of SG steps: 32 bytes of each of the tile's BM + BN rows (A's
+  // first), two buffers. (Read from memory by every lane for its own rows and step, a word at a
+  // time, they touched as many cache lines as the codes: M 8192, N 4096, K 7168 took 155 us,
+  // against 126 without any scales.) 16-byte half x of row r lies at half x ^ (r >> 3 & 1), which
+  // spreads a column of words over the banks. Pieces of the next group are loaded one a step, P
+  // pieces from one step before the current group on (then over again: the same bytes), so that
+  // the last one is published with the step before that group's first. A piece is 64 rows of each
+  // operand, 16 bytes a lane: waves 0 and 1 load A's, 2 and 3 B's.
+  constexpr int SG = 32 / (KT / 32), P = C::BM / 64;
+  static_assert(C::BM == C::BN, "both operands' scales in the same number of pieces");
+  const bool tiny = KB < 16;
+  const uint8_t* base_sc = uniform_ptr(wid < 2 ? p.as + (int64_t)m0 * KB : p.bs + (int64_t)n0 * KB);
+  const int sc_last = uniform(wid < 2 ? p.M - 1 - m0 : p.N - 1 - n0);      // the operand's last row
+  const int sc_r = (wid & 1) * 32 + lane / 2;                              // row in piece 0
+  auto sc_at = [&](int t) { return (uint32_t)min(t * 64 + sc_r, sc_last) * (uint32_t)KB; };
+  const int sc_half = (lane ^ (sc_r >> 3)) & 1;       // the half of the row that slot lane & 1 holds
+  const int sc_byte = step0 * (KT / 32) + 16 * sc_half;
+  const int sc_to = (wid >> 1) * C::BM + (wid & 1) * 32;                   // LDS row of piece 0
+  // AL: past the row's end: its last 16 bytes
+  auto sc_dma = [&](int g, int t) {
+    __builtin_amdgcn_sched_barrier(0);
+    dma_b128(base_sc, sc_at(t) + min(sc_byte + g * 32, KB - 16),
+             to_s + (g & 1) * S_B + (sc_to + t * 64) * 32);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  auto load_scales_short = [&]() {
-    sh_n = KT == 256 ? 0 : 8 * h;
-    const int b0 = KT == 256 ? 4 * h : 0;
+  // else through registers: 16 bytes from the row's byte, or the row's last 16 where it ends
+  // before, then shifted down by the bytes that it starts early. Rows of fewer than 16 blocks:
+  // byte by byte (one group; the steps' loads then read the codes, and are not used).
+  auto sc_load = [&](int g, int t) {
+    uint4 v;
+    __builtin_memcpy(&v, tiny ? p.a : base_sc + (sc_at(t) + min(sc_byte + g * 32, KB - 16)), 16);
+    return v;
+  };
+  auto sc_put = [&](int g, int t, uint4 v) {
+    *(uint4*)&buf_s(g)[(sc_to + t * 64) * 8 + lane * 4] = v;
+  };
+  auto sc_store = [&](int g, int t, uint4 v) {
+    const int early = max(sc_byte + g * 32 - (KB - 16), 0), by = early & 3, wd = early >> 2;
+    uint32_t w0 = __builtin_amdgcn_alignbyte(v.y, v.x, by), w1 = __builtin_amdgcn_alignbyte(v.z, v.y, by),
+             w2 = __builtin_amdgcn_alignbyte(v.w, v.z, by), w3 = __builtin_amdgcn_alignbyte(0u, v.w, by);
+    const bool s1 = wd & 1, s2 = wd & 2;
+    w0 = s1 ? w1 : w0; w1 = s1 ? w2 : w1; w2 = s1 ? w3 : w2; w3 = s1 ? 0u : w3;
+    w0 = s2 ? w2 : w0; w1 = s2 ? w3 : w1; w2 = s2 ? 0u : w2; w3 = s2 ? 0u : w3;
+    sc_put(g, t, make_uint4(w0, w1, w2, w3));
+  };
+  auto sc_short = [&](int t) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    const uint8_t* q = base_sc + sc_at(t);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) asc_n[i] = scales_at(base_as + as[i], b0, KB);
+    for (int i = 0; i < 16; ++i)
+      if (16 * sc_half + i < KB) w[i >> 2] |= (uint32_t)q[16 * sc_half + i] << (8 * (i & 3));
+    sc_put(0, t, make_uint4(w[0], w[1], w[2], w[3]));
+  };
+  // a step's scale words of this lane's rows. KT 256: lane half h takes blocks 4 h .. 4 h + 3,
+  // byte s for sub-step s; KT 128: blocks 0 .. 3, shifted by h, byte 2 s.
+  uint32_t asc[FM], bsc[FN], asc_n[FM], bsc_n[FN];
+  auto read_scales = [&](int kt) {
+    const int w = (KT == 256 ? 2 * (kt % SG) + h : kt % SG) ^ (4 * ((r >> 3) & 1));
+    const uint32_t* S = buf_s(kt / SG);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) bsc_n[j] = scales_at(base_bs + bs[j], b0, KB);
+    for (int i = 0; i < FM; ++i) asc_n[i] = S[(wm * (C::BM / 2) + 32 * i + r) * 8 + w];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bsc_n[j] = S[(C::BM + wn * (C::BN / 2) + 32 * j + r) * 8 + w];
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto take_scales = [&]() {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) asc[i] = asc_n[i] >> sh_n;
+    for (int i = 0; i < FM; ++i) asc[i] = KT == 256 ? asc_n[i] : asc_n[i] >> (8 * h);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) bsc[j] = bsc_n[j] >> sh_n;
+    for (int j = 0; j < FN; ++j) bsc[j] = KT == 256 ? bsc_n[j] : bsc_n[j] >> (8 * h);
   };
   // blocks of step kt that K holds (KT / 32, fewer in a ragged last step)
   auto left = [&](int kt) { return KB - (step0 + kt) * (KT / 32); };
@@ -313,16 +357,18 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
         buf[(wid * Q + q) * 64 + lane] = make_uint4(0, 0, 0, 0);
     }
   };
-  // Step kt is whole in LDS: every wave's DMA and scales issued so far have landed and its LDS
-  // reads are back. LAST: kt may be the ragged last step.
-  auto publish = [&](int kt, auto LAST) {
-    __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
+  // Step kt is whole in LDS: every wave's DMA of it has landed (all but the OUT vector-memory
+  // instructions that it issued last: vmcnt counts in order) and its LDS reads are back. LAST: kt
+  // may be the ragged last step.
+  auto publish = [&](int kt, auto OUT, auto LAST) {
+    static_assert(OUT() < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((OUT() & 15) | ((OUT() >> 4) << 14) | (7 << 4));   // lgkmcnt(0)
     if constexpr (LAST()) {
       if (left(kt) < KT / 32) {
         clear_tail(std::integral_constant<int, FA>{}, std::integral_constant<int, C::RBA>{},
-                   std::integral_constant<int, C::QA>{}, lds_a[kt & 1], kt);
+                   std::integral_constant<int, C::QA>{}, buf_a(kt), kt);
         clear_tail(std::integral_constant<int, FB>{}, std::integral_constant<int, C::RBB>{},
-                   std::integral_constant<int, C::QB>{}, lds_b[kt & 1], kt);
+                   std::integral_constant<int, C::QB>{}, buf_b(kt), kt);
         __builtin_amdgcn_s_waitcnt(0x70);
       }
     }
@@ -346,7 +392,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
   };
   // in the order in which the MFMAs first use them
   auto frags = [&](int kt, int s, int f) {
-    const uint4 *A = lds_a[kt & 1], *B = lds_b[kt & 1];
+    const uint4 *A = buf_a(kt), *B = buf_b(kt);
     auto a_at = [&](int i) {
       fa[f][i] = read(std::integral_constant<int, FA>{}, std::integral_constant<int, C::RBA>{}, A,
                       wm * (C::BM / 2) + 32 * i + r, s);
@@ -379,47 +425,115 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
       }
     __builtin_amdgcn_sched_barrier(0);
   };
-  // One K step. MORE: a step follows (LAST: the last one); DMA: another one after that, whose
-  // loads are issued here. No branches inside: the compiler moves MFMAs past them.
-  auto step = [&](int kt, auto MORE, auto LAST, auto DMA) {
+  // One K step. MORE: a step follows; LAST: it may be the last one; DMA: the loads of step kt + ST
+  // and one scale piece are issued here, and OUT vector-memory instructions may stay in flight at
+  // the barrier. No branches inside the main loop's form: the compiler moves MFMAs past them.
+  auto step = [&](int kt, auto MORE, auto LAST, auto DMA, auto OUT) {
+    const int sg = (kt + 1) / SG + 1, st = (kt + 1) % SG % P;    // the scale piece on its way
+    uint4 sv;
+    if constexpr (DMA() && !C::AL) sv = sc_load(sg, st);
     static_for<SUB - 1>([&](auto s) {
       mfmas(s, [&](int n) {
         if (n == NM / 2 - 1) frags(kt, s() + 1, (s() + 1) & 1);
       });
     });
-    if constexpr (MORE()) publish(kt + 1, LAST);     // and all reads of step kt are back
+    if constexpr (MORE()) publish(kt + 1, OUT, LAST);     // and all reads of step kt are back
     mfmas(std::integral_constant<int, SUB - 1>{}, [&](int n) {
       if constexpr (MORE()) {
+        if (n == 0) read_scales(kt + 1);
         if (n == NM / 2 - 1) frags(kt + 1, 0, 0);
       }
       if constexpr (DMA()) {
+        if (n == 1) {
+          if constexpr (C::AL) sc_dma(sg, st); else sc_store(sg, st, sv);
+        }
 #pragma unroll
-        for (int q = n * NQ / NM; q < (n + 1) * NQ / NM; ++q) issue(kt + 2, q);
+        for (int q = n * NQ / NM; q < (n + 1) * NQ / NM; ++q) issue(kt + ST, q);
       }
     });
     if constexpr (MORE()) take_scales();
-    if constexpr (DMA()) load_scales(kt + 2);
   };
   constexpr std::integral_constant<bool, true> yes{};
   constexpr std::integral_constant<bool, false> no{};
-  issue_all(0);
-  if (KB < 4) load_scales_short(); else load_scales(0);
-  publish(0, yes);
-  take_scales();
-  if (nk > 1) {
-    issue_all(1);
-    load_scales(1);
+  constexpr std::integral_constant<int, 0> none{};
+#pragma unroll
+  for (int t = 0; t < P; ++t) {
+    if constexpr (C::AL) {
+      sc_dma(0, t);
+    } else {
+      if (tiny) sc_short(t);
+      else sc_store(0, t, sc_load(0, t));
+    }
   }
+  if constexpr (C::AL) {
+    sc_dma(1, 0);
+  } else {
+    if (KB > 32) sc_store(1, 0, sc_load(1, 0));
+  }
+  issue_all(0);
+  if (nk >= ST) {
+#pragma unroll
+    for (int i = 1; i < ST; ++i) issue_all(i);
+    publish(0, std::integral_constant<int, (ST - 1) * NQ>{}, yes);
+  } else {
+    for (int i = 1; i < nk; ++i) issue_all(i);
+    publish(0, none, yes);
+  }
+  read_scales(0);
+  take_scales();
   frags(0, 0, 0);
   int kt = 0;
-  for (; kt < nk - 2; ++kt) step(kt, yes, no, yes);
-  if (kt < nk - 1) step(kt++, yes, yes, no);
-  step(kt, no, no, no);
+  for (; kt < nk - ST; ++kt)
+    step(kt, yes, no, yes, std::integral_constant<int, (ST - 2) * (NQ + 1)>{});
+  for (; kt < nk - 1; ++kt) step(kt, yes, yes, no, none);
+  step(kt, no, no, no, none);
+
   void* c = p.c;
   bool f32 = p.out_f32;
   if (p.splits > 1) {
     c = (float*)p.c + (int64_t)blockIdx.z * p.M * p.N;
     f32 = true;
+  }
+  if (p.N % 8 == 0) {
+    // Each wave puts its blocks of 32 rows through its own part of the operand buffers and writes
+    // whole row segments, 16 bytes a lane (straight from the accumulators, 8 bytes a lane and 32
+    // rows an instruction, the stores took 34 of 149 us at M 8192, N 4096, K 7168).
+    constexpr int WN = C::BN / 2;
+    char* mine = lds + wid * (32 * (WN * 4 + 16));
+    __syncthreads();                              // every wave is past its last fragment reads
+    // the lane made opaque again: what derives from it is computed here, not held over the K loop
+    const int lane_ = opaque(threadIdx.x) & 63;
+    auto out = [&, lane = lane_, r = lane_ & 31, h = lane_ >> 5](auto F32) {
+      constexpr int es = F32() ? 4 : 2, ld = WN * es + 16;
+      constexpr int seg = WN * es / 16, at_once = 64 / seg;    // lanes a row, rows a store
+      const int piece = lane % seg, col = n0 + wn * WN + piece * (16 / es);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            char* at = mine + r * ld + (32 * j + 8 * q + 4 * h) * es;
+            const f32x16_t& v = acc[i][j];
+            if constexpr (F32())
+              *(float4*)at = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            else
+              *(uint2*)at = make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]),
+                                       pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
+          }
+        const int row0 = m0 + wm * (C::BM / 2) + 32 * i;
+#pragma unroll
+        for (int x0 = 0; x0 < 32; x0 += at_once) {
+          const int x = x0 + lane / seg;
+          const uint4 v = *(const uint4*)(mine + x * ld + piece * 16);
+          if (row0 + x < p.M && col < p.N)
+            *(uint4*)((char*)c + ((int64_t)(row0 + x) * p.N + col) * es) = v;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    if (f32) out(yes); else out(no);
+    return;
   }
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -479,17 +593,19 @@ hipError_t run_mx(MxArgs p, const Plan& t, float* part, void* c, hipStream_t s) 
   }
   p.tiles_m = (int)cdiv(p.M, t.tile);
   p.tiles_n = (int)cdiv(p.N, t.tile);
-  constexpr int KT = Tile<FA, FB, 128, 128>::KT;
+  constexpr int KT = Tile<FA, FB, 128, 128, true>::KT;
   const int64_t steps = cdiv(p.K, KT);
-  p.steps_per_split = (int)cdiv(steps, t.splits);
+  p.steps_per_split = (int)cdiv(cdiv(steps, t.splits), 4) * 4;   // whole aligned scale pieces
   p.splits = (int)cdiv(steps, p.steps_per_split);       // every range has a step
   p.c = p.splits > 1 ? part : c;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   const dim3 grid((unsigned)(8 * cdiv(tiles, 8)), 1, p.splits);
-  if (t.tile == 256)
-    launch_k(k_mx_tile<Tile<FA, FB, 256, 256>>, grid, dim3(256), 0, s, nullptr, nullptr, p);
-  else
-    launch_k(k_mx_tile<Tile<FA, FB, 128, 128>>, grid, dim3(256), 0, s, nullptr, nullptr, p);
+  const bool al = p.K % 512 == 0 && (uintptr_t)p.as % 16 == 0 && (uintptr_t)p.bs % 16 == 0;
+  auto k = t.tile == 256 ? (al ? k_mx_tile<Tile<FA, FB, 256, 256, true>>
+                               : k_mx_tile<Tile<FA, FB, 256, 256, false>>)
+                         : (al ? k_mx_tile<Tile<FA, FB, 128, 128, true>>
+                               : k_mx_tile<Tile<FA, FB, 128, 128, false>>);
+  launch_k(k, grid, dim3(256), 0, s, nullptr, nullptr, p);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (p.splits > 1) {
     const int64_t elems = (int64_t)p.M * p.N;
