@@ -151,11 +151,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream=None):
+def _stream(stream=None, dev=None):
     if stream is not None:
         return getattr(stream, "cuda_stream", stream)
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    if dev is None:
+        dev = torch.cuda.current_device()
+    # the current stream's handle (building the Stream object around it costs 2.7 us a call)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 # ------------------------------------------------------------------------ entry points
@@ -286,23 +289,23 @@ def mok_get_device_error(workspace, stream=None) -> int:
 # goes to the tensors' own device: its current stream, or `stream`, which must belong to it.
 
 class _Args:
-    """Checks the tensors of one call and holds the device they share."""
+    """Checks the tensors of one call, all on the GPU of the first."""
+    __slots__ = ("fn", "dev")
 
-    def __init__(self, fn: str):
-        self.fn, self.dev = fn, None
+    def __init__(self, fn: str, first):
+        self.fn, self.dev = fn, first.get_device()
+        if self.dev < 0:
+            self.bad()
 
     def bad(self):
         raise MokError(self.fn, MOK_EINVAL)
 
-    def __call__(self, t, dtype, shape=None):
-        """Pointer of t: contiguous, on the call's GPU, of this dtype and shape (None: any)."""
+    def __call__(self, t, dtype, shape):
+        """Pointer of t: contiguous, on the call's GPU, of this dtype and shape (None: none)."""
         if t is None:
             return None
-        dev = t.get_device()
-        if self.dev is None:
-            self.dev = dev
-        if (dev != self.dev or dev < 0 or t.dtype is not dtype or not t.is_contiguous()
-                or (shape is not None and t.shape != shape)):
+        if (t.dtype is not dtype or t.shape != shape or t.get_device() != self.dev
+                or not t.is_contiguous()):
             self.bad()
         return t.data_ptr()
 
@@ -317,10 +320,12 @@ class _Args:
     def run(self, f, *args, stream=None):
         import torch
         if self.dev == torch.cuda.current_device():
-            _check(self.fn, f(*args, _stream(stream)))
+            status = f(*args, _stream(stream, self.dev))
         else:
             with torch.cuda.device(self.dev):
-                _check(self.fn, f(*args, _stream(stream)))
+                status = f(*args, _stream(stream, self.dev))
+        if status != MOK_OK:
+            raise MokError(self.fn, status)
 
 
 def _io_of(a: _Args, t) -> int:
@@ -345,13 +350,13 @@ def mok_balance_loss(logits, topk_idx, alpha: float, loss, counts, mean_prob, ws
     and mean probabilities [S, E] float32 of the S packed sequences of seq_offsets [S + 1] int32
     (None: one sequence). ws: mok_balance_loss_workspace_bytes(T, E, S) bytes."""
     import torch
-    a = _Args("mok_balance_loss")
+    a = _Args("mok_balance_loss", logits)
     if logits.dim() != 2 or topk_idx.dim() != 2:
         a.bad()
     (T, E), k = logits.shape, topk_idx.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
     f32, i32 = torch.float32, torch.int32
-    args = (a(logits, f32), a(topk_idx, i32, (T, k)), T, E, k, a(seq_offsets, i32, (S + 1,)), S,
+    args = (a(logits, f32, (T, E)), a(topk_idx, i32, (T, k)), T, E, k, a(seq_offsets, i32, (S + 1,)), S,
             alpha, a(loss, f32, (1,)), a(counts, i32, (S, E)), a(mean_prob, f32, (S, E)))
     a.run(_lib.mok_balance_loss, *args, *a.scratch(ws), stream=stream)
 
@@ -361,13 +366,13 @@ def mok_balance_loss_backward(logits, counts, k: int, alpha: float, dloss, dlogi
     """Gradient of mok_balance_loss for the logits: dlogits [T, E] float32 (overwritten), with the
     forward's counts and the upstream gradient dloss [1] (both on the device)."""
     import torch
-    a = _Args("mok_balance_loss_backward")
+    a = _Args("mok_balance_loss_backward", logits)
     if logits.dim() != 2:
         a.bad()
     T, E = logits.shape
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
     f32, i32 = torch.float32, torch.int32
-    args = (a(logits, f32), a(counts, i32, (S, E)), T, E, k, a(seq_offsets, i32, (S + 1,)), S,
+    args = (a(logits, f32, (T, E)), a(counts, i32, (S, E)), T, E, k, a(seq_offsets, i32, (S + 1,)), S,
             alpha, a(dloss, f32, (1,)), a(dlogits, f32, (T, E)))
     a.run(_lib.mok_balance_loss_backward, *args, stream=stream)
 
@@ -378,12 +383,12 @@ def mok_rmsnorm(x, weight, eps: float, *, residual=None, h=None, rstd=None, y=No
     that are given: h, y [T, d], rstd [T] float32, y in MXFP8 as codes [T, d] and scales
     [T, d / 32] uint8."""
     import torch
-    a = _Args("mok_rmsnorm")
+    a = _Args("mok_rmsnorm", x)
     if x.dim() != 2:
         a.bad()
     (T, d), t, u8 = x.shape, x.dtype, torch.uint8
     io = _io_of(a, x)
-    args = (a(x, t), a(residual, t, (T, d)), a(weight, t, (d,)), T, d, io, eps, a(h, t, (T, d)),
+    args = (a(x, t, (T, d)), a(residual, t, (T, d)), a(weight, t, (d,)), T, d, io, eps, a(h, t, (T, d)),
             a(rstd, torch.float32, (T,)), a(y, t, (T, d)), a(codes, u8, (T, d)),
             a(scales, u8, (T, d // 32)))
     a.run(_lib.mok_rmsnorm, *args, stream=stream)
@@ -402,12 +407,12 @@ def mok_rmsnorm_backward(dy, h, rstd, weight, dx, dweight=None, ws=None, *, dh=N
     from the residual stream) and dweight [d] float32 (with ws of
     mok_rmsnorm_backward_workspace_bytes(T, d) bytes)."""
     import torch
-    a = _Args("mok_rmsnorm_backward")
+    a = _Args("mok_rmsnorm_backward", dy)
     if dy.dim() != 2:
         a.bad()
     (T, d), t, f32 = dy.shape, dy.dtype, torch.float32
     io = _io_of(a, dy)
-    args = (a(dy, t), a(h, t, (T, d)), a(rstd, f32, (T,)), a(weight, t, (d,)), a(dh, t, (T, d)),
+    args = (a(dy, t, (T, d)), a(h, t, (T, d)), a(rstd, f32, (T,)), a(weight, t, (d,)), a(dh, t, (T, d)),
             T, d, io, a(dx, t, (T, d)), a(dweight, f32, (d,)))
     a.run(_lib.mok_rmsnorm_backward, *args, *a.scratch(ws), stream=stream)
 
@@ -427,13 +432,13 @@ def mok_route_backward(x, w_router, topk_idx, topk_w, dtopk_w, dx=None, dw_route
     dw_router [E, d] float32 (with ws of mok_route_backward_workspace_bytes(T, d, E, x.dtype)
     bytes), from dtopk_w [T, k] and, where given, dlogits [T, E]."""
     import torch
-    a = _Args("mok_route_backward")
+    a = _Args("mok_route_backward", x)
     if x.dim() != 2 or w_router.dim() != 2 or topk_idx.dim() != 2:
         a.bad()
     (T, d), E, k = x.shape, w_router.shape[0], topk_idx.shape[1]
     t, f32 = x.dtype, torch.float32
     io = _io_of(a, x)
-    args = (a(x, t), a(w_router, t, (E, d)), a(topk_idx, torch.int32, (T, k)),
+    args = (a(x, t, (T, d)), a(w_router, t, (E, d)), a(topk_idx, torch.int32, (T, k)),
             a(topk_w, f32, (T, k)), a(dtopk_w, f32, (T, k)), a(dlogits, f32, (T, E)),
             a(dx_in, t, (T, d)), T, d, E, k, io, a(dx, t, (T, d)), a(dw_router, f32, (E, d)))
     a.run(_lib.mok_route_backward, *args, *a.scratch(ws), stream=stream)
@@ -452,7 +457,7 @@ def mok_mx_gemm(a_codes, a_scales, b_codes, b_scales, c, ws=None, *, stream=None
     mok_quantize_mxfp8 / mok_quantize_mxfp4 write them; the format of each operand is
     read from its shapes. ws: mok_mx_gemm_workspace_bytes(M, N, K) bytes."""
     import torch
-    a = _Args("mok_mx_gemm")
+    a = _Args("mok_mx_gemm", a_codes)
     if a_scales.dim() != 2 or b_scales.dim() != 2 or a_codes.dim() != 2 or b_codes.dim() != 2:
         a.bad()
     M, N, K, u8 = a_scales.shape[0], b_scales.shape[0], 32 * a_scales.shape[1], torch.uint8
@@ -471,7 +476,7 @@ def mok_mx_gemm(a_codes, a_scales, b_codes, b_scales, c, ws=None, *, stream=None
         out = MOK_FP32
     else:
         a.bad()
-    args = (a(a_codes, u8, (M, a_codes.shape[1])), a(a_scales, u8), fa,
+    args = (a(a_codes, u8, (M, a_codes.shape[1])), a(a_scales, u8, (M, K // 32)), fa,
             a(b_codes, u8, (N, b_codes.shape[1])), a(b_scales, u8, (N, K // 32)), fb, M, N, K, out,
             a(c, c.dtype, (M, N)))
     a.run(_lib.mok_mx_gemm, *args, *a.scratch(ws), stream=stream)

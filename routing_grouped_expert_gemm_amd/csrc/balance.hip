@@ -29,10 +29,13 @@ namespace {
 constexpr int BAL_NT = 256;                // threads of the row kernels: 4 waves
 constexpr int BAL_W = BAL_NT / 64;
 
-// Tokens of a chunk: at most 2048 chunks, so that the second launch's sums stay short, and at
-// least 16 tokens, a workgroup's rows in one step of the 16-lane form.
-int64_t bal_chunk(int64_t T) {
-  const int64_t c = (T + 2047) / 2048;
+// Tokens of a chunk: at most `most` chunks, and at least 16 tokens, a workgroup's rows in one step
+// of the 16-lane form. Forward: 1024 chunks, which all run at once and keep the second launch's
+// sums short (2048 took as long here, and 2 us more there: T 262,144, E 256). Backward, which has
+// nothing to join: 2048, 8 a CU.
+constexpr int kChunksFwd = 1024, kChunksBwd = 2048;
+int64_t bal_chunk(int64_t T, int most = kChunksFwd) {
+  const int64_t c = (T + most - 1) / most;
   return std::max<int64_t>(16, (c + 15) / 16 * 16);
 }
 int64_t bal_chunks(int64_t T) { return (T + bal_chunk(T) - 1) / bal_chunk(T); }
@@ -126,12 +129,17 @@ struct Row {
   }
 };
 
+// Loads in flight per lane: about 16 values (one row at a time left the reading launch at 3.2 TB/s:
+// T 262,144, E 256).
+constexpr int row_unroll(int values) { return values >= 16 ? 1 : values >= 8 ? 2 : 4; }
+
 template <int W, int L, int NC>
 __global__ __launch_bounds__(BAL_NT) void k_balance_rows(
     const float* __restrict__ logits, const int32_t* __restrict__ idx, int64_t T, int E, int k,
     const int32_t* __restrict__ off, int S, int64_t chunk, float* __restrict__ prob,
     int32_t* __restrict__ count, int32_t* __restrict__ ticket) {
   constexpr int R = 64 / L;                       // rows a wave holds
+  constexpr int U = row_unroll(NC * W);           // ... and loads before it uses the first
   __shared__ float sum_sh[BAL_W][NC * L * W];
   __shared__ int32_t hist[1024];
   const int lane = lane_id(), w = threadIdx.x >> 6, l = lane % L, r = lane / L;
@@ -149,15 +157,21 @@ __global__ __launch_bounds__(BAL_NT) void k_balance_rows(
       if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
     }
     float acc[NC][W] = {};
-    for (int64_t t0 = a + w * R; t0 < b; t0 += BAL_W * R) {
-      const int64_t t = t0 + r;
-      Row<W, L, NC> x;
-      x.load(logits + t * E, E, l, t < b);
-      x.softmax();
+    for (int64_t t0 = a + w * R; t0 < b; t0 += BAL_W * R * U) {
+      Row<W, L, NC> x[U];
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
+      for (int u = 0; u < U; ++u) {
+        const int64_t t = t0 + u * BAL_W * R + r;
+        x[u].load(logits + t * E, E, l, t < b);
+      }
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[n][i] += x.v[n][i];
+      for (int u = 0; u < U; ++u) {
+        x[u].softmax();
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int i = 0; i < W; ++i) acc[n][i] += x[u].v[n][i];
+      }
     }
 #pragma unroll
     for (int n = 0; n < NC; ++n)
@@ -180,55 +194,66 @@ __global__ __launch_bounds__(BAL_NT) void k_balance_rows(
   }
 }
 
-// Workgroup (x, s): 64 experts of sequence s, 16 waves over its chunks.
+// Workgroup (x, s): CW experts of sequence s, 1024 / CW groups over its chunks. Few sequences take
+// narrow workgroups, which share out the chunks; many take one workgroup each, since every
+// workgroup pays for the ticket.
+template <int CW>
 __global__ __launch_bounds__(1024) void k_balance_sum(
-    const float* __restrict__ prob, const int32_t* __restrict__ count, int64_t T, int E, int k,
-    const int32_t* __restrict__ off, int S, int64_t chunk, float alpha, double* terms,
+    const float* __restrict__ prob, const int32_t* __restrict__ count, int T, int E, int k,
+    const int32_t* __restrict__ off, int S, int chunk, float alpha, double* terms,
     int32_t* __restrict__ ticket, float* __restrict__ loss, int32_t* __restrict__ counts,
     float* __restrict__ mean_prob) {
-  __shared__ float psh[16][64];
-  __shared__ int32_t csh[16][64];
+  constexpr int G = 1024 / CW;
+  __shared__ float psh[G][CW];
+  __shared__ int32_t csh[G][CW];
+  __shared__ double tsh[CW / 64];
   __shared__ int last;
-  const int lane = lane_id(), g = threadIdx.x >> 6;
-  const int e = blockIdx.x * 64 + lane, s = blockIdx.y;
-  const int64_t a = seq_at(off, s, T), b = seq_at(off, s + 1, T);
+  const int tid = threadIdx.x, lane = lane_id(), col = tid % CW, g = tid / CW;
+  const int e = blockIdx.x * CW + col, s = blockIdx.y;
+  const int a = (int)seq_at(off, s, T), b = (int)seq_at(off, s + 1, T);
   float p = 0.0f;
   int32_t c = 0;
   if (a < b && e < E) {
-    for (int64_t ch = a / chunk + g; ch <= (b - 1) / chunk; ch += 16) {
-      p += prob[(ch + s) * E + e];
-      c += count[(ch + s) * E + e];
+    const int c1 = (b - 1) / chunk;
+#pragma unroll 4
+    for (int ch = a / chunk + g; ch <= c1; ch += G) {
+      p += prob[(int64_t)(ch + s) * E + e];
+      c += count[(int64_t)(ch + s) * E + e];
     }
   }
-  psh[g][lane] = p;
-  csh[g][lane] = c;
+  psh[g][col] = p;
+  csh[g][col] = c;
   __syncthreads();
-  if (g == 0) {
+  if (tid < CW) {
 #pragma unroll
-    for (int q = 1; q < 16; ++q) {
-      p += psh[q][lane];
-      c += csh[q][lane];
+    for (int q = 1; q < G; ++q) {
+      p += psh[q][col];
+      c += csh[q][col];
     }
     double term = 0.0;
     if (e < E) {
       const double n = (double)(b - a);
-      const float mean = a < b ? (float)(p / n) : 0.0f;
+      const double mean = a < b ? p / n : 0.0;
       counts[(int64_t)s * E + e] = c;
-      mean_prob[(int64_t)s * E + e] = mean;
-      if (a < b) term = (double)c * E / ((double)k * n) * (p / n);
+      mean_prob[(int64_t)s * E + e] = (float)mean;
+      if (a < b) term = (double)c * E / ((double)k * n) * mean;
     }
     for (int m = 1; m < 64; m <<= 1) term += __shfl_xor(term, m, kWave);
-    if (lane == 0) {
-      const int n_terms = gridDim.x * gridDim.y;
-      __hip_atomic_store(&terms[s * gridDim.x + blockIdx.x], term, __ATOMIC_RELAXED,
-                         __HIP_MEMORY_SCOPE_AGENT);
-      const int t = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-      last = t == n_terms - 1;
-    }
+    if (lane == 0) tsh[col / 64] = term;
   }
   __syncthreads();
-  if (last && g == 0) {             // every term is written: the loss, in a fixed order
-    const int n_terms = gridDim.x * gridDim.y;
+  const int n_terms = gridDim.x * gridDim.y;
+  if (tid == 0) {
+    double term = tsh[0];
+#pragma unroll
+    for (int q = 1; q < CW / 64; ++q) term += tsh[q];
+    __hip_atomic_store(&terms[s * gridDim.x + blockIdx.x], term, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+    const int t = __hip_atomic_fetch_add(ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    last = t == n_terms - 1;
+  }
+  __syncthreads();
+  if (last && tid < 64) {           // every term is written: the loss, in a fixed order
     double v = 0.0;
     for (int i = lane; i < n_terms; i += 64)
       v += __hip_atomic_load(&terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -381,8 +406,11 @@ int mok_balance_loss(const float* logits, const int32_t* topk_idx, int64_t T, in
              nullptr, logits, topk_idx, T, E, k, seq_offsets, n_seq, chunk, prob, count, ticket);
   });
   if (hipGetLastError() != hipSuccess) return MOK_EHIP;
-  launch_k(k_balance_sum, dim3((E + 63) / 64, n_seq), dim3(1024), 0, s, nullptr, nullptr, prob,
-           count, T, E, k, seq_offsets, n_seq, chunk, alpha, terms, ticket, loss, counts,
+  const bool few = (int64_t)n_seq * ((E + 63) / 64) <= 32;
+  const int cw = few || E <= 64 ? 64 : E <= 256 ? 256 : 1024;
+  auto sum = cw == 64 ? k_balance_sum<64> : cw == 256 ? k_balance_sum<256> : k_balance_sum<1024>;
+  launch_k(sum, dim3((E + cw - 1) / cw, n_seq), dim3(1024), 0, s, nullptr, nullptr, prob, count,
+           (int)T, E, k, seq_offsets, n_seq, (int)chunk, alpha, terms, ticket, loss, counts,
            mean_prob);
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EHIP;
 }
@@ -395,9 +423,9 @@ int mok_balance_loss_backward(const float* logits, const int32_t* counts, int64_
   if (T == 0) return MOK_OK;
   if (!logits || !counts || !dloss || !dlogits) return MOK_EINVAL;
   hipStream_t s = (hipStream_t)stream;
-  const int64_t chunk = bal_chunk(T);
+  const int64_t chunk = bal_chunk(T, kChunksBwd), n_chunks = (T + chunk - 1) / chunk;
   pick_row(E, bal_vec(E, logits) && bal_vec(E, dlogits), [&](auto W, auto L, auto NC) {
-    launch_k(k_balance_bwd<W(), L(), NC()>, dim3((unsigned)bal_chunks(T)), dim3(BAL_NT), 0, s,
+    launch_k(k_balance_bwd<W(), L(), NC()>, dim3((unsigned)n_chunks), dim3(BAL_NT), 0, s,
              nullptr, nullptr, logits, counts, T, E, k, seq_offsets, n_seq, chunk, alpha, dloss,
              dlogits);
   });

@@ -25,10 +25,13 @@ namespace {
 
 constexpr int NORM_NT = 256;
 
-template <class T> struct Piece;             // 8 consecutive values
+template <class T> struct Piece;             // 8 consecutive values; Raw: as they lie in memory
 template <> struct Piece<bf16_t> {
-  MOK_DEV static void load(const bf16_t* p, float (&v)[8]) {
-    const uint4 q = *(const uint4*)p;
+  typedef uint4 Raw;
+  MOK_DEV static Raw raw(const bf16_t* p) { return *(const uint4*)p; }
+  MOK_DEV static Raw none() { return make_uint4(0, 0, 0, 0); }
+  MOK_DEV static void load(const bf16_t* p, float (&v)[8]) { widen(raw(p), v); }
+  MOK_DEV static void widen(const Raw& q, float (&v)[8]) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -42,8 +45,12 @@ template <> struct Piece<bf16_t> {
   }
 };
 template <> struct Piece<float> {
-  MOK_DEV static void load(const float* p, float (&v)[8]) {
-    const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
+  struct Raw { float4 a, b; };
+  MOK_DEV static Raw raw(const float* p) { return {*(const float4*)p, *(const float4*)(p + 4)}; }
+  MOK_DEV static Raw none() { return {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)}; }
+  MOK_DEV static void load(const float* p, float (&v)[8]) { widen(raw(p), v); }
+  MOK_DEV static void widen(const Raw& q, float (&v)[8]) {
+    const float4 a = q.a, b = q.b;
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
@@ -202,12 +209,12 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_any(
 // Backward over rows blockIdx.x * RPB + ..., stepping by the whole grid: dweight's sums stay in
 // registers from row to row. part [gridDim.x, d]: this workgroup's share of dweight (NULL: none).
 template <class T, int TPR, int NC>
-__global__ __launch_bounds__(NORM_NT) void k_rmsnorm_bwd(
+__global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm_bwd(
     const T* dy, const T* __restrict__ h, const float* __restrict__ rstd,
     const T* __restrict__ weight, const T* dh, int64_t rows, int d, T* dx,
     float* __restrict__ part) {
-  constexpr int RPB = NORM_NT / TPR;
-  __shared__ float sh[2][NORM_NT / 64];
+  constexpr int NT = TPR > NORM_NT ? TPR : NORM_NT, RPB = NT / TPR;
+  __shared__ float sh[2][NT / 64];
   __shared__ float fold[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NC * 8 : 1];
   const int l = threadIdx.x % TPR, r = threadIdx.x / TPR;
   float w[NC][8], acc[NC][8];
@@ -218,22 +225,38 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_bwd(
     for (int i = 0; i < 8; ++i) w[n][i] = acc[n][i] = 0.0f;
     if (c < d) Piece<T>::load(weight + c, w[n]);
   }
-  int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
-    const int64_t row = r0 + r, at = row * d;
+  // The next row's loads are issued before this row's sum: a workgroup walks only a few rows, and
+  // a row's loads, sum and store in sequence left the memory idle in between.
+  typedef typename Piece<T>::Raw Raw;
+  Raw hq[NC], gq[NC], oq[NC];
+  auto fetch = [&](int64_t row) {
     const bool live = row < rows;
-    const float rs = live ? rstd[row] : 0.0f;
-    float n_[NC][8], g[NC][8], dot = 0.0f;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const int c = (n * TPR + l) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) n_[n][i] = g[n][i] = 0.0f;
-      if (live && c < d) {
-        Piece<T>::load(h + at + c, n_[n]);
-        Piece<T>::load(dy + at + c, g[n]);
-      }
+      const int64_t at = row * d + c;
+      const bool ok = live && c < d;
+      hq[n] = ok ? Piece<T>::raw(h + at) : Piece<T>::none();
+      gq[n] = ok ? Piece<T>::raw(dy + at) : Piece<T>::none();
+      oq[n] = ok && dh ? Piece<T>::raw(dh + at) : Piece<T>::none();
     }
+    return live ? rstd[row] : 0.0f;
+  };
+  int turn = 0;
+  const int64_t stride = (int64_t)gridDim.x * RPB;
+  float rs_next = fetch((int64_t)blockIdx.x * RPB + r);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += stride) {
+    const int64_t row = r0 + r, at = row * d;
+    const bool live = row < rows;
+    const float rs = rs_next;
+    float n_[NC][8], g[NC][8], o[NC][8], dot = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      Piece<T>::widen(hq[n], n_[n]);
+      Piece<T>::widen(gq[n], g[n]);
+      Piece<T>::widen(oq[n], o[n]);
+    }
+    rs_next = fetch(row + stride);
 #pragma unroll
     for (int n = 0; n < NC; ++n)
 #pragma unroll
@@ -249,11 +272,9 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_bwd(
     for (int n = 0; n < NC; ++n) {
       const int c = (n * TPR + l) * 8;
       if (live && c < d) {
-        float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (dh) Piece<T>::load(dh + at + c, o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += rs * (g[n][i] - n_[n][i] * dot);
-        Piece<T>::store(dx + at + c, o);
+        for (int i = 0; i < 8; ++i) o[n][i] += rs * (g[n][i] - n_[n][i] * dot);
+        Piece<T>::store(dx + at + c, o[n]);
       }
     }
   }
@@ -269,7 +290,7 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_bwd(
 #pragma unroll
     for (int n = 0; n < NC; ++n) Piece<float>::store(&fold[r][(n * TPR + l) * 8], acc[n]);
     __syncthreads();
-    for (int c = threadIdx.x; c < d; c += NORM_NT) {
+    for (int c = threadIdx.x; c < d; c += NT) {
       float v = fold[0][c];
 #pragma unroll
       for (int q = 1; q < RPB; ++q) v += fold[q][c];
@@ -363,6 +384,9 @@ hipError_t run_norm(const T* x, const T* res, const T* weight, int64_t rows, int
     launch_k(k_rmsnorm_any<T>, dim3((unsigned)rows), dim3(NORM_NT), 0, s, nullptr, nullptr, x, res,
              weight, rows, d, eps, h, rstd, y, codes, scales);
   else if (d <= 512) MOK_NORM(64, 1);
+  // few rows (fewer workgroups than CUs): more threads a row, for the row's latency
+  else if (rows <= 256 && d <= 2048) MOK_NORM(256, 1);
+  else if (rows <= 256 && d <= 8192) MOK_NORM(1024, 1);
   else if (d <= 1024) MOK_NORM(64, 2);
   else if (d <= 2048) MOK_NORM(64, 4);
   else if (d <= 4096) MOK_NORM(256, 2);
@@ -381,10 +405,10 @@ hipError_t run_bwd(const T* dy, const T* h, const float* rstd, const T* weight, 
   float* p = dweight ? part : nullptr;
   int n_part = rows > 0 ? blocks : 0;
   auto go = [&](auto TPR, auto NC) {
-    constexpr int rpb = NORM_NT / TPR();
+    constexpr int nt = TPR() > NORM_NT ? TPR() : NORM_NT, rpb = nt / TPR();
     const int grid = (int)std::min<int64_t>(dweight ? blocks : 1 << 16, (rows + rpb - 1) / rpb);
     n_part = grid;
-    launch_k(k_rmsnorm_bwd<T, TPR(), NC()>, dim3(grid), dim3(NORM_NT), 0, s, nullptr, nullptr, dy,
+    launch_k(k_rmsnorm_bwd<T, TPR(), NC()>, dim3(grid), dim3(nt), 0, s, nullptr, nullptr, dy,
              h, rstd, weight, dh, rows, d, dx, p);
   };
   auto c = [](auto v) { return v; };
@@ -401,9 +425,9 @@ hipError_t run_bwd(const T* dy, const T* h, const float* rstd, const T* weight, 
     }
   } else if (d <= 512) MOK_NORM(64, 1);
   else if (d <= 1024) MOK_NORM(64, 2);
-  else if (d <= 2048) MOK_NORM(64, 4);
+  else if (d <= 2048) MOK_NORM(256, 1);
   else if (d <= 4096) MOK_NORM(256, 2);
-  else MOK_NORM(256, 4);
+  else MOK_NORM(1024, 1);        // (256, 4) needs 256 registers: one wave a SIMD
 #undef MOK_NORM
   if (dweight)
     launch_k(k_column_sum, dim3((d + 15) / 16), dim3(1024), 0, s, nullptr, nullptr,

@@ -164,15 +164,33 @@ __global__ __launch_bounds__(256) void k_route_bwd_planes(const RbArgs a, int EP
       for (int n = 0; n < 8; ++n)
         if (e0 + n < a.E) v[n] = q[n];
     }
-    const float s = pick_dot(a, t);
-    for (int j = 0; j < a.k; ++j) {
-      const int e = a.idx[t * a.k + j];
-      const int n = e - e0;
-      if (e < a.E && n >= 0 && n < 8) {
-        const float g = a.tw[t * a.k + j] * (a.dtw[t * a.k + j] - s);
+    // the token's picks 8 at a time, so that their loads are in flight together
+    float s = 0.0f;
+    int32_t e[8];
+    float w[8], g[8];
+    auto fetch = [&](int j0) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const bool ok = j0 + q < a.k;
+        e[q] = ok ? a.idx[t * a.k + j0 + q] : -1;
+        w[q] = ok ? a.tw[t * a.k + j0 + q] : 0.0f;
+        g[q] = ok ? a.dtw[t * a.k + j0 + q] : 0.0f;
+      }
+    };
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      fetch(j0);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (e[q] >= 0 && e[q] < a.E) s += w[q] * g[q];
+    }
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+      if (a.k > 8) fetch(j0);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int n = e[q] - e0;
 #pragma unroll
         for (int m = 0; m < 8; ++m)
-          if (m == n) v[m] += g;
+          if (m == n && e[q] < a.E) v[m] += w[q] * (g[q] - s);
       }
     }
   }
@@ -227,20 +245,24 @@ MOK_DEV bf16x8_t frag_t(uint32_t tile, int blk, int s, int lane) {
 }
 
 // Both products in one launch, so that dx's streaming runs beside dW's matrix work. 256 threads.
-//  dW: EM experts x 128 columns over a range of tokens, K steps of KT tokens: three planes and x
+//  dW: EM experts x 128 columns over a range of tokens, K steps of 32 tokens: three planes and x
 //      through two LDS buffers by LDS-DMA.
-//  dx: 128 tokens x 128 columns, K steps of 64 experts: two planes (K-contiguous rows, chunk c of
-//      row r at slot c ^ (r >> 1 & 7)) and the weight's rows. The tile goes through LDS in float32,
-//      so that dx_in is read and dx written in whole row segments; dx_in is loaded before the
+//  dx: 128 tokens x 128 columns, K steps of 32 experts: two planes (K-contiguous rows of 64 bytes,
+//      chunk c of row r at slot c ^ (r >> 2 & 3)) and the weight's rows, two buffers (EM 64, where
+//      there are two steps) or three. The tile goes through LDS in float32, half of its rows at a
+//      time, so that dx_in is read and dx written in whole row segments; dx_in is loaded before the
 //      product.
+// Both keep to 48 KB (EM 64) or 72 KB (EM 128) of LDS: 3 or 2 workgroups a CU cover each other's
+// loads (256 experts a workgroup and steps of 64, 112 KB and one workgroup a CU, took 113 us at
+// T 4096, d 7168, E 256).
 template <int EM>
 __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
-  constexpr int KT = EM == 64 ? 64 : 32;
+  constexpr int KT = 32;
   constexpr int PB = KT * EM * 2, XB = KT * 256, WST = 3 * PB + XB;      // bytes of a dW step
-  constexpr int DST = 2 * 128 * 128 + 64 * 256;                         // bytes of a dx step
-  constexpr int DBUF = EM == 64 ? 1 : 2;                                // EP == 64: one step
+  constexpr int DST = 2 * 128 * 64 + 32 * 256;                          // bytes of a dx step
   constexpr int OLD = 132;                                              // floats of a staged row
-  constexpr int BYTES = std::max(std::max(2 * WST, DBUF * DST), 128 * OLD * 4);
+  constexpr int DN = EM == 64 ? 2 : 3;                                  // buffers of dx
+  constexpr int BYTES = std::max(std::max(2 * WST, DN * DST), 64 * OLD * 4);
   __shared__ __align__(1024) char lds[BYTES];
   const uint32_t lds0 = uniform(lds_addr(lds));
   const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
@@ -262,15 +284,13 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
              to + (wid * Q + q) * 1024);
   };
   if ((int)blockIdx.x < a.dw_blocks) {
-    constexpr int FE = EM == 64 ? 1 : EM == 128 ? 2 : 2, FC = EM == 64 ? 2 : EM == 128 ? 2 : 4;
+    constexpr int FE = EM / 64, FC = 2;          // waves: 2 x 2
     const int b = blockIdx.x, c0 = b % a.tiles_d * 128, rest = b / a.tiles_d;
     const int e0 = rest % a.tiles_e * EM;
     const int64_t range = rest / a.tiles_e, tb = range * a.t_range;
     const int64_t te = min(a.T, tb + a.t_range);
     const int nk = te > tb ? (int)((te - tb + KT - 1) / KT) : 0;
-    // waves: EM 256: 4 x 1 of 64 experts x 128 columns; else 2 x 2
-    const int we = EM == 256 ? wid * 64 : (wid >> 1) * 32 * FE;
-    const int wc = EM == 256 ? 0 : (wid & 1) * 32 * FC;
+    const int we = (wid >> 1) * 32 * FE, wc = (wid & 1) * 32 * FC;
     auto issue = [&](int kt) {
       const uint32_t to = lds0 + (kt & 1) * WST;
       const int64_t t0 = tb + (int64_t)kt * KT;
@@ -334,40 +354,45 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
     if (a.dx_in && t < a.T && c < a.d) in[i] = *(const uint4*)(a.dx_in + t * a.d + c);
   }
   const int wt = (wid >> 1) * 64, wc = (wid & 1) * 64;
-  const int nk = (a.E + 63) / 64;       // every step holds an expert
+  const int nk = (a.E + 31) / 32;       // every step holds an expert
   auto issue = [&](int kt) {
-    const uint32_t to = lds0 + (kt & (DBUF - 1)) * DST;
+    const uint32_t to = lds0 + kt % DN * DST;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = (wid * 4 + q) * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ ((r >> 1) & 7);
-        dma_b128(uniform_ptr(a.planes + ((int64_t)p * a.Tp + t0) * a.EP + kt * 64),
-                 (uint32_t)((r * a.EP + 8 * c) * 2), to + p * 16384 + (wid * 4 + q) * 1024);
+      for (int q = 0; q < 2; ++q) {
+        const int r = (wid * 2 + q) * 16 + (lane >> 2);
+        const int c = (lane & 3) ^ ((r >> 2) & 3);
+        dma_b128(uniform_ptr(a.planes + ((int64_t)p * a.Tp + t0) * a.EP + kt * 32),
+                 (uint32_t)((r * a.EP + 8 * c) * 2), to + p * 8192 + (wid * 2 + q) * 1024);
       }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      dma_t(std::integral_constant<int, 16>{}, 4, q, a.w + (int64_t)kt * 64 * a.d, a.d, c0, a.d,
-            min(63, a.E - 1 - kt * 64), to + 32768);
+    for (int q = 0; q < 2; ++q)
+      dma_t(std::integral_constant<int, 16>{}, 2, q, a.w + (int64_t)kt * 32 * a.d, a.d, c0, a.d,
+            min(31, a.E - 1 - kt * 32), to + 16384);
   };
   f32x16_t acc[2][2] = {};
-  issue(0);
+  for (int kt = 0; kt < DN - 1 && kt < nk; ++kt) issue(kt);
   for (int kt = 0; kt < nk; ++kt) {
-    publish();
-    if (kt + 1 < nk) issue(kt + 1);
-    const uint32_t at = lds0 + (kt & (DBUF - 1)) * DST;
+    if (DN == 3 && kt + 1 < nk) {       // the next step's 6 instructions may stay in flight
+      __builtin_amdgcn_s_waitcnt(6 | (7 << 4));
+      lds_barrier();
+    } else {
+      publish();
+    }
+    if (kt + DN - 1 < nk) issue(kt + DN - 1);
+    const uint32_t at = lds0 + kt % DN * DST;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 2; ++s) {
       bf16x8_t fw[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fw[j] = frag_t<16>(at + 32768, wc + 32 * j, s, lane);
+      for (int j = 0; j < 2; ++j) fw[j] = frag_t<16>(at + 16384, wc + 32 * j, s, lane);
 #pragma unroll
       for (int p = 1; p >= 0; --p)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = wt + 32 * i + l;
-          const int off = (int)(at - lds0) + p * 16384 + r * 128 + (((2 * s + h) ^ ((r >> 1) & 7)) << 4);
+          const int off = (int)(at - lds0) + p * 8192 + r * 64 + (((2 * s + h) ^ ((r >> 2) & 3)) << 4);
           const bf16x8_t fp = *(const bf16x8_t*)(lds + off);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
@@ -375,34 +400,40 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
         }
     }
   }
-  __syncthreads();
   float* st = (float*)lds;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int half = 0; half < 2; ++half) {
+    __syncthreads();                    // the operands, or the first half, have been read
+    if ((wid >> 1) == half) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(float4*)(st + (wt + 32 * i + l) * OLD + wc + 32 * j + 8 * q + 4 * h) =
-            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                        acc[i][j][4 * q + 3]);
-  __syncthreads();
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 16 + tid / 16;
-    const int64_t t = t0 + r;
-    const int c = c0 + tid % 16 * 8;
-    if (t >= a.T || c >= a.d) continue;
-    const float* q = st + r * OLD + tid % 16 * 8;
-    const float4 u = *(const float4*)q, v = *(const float4*)(q + 4);
-    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-    const float s[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    uint32_t o[4];
+          for (int q = 0; q < 4; ++q)
+            *(float4*)(st + (32 * i + l) * OLD + wc + 32 * j + 8 * q + 4 * h) =
+                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                            acc[i][j][4 * q + 3]);
+    }
+    __syncthreads();
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-      o[n] = pack_bf16x2(__uint_as_float(w[n] << 16) + s[2 * n],
-                         __uint_as_float(w[n] & 0xFFFF0000u) + s[2 * n + 1]);
-    *(uint4*)(a.dx + t * a.d + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 16 + tid / 16;
+      const int64_t t = t0 + half * 64 + r;
+      const int c = c0 + tid % 16 * 8;
+      if (t >= a.T || c >= a.d) continue;
+      const float* q = st + r * OLD + tid % 16 * 8;
+      const float4 u = *(const float4*)q, v = *(const float4*)(q + 4);
+      const uint4 z = in[half * 4 + i];
+      const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+      const float s[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        o[n] = pack_bf16x2(__uint_as_float(w[n] << 16) + s[2 * n],
+                           __uint_as_float(w[n] & 0xFFFF0000u) + s[2 * n + 1]);
+      *(uint4*)(a.dx + t * a.d + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
@@ -436,10 +467,10 @@ RbPlan rb_plan(int64_t T, int d, int E) {
   RbPlan p;
   p.EP = (int)cdiv(E, 64) * 64;
   if (p.EP > 64) p.EP = (int)cdiv(E, 128) * 128;
-  p.EM = p.EP == 64 ? 64 : p.EP % 256 ? 128 : 256;
+  p.EM = p.EP == 64 ? 64 : 128;
   p.Tp = cdiv(T, 128) * 128;
   const int64_t tiles = cdiv(d, 128) * (p.EP / p.EM);
-  const int64_t n = std::max<int64_t>(1, std::min(cdiv(256, tiles), cdiv(T, 256)));
+  const int64_t n = std::max<int64_t>(1, std::min(cdiv(384, tiles), cdiv(T, 256)));
   p.t_range = cdiv(cdiv(T, n), 64) * 64;
   p.ranges = cdiv(T, p.t_range);
   p.planes = (size_t)3 * p.Tp * p.EP * 2;
@@ -517,8 +548,7 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
     launch_k(k_route_bwd_planes, dim3((unsigned)n_pl), dim3(256), 0, s, nullptr, nullptr, a, p.EP,
              p.Tp, (bf16_t*)ws);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
-    auto k = p.EM == 64 ? k_route_bwd_tile<64> : p.EM == 128 ? k_route_bwd_tile<128>
-                                                           : k_route_bwd_tile<256>;
+    auto k = p.EM == 64 ? k_route_bwd_tile<64> : k_route_bwd_tile<128>;
     launch_k(k, dim3((unsigned)n), dim3(RB_NT), 0, s, nullptr, nullptr, t);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
     if (dw_router && p.ranges > 1)
