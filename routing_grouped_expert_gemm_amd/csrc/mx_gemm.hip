@@ -25,6 +25,7 @@
 namespace mok {
 namespace {
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int F8 = 0, F4 = 4;                     // the MFMA's operand format codes
 
 template <int F> constexpr int code_bytes(int n) { return F == F8 ? n : n / 2; }
@@ -181,23 +182,25 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
 }
 
 // ------------------------------------------------------------------------- LDS tiles
-// BM x BN tiles, 4 waves (2 x 2) of BM/2 x BN/2. K steps of KT values go to one of ST LDS buffers
+// BM x BN tiles, WM x WN waves of BM/WM x BN/WN: 2 x 2 (2 x 4 and 4 x 2, two waves a SIMD, were
+// within 2% at 256 x 256 and 10 to 20% slower at 128 x 128: they read the LDS more). K steps of KT values go to one of ST LDS buffers
 // by LDS-DMA (16-byte chunks; chunk c of row r at slot c ^ swz(r), so that the 16 rows that a
 // quarter of a wave reads at one chunk hit distinct banks). A step's last sub-step follows the
 // barrier that publishes the next step's buffer: its MFMAs cover the next step's first LDS reads,
 // and the DMA of the step ST steps on, into the buffer just read, is issued among them.
 // 128 x 128 tiles leave room for 4 buffers: their steps are shorter than a load's way from memory.
 // AL: K % 512 == 0, so that 16-byte pieces of the scale rows are aligned and also go by DMA.
-template <int FA_, int FB_, int BM_, int BN_, bool AL_>
+template <int FA_, int FB_, int BM_, int BN_, int WM_, int WN_, bool AL_>
 struct Tile {
+  static constexpr int WM = WM_, WN = WN_, NW = WM * WN;          // waves over rows and columns
   static constexpr int FA = FA_, FB = FB_, BM = BM_, BN = BN_;
   static constexpr bool AL = AL_;
   static constexpr int KT = FA == F4 && FB == F4 ? 256 : 128;
   static constexpr int ST = AL && BM == 128 ? 4 : 2;
   static constexpr int SUB = KT / 64;
-  static constexpr int FM = BM / 64, FN = BN / 64;
+  static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
   static constexpr int RBA = code_bytes<FA>(KT), RBB = code_bytes<FB>(KT);   // bytes of a row
-  static constexpr int QA = BM * RBA / 4096, QB = BN * RBB / 4096;   // DMA instructions a wave
+  static constexpr int QA = BM * RBA / 1024 / NW, QB = BN * RBB / 1024 / NW;   // DMA instructions a wave
 };
 
 template <int RB> MOK_DEV constexpr int swz(int r) {
@@ -205,18 +208,19 @@ template <int RB> MOK_DEV constexpr int swz(int r) {
 }
 
 template <class C>
-__global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
+__global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
   constexpr int FA = C::FA, FB = C::FB, FM = C::FM, FN = C::FN, SUB = C::SUB, KT = C::KT;
   constexpr int ST = C::ST;
   constexpr int A_B = C::BM * C::RBA, B_B = C::BN * C::RBB, S_B = (C::BM + C::BN) * 32;   // bytes
-  __shared__ __align__(1024) char lds[ST * (A_B + B_B) + 2 * S_B];
+  constexpr int OUT_B = C::NW * 32 * (C::BN / C::WN * 4 + 16);      // the epilogue's rows
+  __shared__ __align__(1024) char lds[std::max(ST * (A_B + B_B) + 2 * S_B, OUT_B)];
   char* const lds_b0 = lds + ST * A_B;
   char* const lds_s0 = lds_b0 + ST * B_B;
   auto buf_a = [&](int kt) { return (uint4*)(lds + kt % ST * A_B); };
   auto buf_b = [&](int kt) { return (uint4*)(lds_b0 + kt % ST * B_B); };
   auto buf_s = [&](int g) { return (uint32_t*)(lds_s0 + (g & 1) * S_B); };
   const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
-  const int wm = wid >> 1, wn = wid & 1, h = lane >> 5, r = lane & 31;
+  const int wm = wid / C::WN, wn = wid % C::WN, h = lane >> 5, r = lane & 31;
   // XCD x takes consecutive tiles, 8 M tiles deep, so that its L2 holds their operands
   const int tiles = p.tiles_m * p.tiles_n;
   const int per = (tiles + 7) / 8;
@@ -277,23 +281,23 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
   // against 126 without any scales.) 16-byte half x of row r lies at half x ^ (r >> 3 & 1), which
   // spreads a column of words over the banks. Pieces of the next group are loaded one a step, P
   // pieces from one step before the current group on (then over again: the same bytes), so that
-  // the last one is published with the step before that group's first. A piece is 64 rows of each
-  // operand, 16 bytes a lane: waves 0 and 1 load A's, 2 and 3 B's.
-  constexpr int SG = 32 / (KT / 32), P = C::BM / 64;
+  // the last one is published with the step before that group's first. A piece is 32 rows a
+  // wave, 16 bytes a lane: the first half of the waves loads A's, the second B's.
+  constexpr int SG = 32 / (KT / 32), SH = C::NW / 2, P = C::BM / (32 * SH);
   static_assert(C::BM == C::BN, "both operands' scales in the same number of pieces");
   const bool tiny = KB < 16;
-  const uint8_t* base_sc = uniform_ptr(wid < 2 ? p.as + (int64_t)m0 * KB : p.bs + (int64_t)n0 * KB);
-  const int sc_last = uniform(wid < 2 ? p.M - 1 - m0 : p.N - 1 - n0);      // the operand's last row
-  const int sc_r = (wid & 1) * 32 + lane / 2;                              // row in piece 0
-  auto sc_at = [&](int t) { return (uint32_t)min(t * 64 + sc_r, sc_last) * (uint32_t)KB; };
+  const uint8_t* base_sc = uniform_ptr(wid < SH ? p.as + (int64_t)m0 * KB : p.bs + (int64_t)n0 * KB);
+  const int sc_last = uniform(wid < SH ? p.M - 1 - m0 : p.N - 1 - n0);      // the operand's last row
+  const int sc_r = wid % SH * 32 + lane / 2;                               // row in piece 0
+  auto sc_at = [&](int t) { return (uint32_t)min(t * 32 * SH + sc_r, sc_last) * (uint32_t)KB; };
   const int sc_half = (lane ^ (sc_r >> 3)) & 1;       // the half of the row that slot lane & 1 holds
   const int sc_byte = step0 * (KT / 32) + 16 * sc_half;
-  const int sc_to = (wid >> 1) * C::BM + (wid & 1) * 32;                   // LDS row of piece 0
+  const int sc_to = wid / SH * C::BM + wid % SH * 32;                      // LDS row of piece 0
   // AL: past the row's end: its last 16 bytes
   auto sc_dma = [&](int g, int t) {
     __builtin_amdgcn_sched_barrier(0);
     dma_b128(base_sc, sc_at(t) + min(sc_byte + g * 32, KB - 16),
-             to_s + (g & 1) * S_B + (sc_to + t * 64) * 32);
+             to_s + (g & 1) * S_B + (sc_to + t * 32 * SH) * 32);
     __builtin_amdgcn_sched_barrier(0);
   };
   // else through registers: 16 bytes from the row's byte, or the row's last 16 where it ends
@@ -305,7 +309,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
     return v;
   };
   auto sc_put = [&](int g, int t, uint4 v) {
-    *(uint4*)&buf_s(g)[(sc_to + t * 64) * 8 + lane * 4] = v;
+    *(uint4*)&buf_s(g)[(sc_to + t * 32 * SH) * 8 + lane * 4] = v;
   };
   auto sc_store = [&](int g, int t, uint4 v) {
     const int early = max(sc_byte + g * 32 - (KB - 16), 0), by = early & 3, wd = early >> 2;
@@ -332,9 +336,9 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
     const uint32_t* S = buf_s(kt / SG);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) asc_n[i] = S[(wm * (C::BM / 2) + 32 * i + r) * 8 + w];
+    for (int i = 0; i < FM; ++i) asc_n[i] = S[(wm * (C::BM / C::WM) + 32 * i + r) * 8 + w];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) bsc_n[j] = S[(C::BM + wn * (C::BN / 2) + 32 * j + r) * 8 + w];
+    for (int j = 0; j < FN; ++j) bsc_n[j] = S[(C::BM + wn * (C::BN / C::WN) + 32 * j + r) * 8 + w];
     __builtin_amdgcn_sched_barrier(0);
   };
   auto take_scales = [&]() {
@@ -395,14 +399,14 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
     const uint4 *A = buf_a(kt), *B = buf_b(kt);
     auto a_at = [&](int i) {
       fa[f][i] = read(std::integral_constant<int, FA>{}, std::integral_constant<int, C::RBA>{}, A,
-                      wm * (C::BM / 2) + 32 * i + r, s);
+                      wm * (C::BM / C::WM) + 32 * i + r, s);
     };
     __builtin_amdgcn_sched_barrier(0);
     a_at(0);
 #pragma unroll
     for (int j = 0; j < FN; ++j)
       fb[f][j] = read(std::integral_constant<int, FB>{}, std::integral_constant<int, C::RBB>{}, B,
-                      wn * (C::BN / 2) + 32 * j + r, s);
+                      wn * (C::BN / C::WN) + 32 * j + r, s);
 #pragma unroll
     for (int i = 1; i < FM; ++i) a_at(i);
     __builtin_amdgcn_sched_barrier(0);
@@ -426,15 +430,24 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
     __builtin_amdgcn_sched_barrier(0);
   };
   // One K step. MORE: a step follows; LAST: it may be the last one; DMA: the loads of step kt + ST
-  // and one scale piece are issued here, and OUT vector-memory instructions may stay in flight at
-  // the barrier. No branches inside the main loop's form: the compiler moves MFMAs past them.
-  auto step = [&](int kt, auto MORE, auto LAST, auto DMA, auto OUT) {
+  // and one scale piece are issued here (LATE: also what the step before left of its loads), and
+  // OUT vector-memory instructions may stay in flight at the barrier. No branches inside the main
+  // loop's form: the compiler moves MFMAs past them.
+  // A step's loads are issued among the MFMAs of the last sub-step and, where the buffers give
+  // them the time to land, of the next step's first: NQ of them in one sub-step hold up its MFMAs.
+  constexpr bool SPREAD = SUB == 4 || ST > 2;
+  constexpr int H1 = SPREAD ? (NQ + 1) / 2 : NQ, H2 = NQ - H1;
+  auto step = [&](int kt, auto MORE, auto LAST, auto DMA, auto LATE, auto OUT) {
     const int sg = (kt + 1) / SG + 1, st = (kt + 1) % SG % P;    // the scale piece on its way
     uint4 sv;
     if constexpr (DMA() && !C::AL) sv = sc_load(sg, st);
     static_for<SUB - 1>([&](auto s) {
       mfmas(s, [&](int n) {
         if (n == NM / 2 - 1) frags(kt, s() + 1, (s() + 1) & 1);
+        if constexpr (LATE() && H2 > 0 && s() == 0) {
+#pragma unroll
+          for (int q = n * H2 / NM; q < (n + 1) * H2 / NM; ++q) issue(kt - 1 + ST, H1 + q);
+        }
       });
     });
     if constexpr (MORE()) publish(kt + 1, OUT, LAST);     // and all reads of step kt are back
@@ -448,7 +461,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
           if constexpr (C::AL) sc_dma(sg, st); else sc_store(sg, st, sv);
         }
 #pragma unroll
-        for (int q = n * NQ / NM; q < (n + 1) * NQ / NM; ++q) issue(kt + ST, q);
+        for (int q = n * H1 / NM; q < (n + 1) * H1 / NM; ++q) issue(kt + ST, q);
       }
     });
     if constexpr (MORE()) take_scales();
@@ -473,8 +486,11 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
   issue_all(0);
   if (nk >= ST) {
 #pragma unroll
-    for (int i = 1; i < ST; ++i) issue_all(i);
-    publish(0, std::integral_constant<int, (ST - 1) * NQ>{}, yes);
+    for (int i = 1; i < ST; ++i) {
+#pragma unroll
+      for (int q = 0; q < (i == ST - 1 ? H1 : NQ); ++q) issue(i, q);
+    }
+    publish(0, std::integral_constant<int, (ST - 1) * NQ - H2>{}, yes);
   } else {
     for (int i = 1; i < nk; ++i) issue_all(i);
     publish(0, none, yes);
@@ -484,9 +500,12 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
   frags(0, 0, 0);
   int kt = 0;
   for (; kt < nk - ST; ++kt)
-    step(kt, yes, no, yes, std::integral_constant<int, (ST - 2) * (NQ + 1)>{});
-  for (; kt < nk - 1; ++kt) step(kt, yes, yes, no, none);
-  step(kt, no, no, no, none);
+    step(kt, yes, no, yes, yes, std::integral_constant<int, (ST - 2) * (NQ + 1)>{});
+  if (nk >= ST) step(kt++, yes, yes, no, yes, none);
+  if constexpr (ST > 2) {
+    for (; kt < nk - 1; ++kt) step(kt, yes, yes, no, no, none);
+  }
+  if (kt < nk) step(kt, no, no, no, no, none);
 
   void* c = p.c;
   bool f32 = p.out_f32;
@@ -498,7 +517,7 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
     // Each wave puts its blocks of 32 rows through its own part of the operand buffers and writes
     // whole row segments, 16 bytes a lane (straight from the accumulators, 8 bytes a lane and 32
     // rows an instruction, the stores took 34 of 149 us at M 8192, N 4096, K 7168).
-    constexpr int WN = C::BN / 2;
+    constexpr int WN = C::BN / C::WN;
     char* mine = lds + wid * (32 * (WN * 4 + 16));
     __syncthreads();                              // every wave is past its last fragment reads
     // the lane made opaque again: what derives from it is computed here, not held over the K loop
@@ -521,13 +540,14 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
               *(uint2*)at = make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]),
                                        pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
           }
-        const int row0 = m0 + wm * (C::BM / 2) + 32 * i;
+        const int row0 = m0 + wm * (C::BM / C::WM) + 32 * i;
 #pragma unroll
         for (int x0 = 0; x0 < 32; x0 += at_once) {
           const int x = x0 + lane / seg;
-          const uint4 v = *(const uint4*)(mine + x * ld + piece * 16);
+          const u32x4_t v = *(const u32x4_t*)(mine + x * ld + piece * 16);
+          // non-temporal: C would push the operands out of the L2 (121 -> 116 us)
           if (row0 + x < p.M && col < p.N)
-            *(uint4*)((char*)c + ((int64_t)(row0 + x) * p.N + col) * es) = v;
+            __builtin_nontemporal_store(v, (u32x4_t*)((char*)c + ((int64_t)(row0 + x) * p.N + col) * es));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -541,8 +561,8 @@ __global__ __launch_bounds__(256) void k_mx_tile(const MxArgs p) {
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        store4(p, c, f32, m0 + wm * (C::BM / 2) + 32 * i + r,
-               n0 + wn * (C::BN / 2) + 32 * j + 8 * q + 4 * h,
+        store4(p, c, f32, m0 + wm * (C::BM / C::WM) + 32 * i + r,
+               n0 + wn * (C::BN / C::WN) + 32 * j + 8 * q + 4 * h,
                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                            acc[i][j][4 * q + 3]));
 }
@@ -593,7 +613,7 @@ hipError_t run_mx(MxArgs p, const Plan& t, float* part, void* c, hipStream_t s) 
   }
   p.tiles_m = (int)cdiv(p.M, t.tile);
   p.tiles_n = (int)cdiv(p.N, t.tile);
-  constexpr int KT = Tile<FA, FB, 128, 128, true>::KT;
+  constexpr int KT = Tile<FA, FB, 128, 128, 2, 2, true>::KT;
   const int64_t steps = cdiv(p.K, KT);
   p.steps_per_split = (int)cdiv(cdiv(steps, t.splits), 4) * 4;   // whole aligned scale pieces
   p.splits = (int)cdiv(steps, p.steps_per_split);       // every range has a step
@@ -601,11 +621,16 @@ hipError_t run_mx(MxArgs p, const Plan& t, float* part, void* c, hipStream_t s) 
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   const dim3 grid((unsigned)(8 * cdiv(tiles, 8)), 1, p.splits);
   const bool al = p.K % 512 == 0 && (uintptr_t)p.as % 16 == 0 && (uintptr_t)p.bs % 16 == 0;
-  auto k = t.tile == 256 ? (al ? k_mx_tile<Tile<FA, FB, 256, 256, true>>
-                               : k_mx_tile<Tile<FA, FB, 256, 256, false>>)
-                         : (al ? k_mx_tile<Tile<FA, FB, 128, 128, true>>
-                               : k_mx_tile<Tile<FA, FB, 128, 128, false>>);
-  launch_k(k, grid, dim3(256), 0, s, nullptr, nullptr, p);
+  auto go = [&](auto al_) {
+    typedef Tile<FA, FB, 256, 256, 2, 2, al_()> Big;
+    typedef Tile<FA, FB, 128, 128, 2, 2, al_()> Small;
+    if (t.tile == 256)
+      launch_k(k_mx_tile<Big>, grid, dim3(64 * Big::NW), 0, s, nullptr, nullptr, p);
+    else
+      launch_k(k_mx_tile<Small>, grid, dim3(64 * Small::NW), 0, s, nullptr, nullptr, p);
+  };
+  if (al) go(std::integral_constant<bool, true>{});
+  else go(std::integral_constant<bool, false>{});
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (p.splits > 1) {
     const int64_t elems = (int64_t)p.M * p.N;

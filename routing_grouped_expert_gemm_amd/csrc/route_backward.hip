@@ -42,14 +42,34 @@ struct RbArgs {
   int64_t t_range;    // tokens of one dW range (a multiple of RB_K)
 };
 
-// sum_i w[t,i] dw[t,i] over the token's picks inside [0, E), in pick order.
-MOK_DEV float pick_dot(const RbArgs& a, int64_t t) {
+// add(e, g) for each pick e of token t inside [0, E), in pick order, with its share of dl:
+// g = w (dw - sum_i w_i dw_i). The picks come 8 at a time, their loads in flight together.
+template <class Add>
+MOK_DEV void each_pick(const RbArgs& a, int64_t t, Add&& add) {
   float s = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int32_t e = a.idx[t * a.k + j];
-    if (e >= 0 && e < a.E) s += a.tw[t * a.k + j] * a.dtw[t * a.k + j];
+  int32_t e[8];
+  float w[8], g[8];
+  auto fetch = [&](int j0) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const bool ok = j0 + q < a.k;
+      e[q] = ok ? a.idx[t * a.k + j0 + q] : -1;
+      w[q] = ok ? a.tw[t * a.k + j0 + q] : 0.0f;
+      g[q] = ok ? a.dtw[t * a.k + j0 + q] : 0.0f;
+    }
+  };
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    fetch(j0);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (e[q] >= 0 && e[q] < a.E) s += w[q] * g[q];
   }
-  return s;
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    if (a.k > 8) fetch(j0);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (e[q] >= 0 && e[q] < a.E) add(e[q], w[q] * (g[q] - s));
+  }
 }
 
 // dl of tokens [t0, t0 + nt) and experts [e0, e0 + ne), zero past the tensors, at
@@ -64,15 +84,10 @@ MOK_DEV void build_dl(const RbArgs& a, int64_t t0, int nt, int e0, int ne, float
   }
   __syncthreads();
   if ((int)threadIdx.x < nt && t0 + threadIdx.x < a.T) {
-    const int64_t t = t0 + threadIdx.x;
-    const float s = pick_dot(a, t);
-    for (int j = 0; j < a.k; ++j) {          // in pick order: a repeated expert adds up
-      const int e = a.idx[t * a.k + j] - e0;
-      if (e >= 0 && e < ne && e0 + e < a.E) {
-        float* q = &buf[E_MAJOR ? e * ld + threadIdx.x : threadIdx.x * ld + e];
-        *q += a.tw[t * a.k + j] * (a.dtw[t * a.k + j] - s);
-      }
-    }
+    each_pick(a, t0 + threadIdx.x, [&](int e, float g) {     // a repeated expert adds up
+      e -= e0;
+      if (e >= 0 && e < ne) buf[E_MAJOR ? e * ld + threadIdx.x : threadIdx.x * ld + e] += g;
+    });
   }
   __syncthreads();
 }
@@ -164,35 +179,10 @@ __global__ __launch_bounds__(256) void k_route_bwd_planes(const RbArgs a, int EP
       for (int n = 0; n < 8; ++n)
         if (e0 + n < a.E) v[n] = q[n];
     }
-    // the token's picks 8 at a time, so that their loads are in flight together
-    float s = 0.0f;
-    int32_t e[8];
-    float w[8], g[8];
-    auto fetch = [&](int j0) {
+    each_pick(a, t, [&](int e, float g) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const bool ok = j0 + q < a.k;
-        e[q] = ok ? a.idx[t * a.k + j0 + q] : -1;
-        w[q] = ok ? a.tw[t * a.k + j0 + q] : 0.0f;
-        g[q] = ok ? a.dtw[t * a.k + j0 + q] : 0.0f;
-      }
-    };
-    for (int j0 = 0; j0 < a.k; j0 += 8) {
-      fetch(j0);
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (e[q] >= 0 && e[q] < a.E) s += w[q] * g[q];
-    }
-    for (int j0 = 0; j0 < a.k; j0 += 8) {
-      if (a.k > 8) fetch(j0);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int n = e[q] - e0;
-#pragma unroll
-        for (int m = 0; m < 8; ++m)
-          if (m == n && e[q] < a.E) v[m] += w[q] * (g[q] - s);
-      }
-    }
+      for (int m = 0; m < 8; ++m) v[m] += m == e - e0 ? g : 0.0f;
+    });
   }
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
