@@ -396,8 +396,8 @@ int mok_balance_loss_backward(const float* logits, const int32_t* counts, int64_
  *   rstd[t] = 1 / sqrt(mean_i h[t,i]^2 + eps),   y[t,i] = h[t,i] rstd[t] weight[i]
  * Outputs, each NULL where not wanted (one at least is): h [rows, d] and y [rows, d] in the
  * storage type, rstd [rows] float32, and y in MXFP8 (both or none): codes [rows, d] E4M3 and
- * scales [rows, d / 32] E8M0 in the layout and by the rules of mok_quantize_mxfp8_f32, from the
- * float32 y. A 32-value block of y with an infinity or a NaN is all NaN (codes 0x7F, scale 0xFF).
+ * scales [rows, d / 32] E8M0 in the layout and by the rules of mok_quantize_mxfp8_f32, from y
+ * rounded once to float32. A 32-value block of y with an infinity or a NaN is all NaN (codes 0x7F, scale 0xFF).
  * x, residual, weight [d]: float32 or bf16 (io_dtype). h may be x or residual, and y may be x or
  * residual where h is not the same one; other overlaps are not allowed. d >= 1, d % 32 == 0 with
  * codes, d <= 2^24; rows < 2^31; eps >= 0. Rows of d % 8 == 0, d <= 16384, with 16-byte aligned
@@ -445,7 +445,10 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
  * C[m,n] = sum_k A[m,k] B[n,k] of operands in the mok_quantize_mx* layouts: codes [rows, K]
  * (MXFP8) or [rows, K/2] (MXFP4), E8M0 scales [rows, K/32]; a_dtype and b_dtype are MOK_MXFP8 or
  * MOK_MXFP4, in any combination. c [M, N] bf16 or float32 (out_dtype: MOK_BF16, MOK_FP32), rounded
- * once from float32 sums. K % 32 == 0, 32 <= K <= 2^22; M, N >= 0, < 2^31 (and fewer than 2^23
+ * once from float32 sums. Products are exact but for operands in MXFP8: the matrix instruction adds
+ * a block's products on a grid 13 bits below the largest, which leaves 1.5e-5 of the result's norm
+ * for two MXFP8 operands, 5e-6 for one with bf16 results, and less than 1e-7 with float32 ones
+ * (which then take twice the instructions). K % 32 == 0, 32 <= K <= 2^22; M, N >= 0, < 2^31 (and fewer than 2^23
  * tiles). Codes and c start on 16 bytes. A scale of 0xFF (NaN) or a NaN code makes what it enters
  * NaN. ws: device scratch of mok_mx_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned (0 bytes:
  * may be NULL). Bit-identical reruns. */

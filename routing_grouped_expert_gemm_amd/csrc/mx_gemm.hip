@@ -70,6 +70,63 @@ MOK_DEV f32x16_t mfma(const Frag<FB>& b, const Frag<FA>& a, f32x16_t acc, uint32
                                                          (int)bsc, SEL, (int)asc);
 }
 
+// The instruction adds the products of a 32-value block on a grid 13 bits below its largest one
+// (measured: 256 + 2^-5 is exact, 256 + 2^-6 gives 256) and rounds to float32 after that. E2M1
+// products span 8 bits and are exact. An E4M3 operand's span 18 binades: with an E2M1 one the
+// result is off by 4.6e-6 of its norm, far below bf16's 2^-9, but not below float32's. For float32
+// results (X) the E4M3 operand is therefore split at 8 into two, large values and small, each
+// within the grid but for values below 2^-7 of their scale, and the products are two instructions.
+// (Two E4M3 operands span 36 binades: 1.5e-5 of the norm, in either output type.)
+MOK_DEV Frag<F8> large_of(const Frag<F8>& v) {
+  Frag<F8> o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4] = {v.q[i].x, v.q[i].y, v.q[i].z, v.q[i].w};
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      // per byte: all ones where the code without its sign is at least 0x50 (the value 8)
+      const uint32_t ge = (((w[n] & 0x7F7F7F7Fu) + 0x30303030u) >> 7) & 0x01010101u;
+      w[n] &= (ge << 8) - ge;
+    }
+    o.q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return o;
+}
+MOK_DEV Frag<F8> without(const Frag<F8>& v, const Frag<F8>& u) {
+  Frag<F8> o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    o.q[i] = make_uint4(v.q[i].x ^ u.q[i].x, v.q[i].y ^ u.q[i].y, v.q[i].z ^ u.q[i].z,
+                        v.q[i].w ^ u.q[i].w);
+  return o;
+}
+// The products of one a with N b's; after(j) follows the j-th.
+template <int FA, int FB, int SEL, bool X, int N, class After>
+MOK_DEV void mfma_row(const Frag<FB> (&b)[N], const Frag<FA>& a, f32x16_t (&acc)[N],
+                      const uint32_t (&bsc)[N], uint32_t asc, After&& after) {
+  if constexpr (X && FA == F8 && FB == F4) {
+    const Frag<F8> hi = large_of(a), lo = without(a, hi);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      acc[j] = mfma<FA, FB, SEL>(b[j], lo, acc[j], bsc[j], asc);
+      acc[j] = mfma<FA, FB, SEL>(b[j], hi, acc[j], bsc[j], asc);
+      after(j);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if constexpr (X && FA == F4 && FB == F8) {
+        const Frag<F8> hi = large_of(b[j]), lo = without(b[j], hi);
+        acc[j] = mfma<FA, FB, SEL>(lo, a, acc[j], bsc[j], asc);
+        acc[j] = mfma<FA, FB, SEL>(hi, a, acc[j], bsc[j], asc);
+      } else {
+        acc[j] = mfma<FA, FB, SEL>(b[j], a, acc[j], bsc[j], asc);
+      }
+      after(j);
+    }
+  }
+}
+
 // A 4-byte word at any address.
 MOK_DEV uint32_t load_word(const uint8_t* p) {
   uint32_t v;
@@ -110,7 +167,7 @@ MOK_DEV void store4(const MxArgs& p, void* c, bool f32, int m, int n, float4 v) 
 // order. B is read once over the grid.
 constexpr int KS = 8;
 
-template <int FA, int FB, int MT>
+template <int FA, int FB, int MT, bool X>
 __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
   __shared__ float4 red[KS][MT][4][64];
   const int lane = lane_id(), w = uniform(threadIdx.x >> 6), h = lane >> 5, r = lane & 31;
@@ -126,7 +183,7 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
     a[i] = p.a + ra * code_bytes<FA>(p.K);
     as[i] = p.as + ra * KB;
   }
-  f32x16_t acc[MT] = {};
+  f32x16_t acc[MT][1] = {};
   // this lane's part of the MFMA of blocks b0 + s and b0 + 4 + s
   auto frag = [&](auto f, const uint8_t* row, int b0, int s) {
     Frag<f()> v;
@@ -146,11 +203,11 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
   std::integral_constant<int, FA> fa;
   std::integral_constant<int, FB> fb;
   for (int b0 = 8 * w; b0 < KB; b0 += 8 * KS) {
-    Frag<FB> vb[4];
+    Frag<FB> vb[4][1];
     Frag<FA> va[MT][4];
-    uint32_t sb = scales_at(bs, b0 + 4 * h, KB), sa[MT];
+    uint32_t sb[1] = {scales_at(bs, b0 + 4 * h, KB)}, sa[MT];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) vb[s] = frag(fb, b, b0, s);
+    for (int s = 0; s < 4; ++s) vb[s][0] = frag(fb, b, b0, s);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       sa[i] = scales_at(as[i], b0 + 4 * h, KB);
@@ -159,15 +216,16 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
     }
     static_for<4>([&](auto s) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) acc[i] = mfma<FA, FB, s()>(vb[s()], va[i][s()], acc[i], sb, sa[i]);
+      for (int i = 0; i < MT; ++i)
+        mfma_row<FA, FB, s(), X>(vb[s()], va[i][s()], acc[i], sb, sa[i], [](int) {});
     });
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      red[w][i][q][lane] = make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2],
-                                       acc[i][4 * q + 3]);
+      red[w][i][q][lane] = make_float4(acc[i][0][4 * q], acc[i][0][4 * q + 1],
+                                       acc[i][0][4 * q + 2], acc[i][0][4 * q + 3]);
   __syncthreads();
   for (int t = threadIdx.x; t < 256 * MT; t += 64 * KS) {
     const int l = t & 63, q = (t >> 6) & 3, i = t >> 8;
@@ -190,11 +248,11 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
 // and the DMA of the step ST steps on, into the buffer just read, is issued among them.
 // 128 x 128 tiles leave room for 4 buffers: their steps are shorter than a load's way from memory.
 // AL: K % 512 == 0, so that 16-byte pieces of the scale rows are aligned and also go by DMA.
-template <int FA_, int FB_, int BM_, int BN_, int WM_, int WN_, bool AL_>
+template <int FA_, int FB_, int BM_, int BN_, int WM_, int WN_, bool AL_, bool X_>
 struct Tile {
   static constexpr int WM = WM_, WN = WN_, NW = WM * WN;          // waves over rows and columns
   static constexpr int FA = FA_, FB = FB_, BM = BM_, BN = BN_;
-  static constexpr bool AL = AL_;
+  static constexpr bool AL = AL_, X = X_;
   static constexpr int KT = FA == F4 && FB == F4 ? 256 : 128;
   static constexpr int ST = AL && BM == 128 ? 4 : 2;
   static constexpr int SUB = KT / 64;
@@ -422,11 +480,8 @@ __global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
     constexpr int SEL = KT == 256 ? s() : 2 * s(), F = s() & 1;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        acc[i][j] = mfma<FA, FB, SEL>(fb[F][j], fa[F][i], acc[i][j], bsc[j], asc[i]);
-        after(i * FN + j);
-      }
+      mfma_row<FA, FB, SEL, C::X>(fb[F], fa[F][i], acc[i], bsc, asc[i],
+                                  [&](int j) { after(i * FN + j); });
     __builtin_amdgcn_sched_barrier(0);
   };
   // One K step. MORE: a step follows; LAST: it may be the last one; DMA: the loads of step kt + ST
@@ -600,20 +655,17 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   return t;
 }
 
-template <int FA, int FB>
+template <int FA, int FB, bool X>
 hipError_t run_mx(MxArgs p, const Plan& t, float* part, void* c, hipStream_t s) {
   if (t.rows) {
     p.c = c;
-    const dim3 grid((unsigned)cdiv(p.N, 32), 1);
-    if (p.M <= 32)
-      launch_k(k_mx_rows<FA, FB, 1>, grid, dim3(64 * KS), 0, s, nullptr, nullptr, p);
-    else
-      launch_k(k_mx_rows<FA, FB, 2>, grid, dim3(64 * KS), 0, s, nullptr, nullptr, p);
+    auto k = p.M <= 32 ? k_mx_rows<FA, FB, 1, X> : k_mx_rows<FA, FB, 2, X>;
+    launch_k(k, dim3((unsigned)cdiv(p.N, 32)), dim3(64 * KS), 0, s, nullptr, nullptr, p);
     return hipGetLastError();
   }
   p.tiles_m = (int)cdiv(p.M, t.tile);
   p.tiles_n = (int)cdiv(p.N, t.tile);
-  constexpr int KT = Tile<FA, FB, 128, 128, 2, 2, true>::KT;
+  constexpr int KT = Tile<FA, FB, 128, 128, 2, 2, true, X>::KT;
   const int64_t steps = cdiv(p.K, KT);
   p.steps_per_split = (int)cdiv(cdiv(steps, t.splits), 4) * 4;   // whole aligned scale pieces
   p.splits = (int)cdiv(steps, p.steps_per_split);       // every range has a step
@@ -621,16 +673,11 @@ hipError_t run_mx(MxArgs p, const Plan& t, float* part, void* c, hipStream_t s) 
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   const dim3 grid((unsigned)(8 * cdiv(tiles, 8)), 1, p.splits);
   const bool al = p.K % 512 == 0 && (uintptr_t)p.as % 16 == 0 && (uintptr_t)p.bs % 16 == 0;
-  auto go = [&](auto al_) {
-    typedef Tile<FA, FB, 256, 256, 2, 2, al_()> Big;
-    typedef Tile<FA, FB, 128, 128, 2, 2, al_()> Small;
-    if (t.tile == 256)
-      launch_k(k_mx_tile<Big>, grid, dim3(64 * Big::NW), 0, s, nullptr, nullptr, p);
-    else
-      launch_k(k_mx_tile<Small>, grid, dim3(64 * Small::NW), 0, s, nullptr, nullptr, p);
-  };
-  if (al) go(std::integral_constant<bool, true>{});
-  else go(std::integral_constant<bool, false>{});
+  auto k = t.tile == 256 ? (al ? k_mx_tile<Tile<FA, FB, 256, 256, 2, 2, true, X>>
+                               : k_mx_tile<Tile<FA, FB, 256, 256, 2, 2, false, X>>)
+                         : (al ? k_mx_tile<Tile<FA, FB, 128, 128, 2, 2, true, X>>
+                               : k_mx_tile<Tile<FA, FB, 128, 128, 2, 2, false, X>>);
+  launch_k(k, grid, dim3(256), 0, s, nullptr, nullptr, p);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (p.splits > 1) {
     const int64_t elems = (int64_t)p.M * p.N;
@@ -686,10 +733,14 @@ int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype
   p.out_f32 = out_dtype == MOK_FP32;
   hipStream_t s = (hipStream_t)stream;
   hipError_t e;
-  if (a_dtype == MOK_MXFP4 && b_dtype == MOK_MXFP4) e = run_mx<F4, F4>(p, t, (float*)ws, c, s);
-  else if (a_dtype == MOK_MXFP8 && b_dtype == MOK_MXFP4) e = run_mx<F8, F4>(p, t, (float*)ws, c, s);
-  else if (a_dtype == MOK_MXFP4) e = run_mx<F4, F8>(p, t, (float*)ws, c, s);
-  else e = run_mx<F8, F8>(p, t, (float*)ws, c, s);
+  float* part = (float*)ws;
+  const bool f32 = p.out_f32;
+  if (a_dtype == MOK_MXFP4 && b_dtype == MOK_MXFP4) e = run_mx<F4, F4, false>(p, t, part, c, s);
+  else if (a_dtype == MOK_MXFP8 && b_dtype == MOK_MXFP8) e = run_mx<F8, F8, false>(p, t, part, c, s);
+  else if (a_dtype == MOK_MXFP8)
+    e = f32 ? run_mx<F8, F4, true>(p, t, part, c, s) : run_mx<F8, F4, false>(p, t, part, c, s);
+  else
+    e = f32 ? run_mx<F4, F8, true>(p, t, part, c, s) : run_mx<F4, F8, false>(p, t, part, c, s);
   return e == hipSuccess ? MOK_OK : MOK_EHIP;
 }
 

@@ -8,9 +8,10 @@
 //   dweight[i] = sum_t dy[t,i] n[t,i]
 //
 // The norm reads h as it is stored, so the backward, which is given the stored h, differentiates
-// exactly the function that the forward computed. Everything between the loads and the stores is
-// float32; each output is rounded once. MXFP8 codes come from the float32 y (not from a rounded
-// one), by the rules of mok_quantize_mxfp8_f32.
+// exactly the function that the forward computed. The sum of squares and rstd are float64 and y is
+// h w rstd rounded once to float32 (then to the output type): every value of a row hangs on rstd,
+// and codes next to a border of two would flip with its last bit. Gradients are float32, each
+// output rounded once. MXFP8 codes come from the float32 y, by the rules of mok_quantize_mxfp8_f32.
 //
 // HBM streams: a row stays in registers between its sum of squares and its output, so each input
 // is read once and each output written once. TPR threads hold a row in NC pieces of 8 values.
@@ -64,11 +65,24 @@ template <class T> MOK_DEV float as_stored(float v);     // v rounded to the sto
 template <> MOK_DEV float as_stored<float>(float v) { return v; }
 template <> MOK_DEV float as_stored<bf16_t>(float v) { return bf16_to_f32(f32_to_bf16(v)); }
 
+// h w rstd in float32, rstd = r + rl: the rounding errors of the products, by fma, added back. h w
+// is exact for bf16 operands. (Contracted, y + e would become fma(p, r, e) and count the error
+// twice.)
+template <class T>
+MOK_DEV float norm_value(float h, float w, float r, float rl) {
+#pragma clang fp contract(off)
+  const float p = h * w;
+  const float y = p * r;
+  float e = __builtin_fmaf(p, rl, __builtin_fmaf(p, r, -y));
+  if constexpr (sizeof(T) == 4) e = __builtin_fmaf(__builtin_fmaf(h, w, -p), r, e);
+  return fabsf(y) < INFINITY ? y + e : y;
+}
+
 // Sum over the row's TPR threads, the same value in each (xor order within a wave, then the
 // waves in ascending order). slot: LDS words of this call, one per wave; two calls in a row use
 // two slots, so one barrier each is enough.
-template <int TPR>
-MOK_DEV float row_total(float v, float* slot) {
+template <int TPR, class V>
+MOK_DEV V row_total(V v, V* slot) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, kWave);
   if constexpr (TPR > 64) {
@@ -108,13 +122,13 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm(
     T* h_out, float* __restrict__ rstd_out, T* y, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ scales) {
   constexpr int NT = TPR > NORM_NT ? TPR : NORM_NT, RPB = NT / TPR;
-  __shared__ float sh[NT / 64];
+  __shared__ double sh[NT / 64];
   const int l = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const bool live = row < rows;
   const int64_t at = row * d;
   float h[NC][8];
-  float ss = 0.0f;
+  double ss = 0.0;
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     const int c = (n * TPR + l) * 8;
@@ -135,10 +149,10 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm(
     const int c = (n * TPR + l) * 8;
     if (h_out && live && c < d) Piece<T>::store(h_out + at + c, h[n]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += h[n][i] * h[n][i];
+    for (int i = 0; i < 8; ++i) ss = fma((double)h[n][i], (double)h[n][i], ss);
   }
-  ss = row_total<TPR>(ss, sh);
-  const float rstd = 1.0f / sqrtf(ss / (float)d + eps);
+  const double rd = 1.0 / sqrt(row_total<TPR>(ss, sh) / d + eps);
+  const float rstd = (float)rd, rl = (float)(rd - rstd);
   if (rstd_out && live && l == 0) rstd_out[row] = rstd;
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
@@ -147,7 +161,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm(
     float w[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8];
     if (ok) Piece<T>::load(weight + c, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = h[n][i] * w[i] * rstd;   // bf16: h w is exact
+    for (int i = 0; i < 8; ++i) v[i] = norm_value<T>(h[n][i], w[i], rstd, rl);
     if (y && ok) Piece<T>::store(y + at + c, v);
     if (codes) {                   // d % 32 == 0: a quad's four lanes are all inside the row
       uint8_t s;
@@ -166,26 +180,25 @@ template <class T>
 __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_any(
     const T* x, const T* res, const T* weight, int64_t rows, int d, float eps, T* h_out,
     float* rstd_out, T* y, uint8_t* codes, uint8_t* scales) {
-  __shared__ float sh[NORM_NT / 64];
+  __shared__ double sh[NORM_NT / 64];
   const int64_t row = blockIdx.x, at = row * d;
   auto sum_at = [&](int i) {
     const float v = load_as_f32(x + at + i);
     return res ? as_stored<T>(v + load_as_f32(res + at + i)) : v;
   };
-  float ss = 0.0f;
+  double ss = 0.0;
   for (int i = threadIdx.x; i < d; i += NORM_NT) {
     const float v = sum_at(i);
     if (h_out) h_out[at + i] = f32_to<T>(v);
-    ss += v * v;
+    ss = fma((double)v, (double)v, ss);
   }
   ss = row_total<NORM_NT>(ss, sh);
   __syncthreads();                 // the row's h is written: other threads read it below
-  const float rstd = 1.0f / sqrtf(ss / (float)d + eps);
+  const double rd = 1.0 / sqrt(ss / d + eps);
+  const float rstd = (float)rd, rl = (float)(rd - rstd);
   if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
-  auto y_at = [&](int i) {
-    const float v = h_out ? load_as_f32(h_out + at + i) : sum_at(i);
-    return v * load_as_f32(weight + i) * rstd;
-  };
+  auto h_at = [&](int i) { return h_out ? load_as_f32(h_out + at + i) : sum_at(i); };
+  auto y_at = [&](int i) { return norm_value<T>(h_at(i), load_as_f32(weight + i), rstd, rl); };
   if (codes) {
     for (int b = threadIdx.x; b < d / 32; b += NORM_NT) {
       float amax = 0.0f;

@@ -101,6 +101,39 @@ def test_quantised_rows(M, N, K, fa, fb):
     assert np.array_equal(got, again)
 
 
+@pytest.mark.parametrize("fa,fb", [(8, 4), (4, 8)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 1024), (150, 300, 2048), (130, 70, 96), (3400, 3500, 512)])
+def test_float32_result_of_one_mxfp8_operand(M, N, K, fa, fb):
+    """Rows of normal values, float32 result. Each of the two instructions per block adds products
+    on a grid 13 bits below its largest. Large values (8 to 448): products of at least 8 * 2^-3 *
+    1/2 * 8 / 8 steps of 1/2, at most 448 * 6 < 2^12 and grid at most 2^(11 - 13): exact. Small
+    values (below 8): products below 48, grid at most 2^(5 - 13), so each of the 32 products of a
+    block loses less than 2^-8 of the block's scale; only values below 2^-4 of a scale have such
+    bits at all. Then K / 32 float32 sums: (K / 16 + 8) 2^-24 of sum |a b|."""
+    import routing_grouped_expert_gemm_amd as mok
+    g = torch.Generator().manual_seed(M + N + K + fa)
+    deq = {8: oracle.mxfp8_dequantize, 4: oracle.mxfp4_dequantize}
+    ops = []
+    for rows, f in ((M, fa), (N, fb)):
+        x = torch.randn(rows, K, generator=g).to(torch.bfloat16).to(DEV)
+        codes = torch.empty((rows, K if f == 8 else K // 2), dtype=torch.uint8, device=DEV)
+        sc = torch.empty((rows, K // 32), dtype=torch.uint8, device=DEV)
+        (mok.mok_quantize_mxfp8 if f == 8 else mok.mok_quantize_mxfp4)(x, codes, sc)
+        torch.cuda.synchronize()
+        ops.append((codes.cpu().numpy(), sc.cpu().numpy()))
+    (a, asc), (b, bsc) = ops
+    A = torch.from_numpy(deq[fa](a, asc).astype(np.float64)).to(DEV)
+    B = torch.from_numpy(deq[fb](b, bsc).astype(np.float64)).to(DEV)
+    sa, sb = (torch.from_numpy(2.0 ** (s.astype(np.float64) - 127)).to(DEV) for s in (asc, bsc))
+    ref, mag = (A @ B.T).cpu(), (A.abs() @ B.abs().T).cpu()
+    tol = (K / 16 + 8) * 2.0 ** -24 * mag + 32 * 2.0 ** -8 * (sa @ sb.T).cpu()
+    got = gemm(mok, a, asc, b, bsc).double()
+    assert ((got - ref).abs() <= tol).all()
+    # what the split is for: the norm of the error, 4.6e-6 of the result's with one instruction a
+    # block (the bound: float32 sums' random roundings, sqrt(K / 16) 2^-24, and as much again)
+    assert float((got - ref).norm() / ref.norm()) <= 4 * (K / 16 + 8) ** 0.5 * 2.0 ** -24
+
+
 @pytest.mark.parametrize("M", [2, 100])
 def test_scale_range(M):
     """Scales over the whole E8M0 range whose products stay normal float32 values."""
