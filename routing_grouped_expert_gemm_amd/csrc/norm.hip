@@ -176,23 +176,23 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm(
 
 // Any d and alignment: one workgroup a row, one value a thread and step (one 32-value block a
 // thread for the codes). The second pass reads back what the first stored in h_out.
-template <class T>
-__global__ __launch_bounds__(NORM_NT) void k_rmsnorm_any(
+template <class T, int NT>
+__global__ __launch_bounds__(NT) void k_rmsnorm_any(
     const T* x, const T* res, const T* weight, int64_t rows, int d, float eps, T* h_out,
     float* rstd_out, T* y, uint8_t* codes, uint8_t* scales) {
-  __shared__ double sh[NORM_NT / 64];
+  __shared__ double sh[NT / 64];
   const int64_t row = blockIdx.x, at = row * d;
   auto sum_at = [&](int i) {
     const float v = load_as_f32(x + at + i);
     return res ? as_stored<T>(v + load_as_f32(res + at + i)) : v;
   };
   double ss = 0.0;
-  for (int i = threadIdx.x; i < d; i += NORM_NT) {
+  for (int i = threadIdx.x; i < d; i += NT) {
     const float v = sum_at(i);
     if (h_out) h_out[at + i] = f32_to<T>(v);
     ss = fma((double)v, (double)v, ss);
   }
-  ss = row_total<NORM_NT>(ss, sh);
+  ss = row_total<NT>(ss, sh);
   __syncthreads();                 // the row's h is written: other threads read it below
   const double rd = 1.0 / sqrt(ss / d + eps);
   const float rstd = (float)rd, rl = (float)(rd - rstd);
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_any(
   auto h_at = [&](int i) { return h_out ? load_as_f32(h_out + at + i) : sum_at(i); };
   auto y_at = [&](int i) { return norm_value<T>(h_at(i), load_as_f32(weight + i), rstd, rl); };
   if (codes) {
-    for (int b = threadIdx.x; b < d / 32; b += NORM_NT) {
+    for (int b = threadIdx.x; b < d / 32; b += NT) {
       float amax = 0.0f;
       bool bad = false;
       for (int i = 0; i < 32; ++i) {
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_any(
     __syncthreads();               // y may be x: its first write follows the codes' last read
   }
   if (y)
-    for (int i = threadIdx.x; i < d; i += NORM_NT) y[at + i] = f32_to<T>(y_at(i));
+    for (int i = threadIdx.x; i < d; i += NT) y[at + i] = f32_to<T>(y_at(i));
 }
 
 // Backward over rows blockIdx.x * RPB + ..., stepping by the whole grid: dweight's sums stay in
@@ -326,18 +326,18 @@ __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_dw_any(const T* dy, const T
   part[(int64_t)blockIdx.y * d + c] = v;
 }
 
-template <class T>
-__global__ __launch_bounds__(NORM_NT) void k_rmsnorm_bwd_any(const T* dy, const T* h,
+template <class T, int NT>
+__global__ __launch_bounds__(NT) void k_rmsnorm_bwd_any(const T* dy, const T* h,
                                                              const float* rstd, const T* weight,
                                                              const T* dh, int d, T* dx) {
-  __shared__ float sh[NORM_NT / 64];
+  __shared__ float sh[NT / 64];
   const int64_t row = blockIdx.x, at = row * d;
   const float rs = rstd[row];
   float dot = 0.0f;
-  for (int i = threadIdx.x; i < d; i += NORM_NT)
+  for (int i = threadIdx.x; i < d; i += NT)
     dot += load_as_f32(dy + at + i) * load_as_f32(weight + i) * (load_as_f32(h + at + i) * rs);
-  dot = row_total<NORM_NT>(dot, sh) / (float)d;
-  for (int i = threadIdx.x; i < d; i += NORM_NT) {
+  dot = row_total<NT>(dot, sh) / (float)d;
+  for (int i = threadIdx.x; i < d; i += NT) {
     const float g = load_as_f32(dy + at + i) * load_as_f32(weight + i);
     const float o = rs * (g - load_as_f32(h + at + i) * rs * dot);
     dx[at + i] = f32_to<T>(o + (dh ? load_as_f32(dh + at + i) : 0.0f));
@@ -394,8 +394,9 @@ hipError_t run_norm(const T* x, const T* res, const T* weight, int64_t rows, int
   auto c = [](auto v) { return v; };
 #define MOK_NORM(TPR, NC) go(c(std::integral_constant<int, TPR>{}), c(std::integral_constant<int, NC>{}))
   if (!vec)
-    launch_k(k_rmsnorm_any<T>, dim3((unsigned)rows), dim3(NORM_NT), 0, s, nullptr, nullptr, x, res,
-             weight, rows, d, eps, h, rstd, y, codes, scales);
+    launch_k(d > 2048 ? k_rmsnorm_any<T, 1024> : k_rmsnorm_any<T, 256>, dim3((unsigned)rows),
+             dim3(d > 2048 ? 1024 : 256), 0, s, nullptr, nullptr, x, res, weight, rows, d, eps, h,
+             rstd, y, codes, scales);
   else if (d <= 512) MOK_NORM(64, 1);
   // few rows (fewer workgroups than CUs): more threads a row, for the row's latency
   else if (rows <= 256 && d <= 2048) MOK_NORM(256, 1);
@@ -433,8 +434,9 @@ hipError_t run_bwd(const T* dy, const T* h, const float* rstd, const T* weight, 
                nullptr, nullptr, dy, h, rstd, rows, d, p);
     for (int64_t r = 0; r < rows; r += kMaxLaunchRows) {
       const int64_t n = std::min(rows - r, kMaxLaunchRows), o = r * d;
-      launch_k(k_rmsnorm_bwd_any<T>, dim3((unsigned)n), dim3(NORM_NT), 0, s, nullptr, nullptr,
-               dy + o, h + o, rstd + r, weight, dh ? dh + o : dh, d, dx + o);
+      launch_k(d > 2048 ? k_rmsnorm_bwd_any<T, 1024> : k_rmsnorm_bwd_any<T, 256>, dim3((unsigned)n),
+               dim3(d > 2048 ? 1024 : 256), 0, s, nullptr, nullptr, dy + o, h + o, rstd + r, weight,
+               dh ? dh + o : dh, d, dx + o);
     }
   } else if (d <= 512) MOK_NORM(64, 1);
   else if (d <= 1024) MOK_NORM(64, 2);

@@ -9,9 +9,11 @@
 // fixed. dW's token sum is cut into ranges whose partial sums a last launch adds in order: no
 // atomics, the same bits every run. Two forms:
 //
-//  k_route_bwd_any  any type, size and alignment: 64 x 64 tiles of both products on the float32
-//    MFMA (operands and sums in float32), 4 waves of 32 x 32, K steps of 32 through LDS; a
-//    workgroup builds the part of dl it needs in LDS from the picks and the given dlogits.
+//  k_route_bwd_any  any type, size and alignment: 64 x 64 tiles of both products on the float32 MFMA
+//    (operands and sums in float32), 4 waves of 32 x 32, K steps of 32 through LDS, the next step's
+//    values loaded into registers under the MFMAs. dl is written once in float32 (DL), or, where
+//    T d E < 2^27, built by each workgroup in LDS from the given dlogits and the picks, which saves
+//    a launch (float32, T 257, d 272, E 20: 12 against 15 us; T 508, d 4864, E 182: 63 against 46).
 //  k_route_bwd_tile  bf16 rows of d % 8 == 0: dl is written once as three bf16 planes that sum to
 //    it (8 + 8 + 8 significant bits: 24, all of float32's), and both products run on the bf16
 //    MFMA with float32 sums: dW on all three planes, dx, which is rounded to 8 bits, on two.
@@ -32,10 +34,11 @@ struct RbArgs {
   const int32_t* idx;
   const float *tw, *dtw, *dlogits;
   const void* dx_in;
+  const float* dl;    // dl [Tp, EP], zero past T and E
   void* dx;
   float* dw;          // dW itself (one range) or its partial sums [ranges, E, d]
   int64_t T;
-  int d, E, k;
+  int d, E, k, EP;
   int tiles_d;        // tiles of 64 columns
   int64_t dx_tiles;   // workgroups of the dx product; the rest are dW's
   int tiles_e;
@@ -72,26 +75,6 @@ MOK_DEV void each_pick(const RbArgs& a, int64_t t, Add&& add) {
   }
 }
 
-// dl of tokens [t0, t0 + nt) and experts [e0, e0 + ne), zero past the tensors, at
-// buf[row * ld + column] (E_MAJOR: row = expert). nt <= RB_NT. Ends with a barrier.
-template <bool E_MAJOR>
-MOK_DEV void build_dl(const RbArgs& a, int64_t t0, int nt, int e0, int ne, float* buf, int ld) {
-  for (int i = threadIdx.x; i < nt * ne; i += RB_NT) {
-    const int e = i % ne, t = i / ne;
-    const bool ok = t0 + t < a.T && e0 + e < a.E;
-    buf[E_MAJOR ? e * ld + t : t * ld + e] =
-        ok && a.dlogits ? a.dlogits[(t0 + t) * a.E + e0 + e] : 0.0f;
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < nt && t0 + threadIdx.x < a.T) {
-    each_pick(a, t0 + threadIdx.x, [&](int e, float g) {     // a repeated expert adds up
-      e -= e0;
-      if (e >= 0 && e < ne) buf[E_MAJOR ? e * ld + threadIdx.x : threadIdx.x * ld + e] += g;
-    });
-  }
-  __syncthreads();
-}
-
 // acc += A^T B over one K step: A and B lie as [RB_K][RB_TILE + pad] in LDS, the wave's block is
 // rows am .. am + 32 of A and columns bn .. bn + 32 of B.
 MOK_DEV void mma_step(const float* A, const float* B, int am, int bn, f32x16_t& acc) {
@@ -105,7 +88,7 @@ MOK_DEV void mma_step(const float* A, const float* B, int am, int bn, f32x16_t& 
 }
 
 // One 64 x 64 tile of dx or of a range of dW per workgroup.
-template <class T>
+template <class T, bool DL>
 __global__ __launch_bounds__(RB_NT) void k_route_bwd_any(const RbArgs a) {
   __shared__ float A[RB_K * (RB_TILE + RB_PAD)], B[RB_K * (RB_TILE + RB_PAD)];
   constexpr int LD = RB_TILE + RB_PAD;
@@ -116,22 +99,53 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_any(const RbArgs a) {
   const int c0 = (int)(b % a.tiles_d) * RB_TILE;
   const int64_t rest = b / a.tiles_d;
   f32x16_t acc = {};
-  // rows of B: T or E rows of `src` [.., d] from row k0, columns c0 ..
-  auto load_b = [&](const T* src, int64_t k0, int64_t rows) {
-    for (int i = threadIdx.x; i < RB_K * RB_TILE; i += RB_NT) {
-      const int c = i % RB_TILE, r = i / RB_TILE;
-      B[r * LD + c] = k0 + r < rows && c0 + c < a.d ? load_as_f32(src + (k0 + r) * a.d + c0 + c)
-                                                    : 0.0f;
+  constexpr int N = RB_K * RB_TILE / RB_NT;       // values of an operand a thread holds
+  float ra[N], rb[N];
+  // dx: A row = expert k0 + e, column = token; dW: A row = token k0 + t, column = expert
+  const int64_t t0 = rest * RB_TILE;              // dx: first token
+  const int e0 = (int)(rest % a.tiles_e) * RB_TILE;               // dW: first expert
+  const int64_t range = rest / a.tiles_e;                         // dW: range of tokens
+  const int64_t k_begin = is_dx ? 0 : range * a.t_range;
+  const int64_t k_end = is_dx ? a.E : min(a.T, k_begin + a.t_range);
+  const T* const src = (const T*)(is_dx ? a.w : a.x);             // B rows: experts or tokens
+  auto load = [&](int64_t k0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * RB_NT;
+      const int64_t t = is_dx ? t0 + i / RB_K : k0 + i / RB_TILE;
+      const int e = is_dx ? (int)k0 + i % RB_K : e0 + i % RB_TILE;
+      if constexpr (DL) ra[n] = a.dl[t * a.EP + e];
+      else ra[n] = a.dlogits && t < a.T && e < a.E ? a.dlogits[t * a.E + e] : 0.0f;
+      const int c = c0 + i % RB_TILE;
+      const int64_t r = k0 + i / RB_TILE;
+      rb[n] = r < k_end && c < a.d ? load_as_f32(src + r * a.d + c) : 0.0f;
     }
   };
-  if (is_dx) {
-    const int64_t t0 = rest * RB_TILE;
-    for (int e0 = 0; e0 < a.E; e0 += RB_K) {
-      load_b((const T*)a.w, e0, a.E);
-      build_dl<true>(a, t0, RB_TILE, e0, RB_K, A, LD);
-      mma_step(A, B, am, bn, acc);
+  if (k_begin < k_end) load(k_begin);
+  for (int64_t k0 = k_begin; k0 < k_end; k0 += RB_K) {
+    __syncthreads();                              // every wave is past the previous step's reads
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = threadIdx.x + n * RB_NT;
+      A[is_dx ? i % RB_K * LD + i / RB_K : i / RB_TILE * LD + i % RB_TILE] = ra[n];
+      B[i / RB_TILE * LD + i % RB_TILE] = rb[n];
+    }
+    __syncthreads();
+    if constexpr (!DL) {                          // the picks' share: a thread a token
+      const int64_t t = (is_dx ? t0 : k0) + threadIdx.x;
+      if (threadIdx.x < (is_dx ? RB_TILE : RB_K) && t < a.T) {
+        const int eb = is_dx ? (int)k0 : e0, ne = is_dx ? RB_K : RB_TILE;
+        each_pick(a, t, [&](int e, float g) {     // a repeated expert adds up
+          e -= eb;
+          if (e >= 0 && e < ne) A[is_dx ? e * LD + threadIdx.x : threadIdx.x * LD + e] += g;
+        });
+      }
       __syncthreads();
     }
+    if (k0 + RB_K < k_end) load(k0 + RB_K);
+    mma_step(A, B, am, bn, acc);
+  }
+  if (is_dx) {
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
       const int64_t t = t0 + am + 8 * (v >> 2) + 4 * h + (v & 3);
@@ -143,15 +157,6 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_any(const RbArgs a) {
       }
     }
   } else {
-    const int e0 = (int)(rest % a.tiles_e) * RB_TILE;
-    const int64_t range = rest / a.tiles_e;
-    const int64_t t_end = min(a.T, (range + 1) * a.t_range);
-    for (int64_t t0 = range * a.t_range; t0 < t_end; t0 += RB_K) {
-      load_b((const T*)a.x, t0, a.T);
-      build_dl<false>(a, t0, RB_K, e0, RB_TILE, A, LD);
-      mma_step(A, B, am, bn, acc);
-      __syncthreads();
-    }
     float* out = a.dw + range * a.E * a.d;
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
@@ -162,10 +167,12 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_any(const RbArgs a) {
 }
 
 // ------------------------------------------------------------------------- bf16 planes
-// dl as bf16 planes P0 + P1 + P2 [3][Tp][EP], zero past T tokens and E experts: each plane is the
-// rounding of what the ones before leave, so the sum holds 24 bits. 8 experts a thread.
-__global__ __launch_bounds__(256) void k_route_bwd_planes(const RbArgs a, int EP, int64_t Tp,
-                                                          bf16_t* __restrict__ planes) {
+// dl [Tp][EP], zero past T tokens and E experts, 8 experts a thread: in float32, or (PLANES) as bf16
+// planes P0 + P1 + P2 [3][Tp][EP], each the rounding of what the ones before leave, so that the sum
+// holds 24 bits.
+template <bool PLANES>
+__global__ __launch_bounds__(256) void k_route_bwd_dl(const RbArgs a, int EP, int64_t Tp,
+                                                      void* __restrict__ out) {
   const int per = EP / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t t = i / per;
@@ -184,6 +191,12 @@ __global__ __launch_bounds__(256) void k_route_bwd_planes(const RbArgs a, int EP
       for (int m = 0; m < 8; ++m) v[m] += m == e - e0 ? g : 0.0f;
     });
   }
+  if constexpr (!PLANES) {
+    float* q = (float*)out + t * EP + e0;
+    *(float4*)q = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4*)(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
 #pragma unroll
   for (int p = 0; p < 3; ++p) {
     uint32_t w[4];
@@ -194,7 +207,7 @@ __global__ __launch_bounds__(256) void k_route_bwd_planes(const RbArgs a, int EP
       v[2 * n] = fabsf(lo) == INFINITY ? 0.0f : v[2 * n] - lo;     // an infinity stays one
       v[2 * n + 1] = fabsf(hi) == INFINITY ? 0.0f : v[2 * n + 1] - hi;
     }
-    *(uint4*)(planes + ((int64_t)p * Tp + t) * EP + e0) = make_uint4(w[0], w[1], w[2], w[3]);
+    *(uint4*)((bf16_t*)out + ((int64_t)p * Tp + t) * EP + e0) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -441,10 +454,26 @@ __global__ __launch_bounds__(256) void k_route_bwd_sum(const float* __restrict__
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Token ranges of dW: as many as give about two workgroups a CU, each of at least 64 tokens.
-int64_t any_ranges(int64_t T, int d, int E) {
+// The any-size form's shapes: dl (if written) padded to whole tiles; dW's token ranges, as many as
+// give about two workgroups a CU, each of at least 64 tokens.
+struct RbAny {
+  bool write_dl;
+  int EP;
+  int64_t Tp, ranges, t_range;
+  size_t dl, total;                   // bytes; the partial sums follow dl
+};
+RbAny rb_any(int64_t T, int d, int E) {
+  RbAny p;
+  p.EP = (int)cdiv(E, RB_TILE) * RB_TILE;
+  p.Tp = cdiv(T, RB_TILE) * RB_TILE;
   const int64_t tiles = cdiv(d, RB_TILE) * cdiv(E, RB_TILE);
-  return std::max<int64_t>(1, std::min(cdiv(512, tiles), cdiv(T, 64)));
+  const int64_t n = std::max<int64_t>(1, std::min(cdiv(512, tiles), cdiv(T, 64)));
+  p.t_range = std::max<int64_t>(1, cdiv(cdiv(T, n), RB_K)) * RB_K;
+  p.ranges = std::max<int64_t>(1, cdiv(T, p.t_range));
+  p.write_dl = (double)T * d * E >= (double)(1 << 27);
+  p.dl = p.write_dl ? (size_t)p.Tp * p.EP * sizeof(float) : 0;
+  p.total = std::max<size_t>(256, p.dl + (p.ranges > 1 ? (size_t)p.ranges * E * d * sizeof(float) : 0));
+  return p;
 }
 
 // The plane form's shapes: experts padded to the tile EM, tokens to dx's tiles, dW's ranges.
@@ -484,8 +513,7 @@ extern "C" {
 int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t io_dtype,
                                        size_t* bytes) {
   if (!bytes || rb_check(T, d, E, 1, io_dtype) != MOK_OK) return MOK_EINVAL;
-  const int64_t n = any_ranges(T, d, E);
-  size_t need = n > 1 ? (size_t)n * E * d * sizeof(float) : 256;
+  size_t need = rb_any(T, d, E).total;
   if (io_dtype == MOK_BF16 && T > 0) {
     const RbPlan p = rb_plan(T, d, E);
     need = std::max(need, p.planes + (p.ranges > 1 ? (size_t)p.ranges * E * d * sizeof(float) : 0));
@@ -516,7 +544,7 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
                (const float*)ws, 0, elems, dw_router);
     return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EHIP;
   }
-  RbArgs a;
+  RbArgs a = {};
   a.x = x; a.w = w_router; a.idx = topk_idx; a.tw = topk_w; a.dtw = dtopk_w; a.dlogits = dlogits;
   a.dx_in = dx_in; a.dx = dx; a.T = T; a.d = d; a.E = E; a.k = k;
   auto al16 = [](const void* p) { return (uintptr_t)p % 16 == 0; };
@@ -535,8 +563,8 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
     const int64_t n = n_dw + (dx ? p.Tp / 128 * t.tiles_d : 0), n_pl = cdiv(p.Tp * (p.EP / 8), 256);
     if (n * RB_NT >= (int64_t)1 << 32 || n_pl * 256 >= (int64_t)1 << 32) return MOK_EUNSUPPORTED;
     t.dw_blocks = (int)n_dw;
-    launch_k(k_route_bwd_planes, dim3((unsigned)n_pl), dim3(256), 0, s, nullptr, nullptr, a, p.EP,
-             p.Tp, (bf16_t*)ws);
+    launch_k(k_route_bwd_dl<true>, dim3((unsigned)n_pl), dim3(256), 0, s, nullptr, nullptr, a, p.EP,
+             p.Tp, ws);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
     auto k = p.EM == 64 ? k_route_bwd_tile<64> : k_route_bwd_tile<128>;
     launch_k(k, dim3((unsigned)n), dim3(RB_NT), 0, s, nullptr, nullptr, t);
@@ -546,22 +574,31 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
                (const float*)t.dw, (int)p.ranges, elems, dw_router);
     return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EHIP;
   }
+  const RbAny p = rb_any(T, d, E);
+  a.dl = (const float*)ws;
+  a.EP = p.EP;
   a.tiles_d = (int)cdiv(d, RB_TILE);
-  a.tiles_e = (int)cdiv(E, RB_TILE);
-  a.dx_tiles = dx ? cdiv(T, RB_TILE) * a.tiles_d : 0;
-  const int64_t ranges = dw_router ? any_ranges(T, d, E) : 0;
-  a.t_range = ranges ? cdiv(cdiv(T, ranges), RB_K) * RB_K : RB_K;
-  a.dw = ranges > 1 ? (float*)ws : dw_router;
-  const int64_t grid = a.dx_tiles + ranges * a.tiles_e * a.tiles_d;
-  if (grid * RB_NT >= (int64_t)1 << 32) return MOK_EUNSUPPORTED;
-  if (io_dtype == MOK_BF16)
-    launch_k(k_route_bwd_any<bf16_t>, dim3((unsigned)grid), dim3(RB_NT), 0, s, nullptr, nullptr, a);
-  else
-    launch_k(k_route_bwd_any<float>, dim3((unsigned)grid), dim3(RB_NT), 0, s, nullptr, nullptr, a);
+  a.tiles_e = p.EP / RB_TILE;
+  a.dx_tiles = dx ? p.Tp / RB_TILE * a.tiles_d : 0;
+  a.t_range = p.t_range;
+  float* const part = (float*)((char*)ws + p.dl);
+  a.dw = p.ranges > 1 ? part : dw_router;
+  const int64_t grid = a.dx_tiles + (dw_router ? p.ranges * a.tiles_e * a.tiles_d : 0);
+  const int64_t n_dl = cdiv(p.Tp * (p.EP / 8), 256);
+  if (grid * RB_NT >= (int64_t)1 << 32 || n_dl * 256 >= (int64_t)1 << 32) return MOK_EUNSUPPORTED;
+  if (p.write_dl) {
+    launch_k(k_route_bwd_dl<false>, dim3((unsigned)n_dl), dim3(256), 0, s, nullptr, nullptr, a,
+             p.EP, p.Tp, ws);
+    if (hipGetLastError() != hipSuccess) return MOK_EHIP;
+  }
+  const bool bf = io_dtype == MOK_BF16;
+  auto kern = p.write_dl ? (bf ? k_route_bwd_any<bf16_t, true> : k_route_bwd_any<float, true>)
+                         : (bf ? k_route_bwd_any<bf16_t, false> : k_route_bwd_any<float, false>);
+  launch_k(kern, dim3((unsigned)grid), dim3(RB_NT), 0, s, nullptr, nullptr, a);
   if (hipGetLastError() != hipSuccess) return MOK_EHIP;
-  if (ranges > 1)
-    launch_k(k_route_bwd_sum, dim3(sum_grid), dim3(256), 0, s, nullptr, nullptr, (const float*)ws,
-             (int)ranges, elems, dw_router);
+  if (dw_router && p.ranges > 1)
+    launch_k(k_route_bwd_sum, dim3(sum_grid), dim3(256), 0, s, nullptr, nullptr, (const float*)part,
+             (int)p.ranges, elems, dw_router);
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EHIP;
 }
 

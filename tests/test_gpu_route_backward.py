@@ -74,7 +74,7 @@ CASES = [  # T, d, E, k
     (1, 1, 1, 1), (1, 64, 8, 2), (3, 17, 5, 5), (45, 144, 16, 4), (257, 272, 20, 4), (64, 128, 64, 6),
     (100, 100, 63, 3), (130, 192, 65, 8), (33, 256, 96, 8), (300, 448, 130, 8), (70, 512, 256, 8),
     (129, 320, 384, 8), (31, 64, 1000, 16), (20, 128, 1024, 64), (1000, 2048, 64, 6),
-    (2100, 64, 16, 2), (5000, 40, 8, 2), (512, 2056, 64, 6), (515, 1984, 32, 4)]
+    (2100, 64, 16, 2), (5000, 40, 8, 2), (512, 2056, 64, 6), (515, 1984, 32, 4), (700, 1999, 130, 8), (40, 30001, 128, 4)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
