@@ -401,7 +401,7 @@ int mok_balance_loss_backward(const float* logits, const int32_t* counts, int64_
  * x, residual, weight [d]: float32 or bf16 (io_dtype). h may be x or residual, and y may be x or
  * residual where h is not the same one; other overlaps are not allowed. d >= 1, d % 32 == 0 with
  * codes, d <= 2^24; rows < 2^31; eps >= 0. Rows of d % 8 == 0, d <= 16384, with 16-byte aligned
- * pointers are read once; others take a slower form.
+ * pointers are read once (backward: d <= 8192); others take a slower form.
  *
  * Backward, g = dy weight, n = h rstd:
  *   dx[t,i] = rstd[t] (g[t,i] - n[t,i] mean_j(g[t,j] n[t,j])) + dh[t,i]
@@ -431,7 +431,8 @@ int mok_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const
  * may be NULL where not wanted. Picks outside [0, E) take no part; an expert named twice adds up.
  * dx may be dx_in, and overlaps nothing else. Sums in float32 (bf16 operands enter as they are,
  * dl with at least 16 significant bits for dx and 24 for dw_router); each output is rounded once;
- * no atomics: bit-identical reruns. Sizes as mok_route, d <= 2^24, T k < 2^31.
+ * no atomics: bit-identical reruns. Every token's row of x and every dtopk_w entry is read; infinite
+ * or NaN values in them (or in w_router) make what they enter NaN. Sizes as mok_route, d <= 2^24, T k < 2^31.
  * ws: device scratch of mok_route_backward_workspace_bytes(...) bytes, 16-byte aligned. */
 int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t io_dtype,
                                        size_t* bytes);
@@ -449,7 +450,7 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
  * a block's products on a grid 13 bits below the largest, which leaves 1.5e-5 of the result's norm
  * for two MXFP8 operands, 5e-6 for one with bf16 results, and less than 1e-7 with float32 ones
  * (which then take twice the instructions). K % 32 == 0, 32 <= K <= 2^22; M, N >= 0, < 2^31 (and fewer than 2^23
- * tiles). Codes and c start on 16 bytes. A scale of 0xFF (NaN) or a NaN code makes what it enters
+ * tiles of 128 x 128; up to 64 rows: N <= 2^27). Codes and c start on 16 bytes. A scale of 0xFF (NaN) or a NaN code makes what it enters
  * NaN. ws: device scratch of mok_mx_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned (0 bytes:
  * may be NULL). Bit-identical reruns. */
 int mok_mx_gemm_workspace_bytes(int64_t M, int64_t N, int32_t K, size_t* bytes);

@@ -351,7 +351,8 @@ def mok_balance_loss(logits, topk_idx, alpha: float, loss, counts, mean_prob, ws
     (None: one sequence). ws: mok_balance_loss_workspace_bytes(T, E, S) bytes."""
     import torch
     a = _Args("mok_balance_loss", logits)
-    if logits.dim() != 2 or topk_idx.dim() != 2:
+    if logits.dim() != 2 or topk_idx.dim() != 2 or (seq_offsets is not None
+                                                    and seq_offsets.dim() != 1):
         a.bad()
     (T, E), k = logits.shape, topk_idx.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
@@ -367,7 +368,7 @@ def mok_balance_loss_backward(logits, counts, k: int, alpha: float, dloss, dlogi
     forward's counts and the upstream gradient dloss [1] (both on the device)."""
     import torch
     a = _Args("mok_balance_loss_backward", logits)
-    if logits.dim() != 2:
+    if logits.dim() != 2 or (seq_offsets is not None and seq_offsets.dim() != 1):
         a.bad()
     T, E = logits.shape
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1

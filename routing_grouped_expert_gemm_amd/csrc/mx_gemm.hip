@@ -729,7 +729,8 @@ int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype
   if ((uintptr_t)a_codes % 16 || (uintptr_t)b_codes % 16 || (uintptr_t)c % 16) return MOK_EINVAL;
   const Plan t = plan_of(M, N, K);
   // a launch counts its threads in 32 bits
-  if (cdiv(M, t.tile) * cdiv(N, t.tile) >= (int64_t)1 << 23) return MOK_EUNSUPPORTED;
+  const int64_t threads = t.rows ? cdiv(N, 32) * 64 * KS : cdiv(M, t.tile) * cdiv(N, t.tile) * 256;
+  if (threads >= (int64_t)1 << 31) return MOK_EUNSUPPORTED;
   size_t need = 0;
   mok_mx_gemm_workspace_bytes(M, N, K, &need);
   if (need && (!ws || ws_bytes < need || (uintptr_t)ws % 16)) return MOK_EWORKSPACE;

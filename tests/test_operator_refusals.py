@@ -102,6 +102,7 @@ def test_mx_gemm(lib):
     for kw in (dict(ws=None), dict(ws_bytes=64), dict(ws=24)):
         refuse(lib.mok_mx_gemm, b, EWORKSPACE, **kw)
     refuse(lib.mok_mx_gemm, b, EUNSUPPORTED, M=(1 << 31) - 1, N=(1 << 31) - 1)
+    refuse(lib.mok_mx_gemm, b, EUNSUPPORTED, M=1, N=1 << 28)
     refuse(lib.mok_mx_gemm, b, OK, M=0, a=None, c=None)
 
 
