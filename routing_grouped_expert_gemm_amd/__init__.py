@@ -288,52 +288,47 @@ def mok_get_device_error(workspace, stream=None) -> int:
 # another device than the first raises MokError (MOK_EINVAL) before anything is enqueued. The work
 # goes to the tensors' own device: its current stream, or `stream`, which must belong to it.
 
-class _Args:
-    """Checks the tensors of one call, all on the GPU of the first."""
-    __slots__ = ("fn", "dev")
+def _refuse(fn: str):
+    raise MokError(fn, MOK_EINVAL)
 
-    def __init__(self, fn: str, first):
-        self.fn, self.dev = fn, first.get_device()
-        if self.dev < 0:
-            self.bad()
 
-    def bad(self):
-        raise MokError(self.fn, MOK_EINVAL)
-
-    def __call__(self, t, dtype, shape):
-        """Pointer of t: contiguous, on the call's GPU, of this dtype and shape (None: none)."""
-        if t is None:
-            return None
-        if (t.dtype is not dtype or t.shape != shape or t.get_device() != self.dev
-                or not t.is_contiguous()):
-            self.bad()
+def _arg(fn: str, t, dtype, shape, dev: int):
+    """Pointer of t (None: NULL): contiguous, of this dtype and shape, on GPU dev."""
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev >= 0
+            and t.is_contiguous()):
         return t.data_ptr()
-
-    def scratch(self, ws):
-        """(pointer, bytes) of a workspace tensor of any dtype."""
-        if ws is None:
-            return None, 0
-        if ws.get_device() != self.dev or not ws.is_contiguous():
-            self.bad()
-        return ws.data_ptr(), ws.numel() * ws.element_size()
-
-    def run(self, f, *args, stream=None):
-        import torch
-        if self.dev == torch.cuda.current_device():
-            status = f(*args, _stream(stream, self.dev))
-        else:
-            with torch.cuda.device(self.dev):
-                status = f(*args, _stream(stream, self.dev))
-        if status != MOK_OK:
-            raise MokError(self.fn, status)
+    _refuse(fn)
 
 
-def _io_of(a: _Args, t) -> int:
+def _scratch(fn: str, ws, dev: int):
+    """(pointer, bytes) of a workspace tensor of any dtype."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(fn)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _enqueue(fn: str, dev: int, f, args, stream) -> None:
+    """f(*args, stream) with GPU dev current."""
+    import torch
+    if torch.cuda.current_device() == dev:
+        status = f(*args, _stream(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, _stream(stream, dev))
+    if status != MOK_OK:
+        raise MokError(fn, status)
+
+
+def _io_of(fn: str, t) -> int:
     import torch
     if t.dtype is torch.bfloat16:
         return MOK_BF16
     if t.dtype is not torch.float32:
-        a.bad()
+        _refuse(fn)
     return MOK_FP32
 
 
@@ -350,16 +345,17 @@ def mok_balance_loss(logits, topk_idx, alpha: float, loss, counts, mean_prob, ws
     and mean probabilities [S, E] float32 of the S packed sequences of seq_offsets [S + 1] int32
     (None: one sequence). ws: mok_balance_loss_workspace_bytes(T, E, S) bytes."""
     import torch
-    a = _Args("mok_balance_loss", logits)
+    fn, f32, i32 = "mok_balance_loss", torch.float32, torch.int32
     if logits.dim() != 2 or topk_idx.dim() != 2 or (seq_offsets is not None
                                                     and seq_offsets.dim() != 1):
-        a.bad()
-    (T, E), k = logits.shape, topk_idx.shape[1]
+        _refuse(fn)
+    (T, E), k, dev = logits.shape, topk_idx.shape[1], logits.get_device()
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
-    f32, i32 = torch.float32, torch.int32
-    args = (a(logits, f32, (T, E)), a(topk_idx, i32, (T, k)), T, E, k, a(seq_offsets, i32, (S + 1,)), S,
-            alpha, a(loss, f32, (1,)), a(counts, i32, (S, E)), a(mean_prob, f32, (S, E)))
-    a.run(_lib.mok_balance_loss, *args, *a.scratch(ws), stream=stream)
+    _enqueue(fn, dev, _lib.mok_balance_loss,
+             (_arg(fn, logits, f32, (T, E), dev), _arg(fn, topk_idx, i32, (T, k), dev), T, E, k,
+              _arg(fn, seq_offsets, i32, (S + 1,), dev), S, alpha, _arg(fn, loss, f32, (1,), dev),
+              _arg(fn, counts, i32, (S, E), dev), _arg(fn, mean_prob, f32, (S, E), dev),
+              *_scratch(fn, ws, dev)), stream)
 
 
 def mok_balance_loss_backward(logits, counts, k: int, alpha: float, dloss, dlogits, *,
@@ -367,15 +363,15 @@ def mok_balance_loss_backward(logits, counts, k: int, alpha: float, dloss, dlogi
     """Gradient of mok_balance_loss for the logits: dlogits [T, E] float32 (overwritten), with the
     forward's counts and the upstream gradient dloss [1] (both on the device)."""
     import torch
-    a = _Args("mok_balance_loss_backward", logits)
+    fn, f32, i32 = "mok_balance_loss_backward", torch.float32, torch.int32
     if logits.dim() != 2 or (seq_offsets is not None and seq_offsets.dim() != 1):
-        a.bad()
-    T, E = logits.shape
+        _refuse(fn)
+    (T, E), dev = logits.shape, logits.get_device()
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
-    f32, i32 = torch.float32, torch.int32
-    args = (a(logits, f32, (T, E)), a(counts, i32, (S, E)), T, E, k, a(seq_offsets, i32, (S + 1,)), S,
-            alpha, a(dloss, f32, (1,)), a(dlogits, f32, (T, E)))
-    a.run(_lib.mok_balance_loss_backward, *args, stream=stream)
+    _enqueue(fn, dev, _lib.mok_balance_loss_backward,
+             (_arg(fn, logits, f32, (T, E), dev), _arg(fn, counts, i32, (S, E), dev), T, E, k,
+              _arg(fn, seq_offsets, i32, (S + 1,), dev), S, alpha, _arg(fn, dloss, f32, (1,), dev),
+              _arg(fn, dlogits, f32, (T, E), dev)), stream)
 
 
 def mok_rmsnorm(x, weight, eps: float, *, residual=None, h=None, rstd=None, y=None, codes=None,
@@ -384,15 +380,16 @@ def mok_rmsnorm(x, weight, eps: float, *, residual=None, h=None, rstd=None, y=No
     that are given: h, y [T, d], rstd [T] float32, y in MXFP8 as codes [T, d] and scales
     [T, d / 32] uint8."""
     import torch
-    a = _Args("mok_rmsnorm", x)
+    fn, u8 = "mok_rmsnorm", torch.uint8
     if x.dim() != 2:
-        a.bad()
-    (T, d), t, u8 = x.shape, x.dtype, torch.uint8
-    io = _io_of(a, x)
-    args = (a(x, t, (T, d)), a(residual, t, (T, d)), a(weight, t, (d,)), T, d, io, eps, a(h, t, (T, d)),
-            a(rstd, torch.float32, (T,)), a(y, t, (T, d)), a(codes, u8, (T, d)),
-            a(scales, u8, (T, d // 32)))
-    a.run(_lib.mok_rmsnorm, *args, stream=stream)
+        _refuse(fn)
+    (T, d), t, dev, io = x.shape, x.dtype, x.get_device(), _io_of(fn, x)
+    rows = (T, d)
+    _enqueue(fn, dev, _lib.mok_rmsnorm,
+             (_arg(fn, x, t, rows, dev), _arg(fn, residual, t, rows, dev),
+              _arg(fn, weight, t, (d,), dev), T, d, io, eps, _arg(fn, h, t, rows, dev),
+              _arg(fn, rstd, torch.float32, (T,), dev), _arg(fn, y, t, rows, dev),
+              _arg(fn, codes, u8, rows, dev), _arg(fn, scales, u8, (T, d // 32), dev)), stream)
 
 
 def mok_rmsnorm_backward_workspace_bytes(T: int, d: int) -> int:
@@ -408,14 +405,16 @@ def mok_rmsnorm_backward(dy, h, rstd, weight, dx, dweight=None, ws=None, *, dh=N
     from the residual stream) and dweight [d] float32 (with ws of
     mok_rmsnorm_backward_workspace_bytes(T, d) bytes)."""
     import torch
-    a = _Args("mok_rmsnorm_backward", dy)
+    fn, f32 = "mok_rmsnorm_backward", torch.float32
     if dy.dim() != 2:
-        a.bad()
-    (T, d), t, f32 = dy.shape, dy.dtype, torch.float32
-    io = _io_of(a, dy)
-    args = (a(dy, t, (T, d)), a(h, t, (T, d)), a(rstd, f32, (T,)), a(weight, t, (d,)), a(dh, t, (T, d)),
-            T, d, io, a(dx, t, (T, d)), a(dweight, f32, (d,)))
-    a.run(_lib.mok_rmsnorm_backward, *args, *a.scratch(ws), stream=stream)
+        _refuse(fn)
+    (T, d), t, dev, io = dy.shape, dy.dtype, dy.get_device(), _io_of(fn, dy)
+    rows = (T, d)
+    _enqueue(fn, dev, _lib.mok_rmsnorm_backward,
+             (_arg(fn, dy, t, rows, dev), _arg(fn, h, t, rows, dev), _arg(fn, rstd, f32, (T,), dev),
+              _arg(fn, weight, t, (d,), dev), _arg(fn, dh, t, rows, dev), T, d, io,
+              _arg(fn, dx, t, rows, dev), _arg(fn, dweight, f32, (d,), dev),
+              *_scratch(fn, ws, dev)), stream)
 
 
 def mok_route_backward_workspace_bytes(T: int, d: int, E: int, dtype) -> int:
@@ -433,16 +432,17 @@ def mok_route_backward(x, w_router, topk_idx, topk_w, dtopk_w, dx=None, dw_route
     dw_router [E, d] float32 (with ws of mok_route_backward_workspace_bytes(T, d, E, x.dtype)
     bytes), from dtopk_w [T, k] and, where given, dlogits [T, E]."""
     import torch
-    a = _Args("mok_route_backward", x)
+    fn, f32 = "mok_route_backward", torch.float32
     if x.dim() != 2 or w_router.dim() != 2 or topk_idx.dim() != 2:
-        a.bad()
+        _refuse(fn)
     (T, d), E, k = x.shape, w_router.shape[0], topk_idx.shape[1]
-    t, f32 = x.dtype, torch.float32
-    io = _io_of(a, x)
-    args = (a(x, t, (T, d)), a(w_router, t, (E, d)), a(topk_idx, torch.int32, (T, k)),
-            a(topk_w, f32, (T, k)), a(dtopk_w, f32, (T, k)), a(dlogits, f32, (T, E)),
-            a(dx_in, t, (T, d)), T, d, E, k, io, a(dx, t, (T, d)), a(dw_router, f32, (E, d)))
-    a.run(_lib.mok_route_backward, *args, *a.scratch(ws), stream=stream)
+    t, dev, io = x.dtype, x.get_device(), _io_of(fn, x)
+    _enqueue(fn, dev, _lib.mok_route_backward,
+             (_arg(fn, x, t, (T, d), dev), _arg(fn, w_router, t, (E, d), dev),
+              _arg(fn, topk_idx, torch.int32, (T, k), dev), _arg(fn, topk_w, f32, (T, k), dev),
+              _arg(fn, dtopk_w, f32, (T, k), dev), _arg(fn, dlogits, f32, (T, E), dev),
+              _arg(fn, dx_in, t, (T, d), dev), T, d, E, k, io, _arg(fn, dx, t, (T, d), dev),
+              _arg(fn, dw_router, f32, (E, d), dev), *_scratch(fn, ws, dev)), stream)
 
 
 def mok_mx_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -458,29 +458,19 @@ def mok_mx_gemm(a_codes, a_scales, b_codes, b_scales, c, ws=None, *, stream=None
     mok_quantize_mxfp8 / mok_quantize_mxfp4 write them; the format of each operand is
     read from its shapes. ws: mok_mx_gemm_workspace_bytes(M, N, K) bytes."""
     import torch
-    a = _Args("mok_mx_gemm", a_codes)
+    fn, u8 = "mok_mx_gemm", torch.uint8
     if a_scales.dim() != 2 or b_scales.dim() != 2 or a_codes.dim() != 2 or b_codes.dim() != 2:
-        a.bad()
-    M, N, K, u8 = a_scales.shape[0], b_scales.shape[0], 32 * a_scales.shape[1], torch.uint8
-
-    def fmt(codes):
-        if codes.shape[1] == K:
-            return MOK_MXFP8
-        if 2 * codes.shape[1] != K:
-            a.bad()
-        return MOK_MXFP4
-
-    fa, fb = fmt(a_codes), fmt(b_codes)
-    if c.dtype is torch.bfloat16:
-        out = MOK_BF16
-    elif c.dtype is torch.float32:
-        out = MOK_FP32
-    else:
-        a.bad()
-    args = (a(a_codes, u8, (M, a_codes.shape[1])), a(a_scales, u8, (M, K // 32)), fa,
-            a(b_codes, u8, (N, b_codes.shape[1])), a(b_scales, u8, (N, K // 32)), fb, M, N, K, out,
-            a(c, c.dtype, (M, N)))
-    a.run(_lib.mok_mx_gemm, *args, *a.scratch(ws), stream=stream)
+        _refuse(fn)
+    (M, nb), N, dev = a_scales.shape, b_scales.shape[0], a_codes.get_device()
+    K, ca, cb = 32 * nb, a_codes.shape[1], b_codes.shape[1]
+    out = {torch.bfloat16: MOK_BF16, torch.float32: MOK_FP32}.get(c.dtype)
+    if out is None or ca not in (K, K // 2) or cb not in (K, K // 2):
+        _refuse(fn)
+    _enqueue(fn, dev, _lib.mok_mx_gemm,
+             (_arg(fn, a_codes, u8, (M, ca), dev), _arg(fn, a_scales, u8, (M, nb), dev),
+              MOK_MXFP8 if ca == K else MOK_MXFP4, _arg(fn, b_codes, u8, (N, cb), dev),
+              _arg(fn, b_scales, u8, (N, nb), dev), MOK_MXFP8 if cb == K else MOK_MXFP4, M, N, K,
+              out, _arg(fn, c, c.dtype, (M, N), dev), *_scratch(fn, ws, dev)), stream)
 
 
 # ------------------------------------------------------------------------ layer helper
