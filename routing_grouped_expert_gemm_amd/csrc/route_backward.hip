@@ -219,7 +219,8 @@ struct RbTile {
   int d, E, EP;
   int tiles_d;          // tiles of 128 columns
   int tiles_e;          // tiles of EM experts
-  int dw_blocks;        // workgroups of dW (the first ones); the rest are dx's
+  int dw_tiles, dx_tiles;
+  int dw_blocks;        // workgroups of dW (the first ones, a multiple of 8); the rest are dx's
   int64_t t_range;      // tokens of a dW range, a multiple of 64
 };
 
@@ -275,39 +276,64 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
     __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
     lds_barrier();
   };
-  // LDS-DMA of K rows x CH chunks (row-major source, leading dimension ld): instruction q of this
-  // wave of Q; source row of K row kr: row(kr), columns past the source: the last chunk
-  auto dma_t = [&](auto CH_, int Q, int q, const bf16_t* base, int64_t ld, int c0, int cols,
-                   int last_row, uint32_t to) {
-    constexpr int CH = CH_(), RPI = 64 / CH;
-    const int kr = (wid * Q + q) * RPI + lane / CH;
-    const int c = (lane % CH) ^ tswz<CH>(kr);
-    const int col = min(c0 + 8 * c, cols - 8);
-    dma_b128(uniform_ptr(base), (uint32_t)((min(kr, last_row) * ld + col) * 2),
-             to + (wid * Q + q) * 1024);
+  // LDS-DMA of K rows x CH chunks (row-major source, ld bytes a row): this wave's instruction q of Q
+  // covers rows kr(q) on. at(q): the lane's byte offset; a step whose source ends at row `last`
+  // before the step's last row clamps the rows (their products are with zeros of dl). Offsets are
+  // made once: 64-bit products in every step cost as much issue time as the step's MFMAs.
+  auto row_of = [&](auto CH_, int Q, int q) { return (wid * Q + q) * (64 / CH_()) + lane / CH_(); };
+  auto col_of = [&](auto CH_, int kr, int c0, int cols) {
+    return (uint32_t)min(c0 + 8 * ((lane % CH_()) ^ tswz<CH_()>(kr)), cols - 8) * 2;
   };
+  // XCD x takes an eighth of each product's tiles, neighbours in order: they share a range of dl's
+  // planes (dW) or tokens and, with time, the weight (dx), which its L2 then holds
+  auto tile_of = [](int b, int blocks) { return (b & 7) * (blocks / 8) + (b >> 3); };
   if ((int)blockIdx.x < a.dw_blocks) {
     constexpr int FE = EM / 64, FC = 2;          // waves: 2 x 2
-    const int b = blockIdx.x, c0 = b % a.tiles_d * 128, rest = b / a.tiles_d;
+    const int b = tile_of(blockIdx.x, a.dw_blocks);
+    if (b >= a.dw_tiles) return;
+    const int c0 = b % a.tiles_d * 128, rest = b / a.tiles_d;
     const int e0 = rest % a.tiles_e * EM;
     const int64_t range = rest / a.tiles_e, tb = range * a.t_range;
     const int64_t te = min(a.T, tb + a.t_range);
     const int nk = te > tb ? (int)((te - tb + KT - 1) / KT) : 0;
     const int we = (wid >> 1) * 32 * FE, wc = (wid & 1) * 32 * FC;
+    constexpr int QP = PB / 4096, QX = XB / 4096;
+    static_assert(QP > 0 && QX > 0, "whole instructions a wave");
+    constexpr std::integral_constant<int, EM / 8> CP{};
+    constexpr std::integral_constant<int, 16> CX{};
+    const uint32_t ldp = a.EP * 2, ldx = a.d * 2;
+    uint32_t offp[QP], offx[QX], colx[QX];
+#pragma unroll
+    for (int q = 0; q < QP; ++q) {
+      const int kr = row_of(CP, QP, q);
+      offp[q] = kr * ldp + col_of(CP, kr, 0, EM);
+    }
+#pragma unroll
+    for (int q = 0; q < QX; ++q) {
+      const int kr = row_of(CX, QX, q);
+      colx[q] = col_of(CX, kr, c0, a.d);
+      offx[q] = kr * ldx + colx[q];
+    }
     auto issue = [&](int kt) {
-      const uint32_t to = lds0 + (kt & 1) * WST;
+      const uint32_t to = lds0 + (kt & 1) * WST + wid * 1024 * QP;
       const int64_t t0 = tb + (int64_t)kt * KT;
-      constexpr int QP = PB / 4096, QX = XB / 4096;
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
+      for (int p = 0; p < 3; ++p) {
+        const bf16_t* base = uniform_ptr(a.planes + ((int64_t)p * a.Tp + t0) * a.EP + e0);
 #pragma unroll
-        for (int q = 0; q < QP; ++q)
-          dma_t(std::integral_constant<int, EM / 8>{}, QP, q,
-                a.planes + ((int64_t)p * a.Tp + t0) * a.EP + e0, a.EP, 0, EM, KT - 1, to + p * PB);
+        for (int q = 0; q < QP; ++q) dma_b128(base, offp[q], to + p * PB + q * 1024);
+      }
+      const bf16_t* base = uniform_ptr(a.x + t0 * a.d);
+      const uint32_t tx = lds0 + (kt & 1) * WST + 3 * PB + wid * 1024 * QX;
+      const int last = (int)min((int64_t)KT - 1, a.T - 1 - t0);
+      if (last == KT - 1) {
 #pragma unroll
-      for (int q = 0; q < QX; ++q)
-        dma_t(std::integral_constant<int, 16>{}, QX, q, a.x + t0 * a.d, a.d, c0, a.d,
-              (int)min((int64_t)KT - 1, a.T - 1 - t0), to + 3 * PB);
+        for (int q = 0; q < QX; ++q) dma_b128(base, offx[q], tx + q * 1024);
+      } else {
+#pragma unroll
+        for (int q = 0; q < QX; ++q)
+          dma_b128(base, min(row_of(CX, QX, q), last) * ldx + colx[q], tx + q * 1024);
+      }
     };
     f32x16_t acc[FE][FC] = {};
     if (nk > 0) issue(0);
@@ -346,33 +372,51 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
         }
     return;
   }
-  const int b = blockIdx.x - a.dw_blocks, c0 = b % a.tiles_d * 128;
+  const int b = tile_of(blockIdx.x - a.dw_blocks, gridDim.x - a.dw_blocks);
+  if (b >= a.dx_tiles) return;
+  const int c0 = b % a.tiles_d * 128;
   const int64_t t0 = (int64_t)(b / a.tiles_d) * 128;
-  uint4 in[8];
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 in[8];                          // dx_in and dx pass once: non-temporal
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t t = t0 + i * 16 + tid / 16;
     const int c = c0 + tid % 16 * 8;
-    in[i] = make_uint4(0, 0, 0, 0);
-    if (a.dx_in && t < a.T && c < a.d) in[i] = *(const uint4*)(a.dx_in + t * a.d + c);
+    in[i] = u32x4{0, 0, 0, 0};
+    if (a.dx_in && t < a.T && c < a.d)
+      in[i] = __builtin_nontemporal_load((const u32x4*)(a.dx_in + t * a.d + c));
   }
   const int wt = (wid >> 1) * 64, wc = (wid & 1) * 64;
   const int nk = (a.E + 31) / 32;       // every step holds an expert
+  constexpr std::integral_constant<int, 16> CW{};
+  const uint32_t ldw = a.d * 2;
+  uint32_t offp[2], offw[2], colw[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int r = (wid * 2 + q) * 16 + (lane >> 2);
+    offp[q] = (r * a.EP + 8 * ((lane & 3) ^ ((r >> 2) & 3))) * 2;
+    const int kr = row_of(CW, 2, q);
+    colw[q] = col_of(CW, kr, c0, a.d);
+    offw[q] = kr * ldw + colw[q];
+  }
   auto issue = [&](int kt) {
-    const uint32_t to = lds0 + kt % DN * DST;
+    const uint32_t to = lds0 + kt % DN * DST + wid * 2048;
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < 2; ++p) {
+      const bf16_t* base = uniform_ptr(a.planes + ((int64_t)p * a.Tp + t0) * a.EP + kt * 32);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int r = (wid * 2 + q) * 16 + (lane >> 2);
-        const int c = (lane & 3) ^ ((r >> 2) & 3);
-        dma_b128(uniform_ptr(a.planes + ((int64_t)p * a.Tp + t0) * a.EP + kt * 32),
-                 (uint32_t)((r * a.EP + 8 * c) * 2), to + p * 8192 + (wid * 2 + q) * 1024);
-      }
+      for (int q = 0; q < 2; ++q) dma_b128(base, offp[q], to + p * 8192 + q * 1024);
+    }
+    const bf16_t* base = uniform_ptr(a.w + (int64_t)kt * 32 * a.d);
+    const int last = min(31, a.E - 1 - kt * 32);
+    if (last == 31) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      dma_t(std::integral_constant<int, 16>{}, 2, q, a.w + (int64_t)kt * 32 * a.d, a.d, c0, a.d,
-            min(31, a.E - 1 - kt * 32), to + 16384);
+      for (int q = 0; q < 2; ++q) dma_b128(base, offw[q], to + 16384 + q * 1024);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        dma_b128(base, min(row_of(CW, 2, q), last) * ldw + colw[q], to + 16384 + q * 1024);
+    }
   };
   f32x16_t acc[2][2] = {};
   for (int kt = 0; kt < DN - 1 && kt < nk; ++kt) issue(kt);
@@ -427,15 +471,14 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
       if (t >= a.T || c >= a.d) continue;
       const float* q = st + r * OLD + tid % 16 * 8;
       const float4 u = *(const float4*)q, v = *(const float4*)(q + 4);
-      const uint4 z = in[half * 4 + i];
-      const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+      const u32x4 w = in[half * 4 + i];
       const float s[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-      uint32_t o[4];
+      u32x4 o;
 #pragma unroll
       for (int n = 0; n < 4; ++n)
         o[n] = pack_bf16x2(__uint_as_float(w[n] << 16) + s[2 * n],
                            __uint_as_float(w[n] & 0xFFFF0000u) + s[2 * n + 1]);
-      *(uint4*)(a.dx + t * a.d + c) = make_uint4(o[0], o[1], o[2], o[3]);
+      __builtin_nontemporal_store(o, (u32x4*)(a.dx + t * a.d + c));
     }
   }
 }
@@ -561,9 +604,12 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
     t.tiles_e = p.EP / p.EM;
     t.t_range = p.t_range;
     const int64_t n_dw = dw_router ? p.ranges * t.tiles_e * t.tiles_d : 0;
-    const int64_t n = n_dw + (dx ? p.Tp / 128 * t.tiles_d : 0), n_pl = cdiv(p.Tp * (p.EP / 8), 256);
+    const int64_t n_dx = dx ? p.Tp / 128 * t.tiles_d : 0, n_pl = cdiv(p.Tp * (p.EP / 8), 256);
+    const int64_t n = cdiv(n_dw, 8) * 8 + cdiv(n_dx, 8) * 8;
     if (n * RB_NT >= (int64_t)1 << 32 || n_pl * 256 >= (int64_t)1 << 32) return MOK_EUNSUPPORTED;
-    t.dw_blocks = (int)n_dw;
+    t.dw_tiles = (int)n_dw;
+    t.dx_tiles = (int)n_dx;
+    t.dw_blocks = (int)(cdiv(n_dw, 8) * 8);
     launch_k(k_route_bwd_dl<true>, dim3((unsigned)n_pl), dim3(256), 0, s, nullptr, nullptr, a, p.EP,
              p.Tp, ws);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
