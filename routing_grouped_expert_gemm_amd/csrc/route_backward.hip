@@ -249,26 +249,29 @@ MOK_DEV bf16x8_t frag_t(uint32_t tile, int blk, int s, int lane) {
 }
 
 // Both products in one launch, so that dx's streaming runs beside dW's matrix work. 256 threads.
-//  dW: EM experts x 128 columns over a range of tokens, K steps of 32 tokens: three planes and x
+//  dW: EM experts x XC columns over a range of tokens, K steps of 32 tokens: three planes and x
 //      through two LDS buffers by LDS-DMA.
-//  dx: 128 tokens x 128 columns, K steps of 32 experts: two planes (K-contiguous rows of 64 bytes,
-//      chunk c of row r at slot c ^ (r >> 2 & 3)) and the weight's rows, two buffers (EM 64, where
-//      there are two steps) or three. The tile goes through LDS in float32, half of its rows at a
-//      time, so that dx_in is read and dx written in whole row segments; dx_in is loaded before the
-//      product.
-// Both keep to 48 KB (EM 64) or 72 KB (EM 128) of LDS: 3 or 2 workgroups a CU cover each other's
-// loads (256 experts a workgroup and steps of 64, 112 KB and one workgroup a CU, took 113 us at
-// T 4096, d 7168, E 256).
-template <int EM>
-__global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
+//  dx: 128 tokens x XC columns, K steps of 32 experts: two planes (K-contiguous rows of 64 bytes,
+//      chunk c of row r at slot c ^ (r >> 2 & 3)) and the weight's rows, through three buffers or,
+//      where EM is 64 (two steps) or XC 256 (LDS), two. The tile goes through LDS in float32, half of
+//      its rows at a time, so that dx_in is read and dx written in whole row segments; dx_in is
+//      loaded before the product. Both pass the caches by (T 8192, d 2048, E 64: 36 -> 33 us).
+// 40 to 80 KB of LDS: 2 or 3 workgroups a CU cover each other's loads (256 experts a workgroup and
+// steps of 64, 112 KB and one workgroup a CU, took 113 us at T 4096, d 7168, E 256 where this takes
+// 93). There the tiles do 75 GFLOP, and wait for L2 most: 24 to 31% of the cycles are MFMAs, 37%
+// waits for loads, a quarter of the reads miss L2.
+template <int EM, int XC>
+__global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
   constexpr int KT = 32;
-  constexpr int PB = KT * EM * 2, XB = KT * 256, WST = 3 * PB + XB;      // bytes of a dW step
-  constexpr int DST = 2 * 128 * 64 + 32 * 256;                          // bytes of a dx step
-  constexpr int OLD = 132;                                              // floats of a staged row
-  constexpr int DN = EM == 64 ? 2 : 3;                                  // buffers of dx
+  constexpr int PB = KT * EM * 2, XB = KT * XC * 2, WST = 3 * PB + XB;      // bytes of a dW step
+  constexpr int DST = 2 * 128 * 64 + XB;                                // bytes of a dx step
+  constexpr int OLD = XC + 4;                                             // floats of a staged row
+  constexpr int DN = XC == 256 || EM == 64 ? 2 : 3;                                  // buffers of dx
   constexpr int BYTES = std::max(std::max(2 * WST, DN * DST), 64 * OLD * 4);
   __shared__ __align__(1024) char lds[BYTES];
   const uint32_t lds0 = uniform(lds_addr(lds));
+  constexpr int FC = XC / 64, QX = XB / 4096;
+  constexpr std::integral_constant<int, XC / 8> CX{};
   const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
   const int h = lane >> 5, l = lane & 31;
   // every wave's DMA has landed and its LDS reads are back
@@ -279,28 +282,28 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
   // LDS-DMA of K rows x CH chunks (row-major source, ld bytes a row): this wave's instruction q of Q
   // covers rows kr(q) on. at(q): the lane's byte offset; a step whose source ends at row `last`
   // before the step's last row clamps the rows (their products are with zeros of dl). Offsets are
-  // made once: 64-bit products in every step cost as much issue time as the step's MFMAs.
+  // made once.
   auto row_of = [&](auto CH_, int Q, int q) { return (wid * Q + q) * (64 / CH_()) + lane / CH_(); };
   auto col_of = [&](auto CH_, int kr, int c0, int cols) {
     return (uint32_t)min(c0 + 8 * ((lane % CH_()) ^ tswz<CH_()>(kr)), cols - 8) * 2;
   };
   // XCD x takes an eighth of each product's tiles, neighbours in order: they share a range of dl's
-  // planes (dW) or tokens and, with time, the weight (dx), which its L2 then holds
+  // planes (dW) or tokens and, with time, the weight (dx), which its L2 then holds (T 8192, d 2048,
+  // E 64: 33 -> 31 us)
   auto tile_of = [](int b, int blocks) { return (b & 7) * (blocks / 8) + (b >> 3); };
   if ((int)blockIdx.x < a.dw_blocks) {
-    constexpr int FE = EM / 64, FC = 2;          // waves: 2 x 2
+    constexpr int FE = EM / 64;                  // waves: 2 x 2
     const int b = tile_of(blockIdx.x, a.dw_blocks);
     if (b >= a.dw_tiles) return;
-    const int c0 = b % a.tiles_d * 128, rest = b / a.tiles_d;
+    const int c0 = b % a.tiles_d * XC, rest = b / a.tiles_d;
     const int e0 = rest % a.tiles_e * EM;
     const int64_t range = rest / a.tiles_e, tb = range * a.t_range;
     const int64_t te = min(a.T, tb + a.t_range);
     const int nk = te > tb ? (int)((te - tb + KT - 1) / KT) : 0;
     const int we = (wid >> 1) * 32 * FE, wc = (wid & 1) * 32 * FC;
-    constexpr int QP = PB / 4096, QX = XB / 4096;
+    constexpr int QP = PB / 4096;
     static_assert(QP > 0 && QX > 0, "whole instructions a wave");
     constexpr std::integral_constant<int, EM / 8> CP{};
-    constexpr std::integral_constant<int, 16> CX{};
     const uint32_t ldp = a.EP * 2, ldx = a.d * 2;
     uint32_t offp[QP], offx[QX], colx[QX];
 #pragma unroll
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
       for (int s = 0; s < KT / 16; ++s) {
         bf16x8_t fx[FC];
 #pragma unroll
-        for (int j = 0; j < FC; ++j) fx[j] = frag_t<16>(at + 3 * PB, wc + 32 * j, s, lane);
+        for (int j = 0; j < FC; ++j) fx[j] = frag_t<XC / 8>(at + 3 * PB, wc + 32 * j, s, lane);
 #pragma unroll
         for (int p = 2; p >= 0; --p)           // the smallest plane first
 #pragma unroll
@@ -374,33 +377,37 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
   }
   const int b = tile_of(blockIdx.x - a.dw_blocks, gridDim.x - a.dw_blocks);
   if (b >= a.dx_tiles) return;
-  const int c0 = b % a.tiles_d * 128;
+  const int c0 = b % a.tiles_d * XC;
   const int64_t t0 = (int64_t)(b / a.tiles_d) * 128;
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  u32x4 in[8];                          // dx_in and dx pass once: non-temporal
+  constexpr int TR = XC / 8, RP = RB_NT / TR, NI = 128 / RP;   // threads a row, rows a pass, passes
+  u32x4 in[NI];                          // dx_in and dx pass once: non-temporal
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t t = t0 + i * 16 + tid / 16;
-    const int c = c0 + tid % 16 * 8;
+  for (int i = 0; i < NI; ++i) {
+    const int64_t t = t0 + i * RP + tid / TR;
+    const int c = c0 + tid % TR * 8;
     in[i] = u32x4{0, 0, 0, 0};
     if (a.dx_in && t < a.T && c < a.d)
       in[i] = __builtin_nontemporal_load((const u32x4*)(a.dx_in + t * a.d + c));
   }
-  const int wt = (wid >> 1) * 64, wc = (wid & 1) * 64;
+  const int wt = (wid >> 1) * 64, wc = (wid & 1) * 32 * FC;
   const int nk = (a.E + 31) / 32;       // every step holds an expert
-  constexpr std::integral_constant<int, 16> CW{};
   const uint32_t ldw = a.d * 2;
-  uint32_t offp[2], offw[2], colw[2];
+  uint32_t offp[2], offw[QX], colw[QX];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const int r = (wid * 2 + q) * 16 + (lane >> 2);
     offp[q] = (r * a.EP + 8 * ((lane & 3) ^ ((r >> 2) & 3))) * 2;
-    const int kr = row_of(CW, 2, q);
-    colw[q] = col_of(CW, kr, c0, a.d);
+  }
+#pragma unroll
+  for (int q = 0; q < QX; ++q) {
+    const int kr = row_of(CX, QX, q);
+    colw[q] = col_of(CX, kr, c0, a.d);
     offw[q] = kr * ldw + colw[q];
   }
   auto issue = [&](int kt) {
-    const uint32_t to = lds0 + kt % DN * DST + wid * 2048;
+    const uint32_t at = lds0 + kt % DN * DST, to = at + wid * 2048;
+    const uint32_t tw = at + 16384 + wid * 1024 * QX;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       const bf16_t* base = uniform_ptr(a.planes + ((int64_t)p * a.Tp + t0) * a.EP + kt * 32);
@@ -411,18 +418,18 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
     const int last = min(31, a.E - 1 - kt * 32);
     if (last == 31) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) dma_b128(base, offw[q], to + 16384 + q * 1024);
+      for (int q = 0; q < QX; ++q) dma_b128(base, offw[q], tw + q * 1024);
     } else {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        dma_b128(base, min(row_of(CW, 2, q), last) * ldw + colw[q], to + 16384 + q * 1024);
+      for (int q = 0; q < QX; ++q)
+        dma_b128(base, min(row_of(CX, QX, q), last) * ldw + colw[q], tw + q * 1024);
     }
   };
-  f32x16_t acc[2][2] = {};
+  f32x16_t acc[2][FC] = {};
   for (int kt = 0; kt < DN - 1 && kt < nk; ++kt) issue(kt);
   for (int kt = 0; kt < nk; ++kt) {
-    if (DN == 3 && kt + 1 < nk) {       // the next step's 6 instructions may stay in flight
-      __builtin_amdgcn_s_waitcnt(6 | (7 << 4));
+    if (DN == 3 && kt + 1 < nk) {       // the next step's instructions may stay in flight
+      __builtin_amdgcn_s_waitcnt((4 + QX) | (7 << 4));
       lds_barrier();
     } else {
       publish();
@@ -431,9 +438,9 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
     const uint32_t at = lds0 + kt % DN * DST;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      bf16x8_t fw[2];
+      bf16x8_t fw[FC];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fw[j] = frag_t<16>(at + 16384, wc + 32 * j, s, lane);
+      for (int j = 0; j < FC; ++j) fw[j] = frag_t<XC / 8>(at + 16384, wc + 32 * j, s, lane);
 #pragma unroll
       for (int p = 1; p >= 0; --p)
 #pragma unroll
@@ -442,7 +449,7 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
           const int off = (int)(at - lds0) + p * 8192 + r * 64 + (((2 * s + h) ^ ((r >> 2) & 3)) << 4);
           const bf16x8_t fp = *(const bf16x8_t*)(lds + off);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < FC; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[j], fp, acc[i][j], 0, 0, 0);
         }
     }
@@ -455,7 +462,7 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < FC; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *(float4*)(st + (32 * i + l) * OLD + wc + 32 * j + 8 * q + 4 * h) =
@@ -464,14 +471,14 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_tile(const RbTile a) {
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 16 + tid / 16;
+    for (int i = 0; i < NI / 2; ++i) {
+      const int r = i * RP + tid / TR;
       const int64_t t = t0 + half * 64 + r;
-      const int c = c0 + tid % 16 * 8;
+      const int c = c0 + tid % TR * 8;
       if (t >= a.T || c >= a.d) continue;
-      const float* q = st + r * OLD + tid % 16 * 8;
+      const float* q = st + r * OLD + tid % TR * 8;
       const float4 u = *(const float4*)q, v = *(const float4*)(q + 4);
-      const u32x4 w = in[half * 4 + i];
+      const u32x4 w = in[half * (NI / 2) + i];
       const float s[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
       u32x4 o;
 #pragma unroll
@@ -521,7 +528,7 @@ RbAny rb_any(int64_t T, int d, int E) {
 
 // The plane form's shapes: experts padded to the tile EM, tokens to dx's tiles, dW's ranges.
 struct RbPlan {
-  int EM, EP;
+  int EM, EP, XC;                     // XC: a tile's columns
   int64_t Tp, ranges, t_range;
   size_t planes;                      // bytes; the partial sums follow
 };
@@ -531,9 +538,16 @@ RbPlan rb_plan(int64_t T, int d, int E) {
   if (p.EP > 64) p.EP = (int)cdiv(E, 128) * 128;
   p.EM = p.EP == 64 ? 64 : 128;
   p.Tp = cdiv(T, 128) * 128;
-  // one dW workgroup a CU (T 8192, d 2048, E 64: 45 us with 128 of them, 37 with 256, 41 with 512)
-  const int64_t tiles = cdiv(d, 128) * (p.EP / p.EM);
-  const int64_t n = std::max<int64_t>(1, std::min(cdiv(256, tiles), cdiv(T, 256)));
+  // tiles of 256 columns read a third less into LDS, but fill the chip only with three dx tiles a CU
+  // (128 against 256 columns: T 4096, d 7168, E 256: 101 and 93 us; T 16384, d 4096, E 32: 101 and
+  // 89; T 8192, d 4096, E 128: 72 and 71; T 4096, d 2048, E 128: 30 and 31; T 512, d 2048, E 128:
+  // 18 and 23)
+  p.XC = cdiv(T, 128) * cdiv(d, 256) >= 768 ? 256 : 128;
+  // dW workgroups: one a CU of 128 columns (T 8192, d 2048, E 64: 38 us with 112 of them, 31 with
+  // 256, 36 with 300), fewer of 256, whose partial sums cost more (T 4096, d 7168, E 256: 112 us
+  // with 112, 93 with 168, 99 with 224)
+  const int64_t tiles = cdiv(d, p.XC) * (p.EP / p.EM);
+  const int64_t n = std::max<int64_t>(1, std::min(cdiv(p.XC == 256 ? 160 : 256, tiles), cdiv(T, 256)));
   p.t_range = cdiv(cdiv(T, n), 64) * 64;
   p.ranges = cdiv(T, p.t_range);
   p.planes = (size_t)3 * p.Tp * p.EP * 2;
@@ -600,7 +614,7 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
     t.planes = (const bf16_t*)ws; t.dx = (bf16_t*)dx;
     t.dw = p.ranges > 1 ? (float*)((char*)ws + p.planes) : dw_router;
     t.T = T; t.Tp = p.Tp; t.d = d; t.E = E; t.EP = p.EP;
-    t.tiles_d = (int)cdiv(d, 128);
+    t.tiles_d = (int)cdiv(d, p.XC);
     t.tiles_e = p.EP / p.EM;
     t.t_range = p.t_range;
     const int64_t n_dw = dw_router ? p.ranges * t.tiles_e * t.tiles_d : 0;
@@ -613,7 +627,8 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
     launch_k(k_route_bwd_dl<true>, dim3((unsigned)n_pl), dim3(256), 0, s, nullptr, nullptr, a, p.EP,
              p.Tp, ws);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
-    auto k = p.EM == 64 ? k_route_bwd_tile<64> : k_route_bwd_tile<128>;
+    auto k = p.XC == 256 ? (p.EM == 64 ? k_route_bwd_tile<64, 256> : k_route_bwd_tile<128, 256>)
+                         : (p.EM == 64 ? k_route_bwd_tile<64, 128> : k_route_bwd_tile<128, 128>);
     launch_k(k, dim3((unsigned)n), dim3(RB_NT), 0, s, nullptr, nullptr, t);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
     if (dw_router && p.ranges > 1)

@@ -77,6 +77,11 @@ CASES = [  # T, d, E, k
     (2100, 64, 16, 2), (5000, 40, 8, 2), (512, 2056, 64, 6), (515, 1984, 32, 4), (700, 1999, 130, 8), (40, 30001, 128, 4)]
 
 
+# enough tiles for the wide form of bf16: 768 of 128 tokens x 256 columns
+WIDE = [(16500, 1416, 20, 4), (16400, 1288, 130, 8), (98300, 8, 64, 6), (256, 98056, 100, 8),
+        (1024, 24584, 257, 8)]
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("T,d,E,k", CASES)
 def test_against_float64(T, d, E, k, dtype):
@@ -86,6 +91,17 @@ def test_against_float64(T, d, E, k, dtype):
     check(dx, dw, reference(i), T, E, k, TYPES[dtype])
     dx2, dw2 = run(mok, i)
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("T,d,E,k", WIDE)
+def test_wide_against_float64(T, d, E, k):
+    import routing_grouped_expert_gemm_amd as mok
+    i = inputs(T, d, E, k, "bf16")
+    dx, dw = run(mok, i)
+    check(dx, dw, reference(i), T, E, k, torch.bfloat16)
+    for want in ("dx", "dw"):                 # either product alone: the same bits
+        a, b = run(mok, i, want=(want,))
+        assert torch.equal(a, dx) if want == "dx" else torch.equal(b, dw)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
