@@ -65,12 +65,28 @@ template <class T> MOK_DEV float as_stored(float v);     // v rounded to the sto
 template <> MOK_DEV float as_stored<float>(float v) { return v; }
 template <> MOK_DEV float as_stored<bf16_t>(float v) { return bf16_to_f32(f32_to_bf16(v)); }
 
+// rstd as the norm multiplies by it: y = (h scale) w (r + rl), scale the power of two that brings the
+// row's root mean square to 0.5 .. 1, so that neither h w nor rstd leaves float32's range where y
+// does not (rows of 1e38 with a weight above 3; rows of 1e-40 with eps 0).
+struct RowScale {
+  float scale, r, rl;
+  MOK_DEV explicit RowScale(double rd) {
+    const int e = min(max((int)(__double2hiint(rd) >> 20) - 1023, -126), 126);
+    scale = __int_as_float((e + 127) << 23);
+    const double v = rd * (double)__int_as_float((127 - e) << 23);
+    r = (float)v;
+    rl = (float)(v - r);
+  }
+};
+
 // h w rstd in float32, rstd = r + rl: the rounding errors of the products, by fma, added back. h w
 // is exact for bf16 operands. (Contracted, y + e would become fma(p, r, e) and count the error
 // twice.)
 template <class T>
-MOK_DEV float norm_value(float h, float w, float r, float rl) {
+MOK_DEV float norm_value(float h, float w, const RowScale& q) {
 #pragma clang fp contract(off)
+  const float r = q.r, rl = q.rl;
+  h *= q.scale;
   const float p = h * w;
   const float y = p * r;
   float e = __builtin_fmaf(p, rl, __builtin_fmaf(p, r, -y));
@@ -152,8 +168,8 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm(
     for (int i = 0; i < 8; ++i) ss = fma((double)h[n][i], (double)h[n][i], ss);
   }
   const double rd = 1.0 / sqrt(row_total<TPR>(ss, sh) / d + eps);
-  const float rstd = (float)rd, rl = (float)(rd - rstd);
-  if (rstd_out && live && l == 0) rstd_out[row] = rstd;
+  const RowScale rs(rd);
+  if (rstd_out && live && l == 0) rstd_out[row] = (float)rd;
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     const int c = (n * TPR + l) * 8;
@@ -161,7 +177,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm(
     float w[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8];
     if (ok) Piece<T>::load(weight + c, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = norm_value<T>(h[n][i], w[i], rstd, rl);
+    for (int i = 0; i < 8; ++i) v[i] = norm_value<T>(h[n][i], w[i], rs);
     if (y && ok) Piece<T>::store(y + at + c, v);
     if (codes) {                   // d % 32 == 0: a quad's four lanes are all inside the row
       uint8_t s;
@@ -195,10 +211,10 @@ __global__ __launch_bounds__(NT) void k_rmsnorm_any(
   ss = row_total<NT>(ss, sh);
   __syncthreads();                 // the row's h is written: other threads read it below
   const double rd = 1.0 / sqrt(ss / d + eps);
-  const float rstd = (float)rd, rl = (float)(rd - rstd);
-  if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
+  const RowScale rs(rd);
+  if (rstd_out && threadIdx.x == 0) rstd_out[row] = (float)rd;
   auto h_at = [&](int i) { return h_out ? load_as_f32(h_out + at + i) : sum_at(i); };
-  auto y_at = [&](int i) { return norm_value<T>(h_at(i), load_as_f32(weight + i), rstd, rl); };
+  auto y_at = [&](int i) { return norm_value<T>(h_at(i), load_as_f32(weight + i), rs); };
   if (codes) {
     for (int b = threadIdx.x; b < d / 32; b += NT) {
       float amax = 0.0f;

@@ -147,6 +147,25 @@ def test_float32_norm_is_rounded_once(dtype):
         assert (y.cpu().numpy() != ref).sum() <= T * d >> 16
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 100, 2048, 7168, 9000])
+def test_rows_at_the_ends_of_the_range(d, dtype):
+    """Rows of 1e38, where h weight is past float32 though y is not; of 1e-38 and 1e-40, where (eps
+    0) h weight is a subnormal or rstd past float32; one large value among small ones."""
+    import routing_grouped_expert_gemm_amd as mok
+    t = TYPES[dtype]
+    g = torch.Generator().manual_seed(d)
+    v = torch.rand(4, d, generator=g, dtype=torch.float64) + 0.5
+    v *= torch.tensor([1e38, 1e-38, 1e-40, 1.0], dtype=torch.float64)[:, None]
+    v[3, d // 2] = 1e38
+    x = (v * torch.where(torch.rand(4, d, generator=g) < 0.5, -1, 1)).to(t)
+    w = (8 * torch.randn(d, generator=g)).to(t)
+    y = torch.empty(4, d, dtype=t, device=DEV)
+    mok.mok_rmsnorm(x.to(DEV), w.to(DEV), 0.0, y=y)
+    ref = reference(x, None, w, eps=0.0)
+    near(y, ref["y"], 2 * 64 * U * np.abs(ref["y"]), t)
+
+
 def test_mxfp8_marks_what_is_not_finite():
     """A NaN or an infinity in a row: the blocks of y that hold a NaN are all NaN (0x7F, 0xFF)."""
     import routing_grouped_expert_gemm_amd as mok
