@@ -553,9 +553,11 @@ __global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
   read_scales(0);
   take_scales();
   frags(0, 0, 0);
+  // (ST - 2) NQ of a step's NQ + 1: the prologue's steps have no scale piece among their loads, so
+  // that with (ST - 2) (NQ + 1) the first steps' last loads could still be on their way.
   int kt = 0;
   for (; kt < nk - ST; ++kt)
-    step(kt, yes, no, yes, yes, std::integral_constant<int, (ST - 2) * (NQ + 1)>{});
+    step(kt, yes, no, yes, yes, std::integral_constant<int, (ST - 2) * NQ>{});
   if (nk >= ST) step(kt++, yes, yes, no, yes, none);
   if constexpr (ST > 2) {
     for (; kt < nk - 1; ++kt) step(kt, yes, yes, no, no, none);
