@@ -271,12 +271,13 @@ __global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
   constexpr int ST = C::ST;
   constexpr int A_B = C::BM * C::RBA, B_B = C::BN * C::RBB, S_B = (C::BM + C::BN) * 32;   // bytes
   constexpr int OUT_B = C::NW * 32 * (C::BN / C::WN * 4 + 16);      // the epilogue's rows
-  __shared__ __align__(1024) char lds[std::max(ST * (A_B + B_B) + 2 * S_B, OUT_B)];
+  constexpr int NSB = ST > 2 ? 4 : 2;                               // buffers of scales
+  __shared__ __align__(1024) char lds[std::max(ST * (A_B + B_B) + NSB * S_B, OUT_B)];
   char* const lds_b0 = lds + ST * A_B;
   char* const lds_s0 = lds_b0 + ST * B_B;
   auto buf_a = [&](int kt) { return (uint4*)(lds + kt % ST * A_B); };
   auto buf_b = [&](int kt) { return (uint4*)(lds_b0 + kt % ST * B_B); };
-  auto buf_s = [&](int g) { return (uint32_t*)(lds_s0 + (g & 1) * S_B); };
+  auto buf_s = [&](int g) { return (uint32_t*)(lds_s0 + (g & (NSB - 1)) * S_B); };
   const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
   const int wm = wid / C::WN, wn = wid % C::WN, h = lane >> 5, r = lane & 31;
   // XCD x takes consecutive tiles, 8 M tiles deep, so that its L2 holds their operands
@@ -334,14 +335,19 @@ __global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
     for (int q = 0; q < NQ; ++q) issue(kt, q);
   };
   // Scales go through LDS in groups of SG steps: 32 bytes of each of the tile's BM + BN rows (A's
-  // first), two buffers. (Read from memory by every lane for its own rows and step, a word at a
+  // first), NSB buffers. (Read from memory by every lane for its own rows and step, a word at a
   // time, they touched as many cache lines as the codes: M 8192, N 4096, K 7168 took 155 us,
   // against 126 without any scales.) 16-byte half x of row r lies at half x ^ (r >> 3 & 1), which
-  // spreads a column of words over the banks. Pieces of the next group are loaded one a step, P
-  // pieces from one step before the current group on (then over again: the same bytes), so that
-  // the last one is published with the step before that group's first. A piece is 32 rows a
-  // wave, 16 bytes a lane: the first half of the waves loads A's, the second B's.
+  // spreads a column of words over the banks. Step kt loads a piece of the group SG steps on from
+  // step kt + ST - 1's: with ST 2 the last piece lands with the step before that group's first, with
+  // ST 4, where two steps' loads stay in flight, two steps earlier, hence more buffers.
+  // The first half of the waves loads A's rows, the second B's. A piece is 32 rows a wave, 16 bytes a
+  // lane, P pieces a group, then over again (the same bytes); or (WORDS) 8 rows, a word a lane, where
+  // those are a step's share: a fourth of the cache lines (M 1000, N 4096, K 7168, MXFP8 by MXFP4:
+  // 34.1 -> 32.9 us, by MXFP8: 35.1 -> 33.3; two such loads a step were no faster, 22.5 against 21.8
+  // for MXFP4 operands).
   constexpr int SG = 32 / (KT / 32), SH = C::NW / 2, P = C::BM / (32 * SH);
+  constexpr bool WORDS = C::AL && C::BM == 8 * SH * SG;
   static_assert(C::BM == C::BN, "both operands' scales in the same number of pieces");
   const bool tiny = KB < 16;
   const uint8_t* base_sc = uniform_ptr(wid < SH ? p.as + (int64_t)m0 * KB : p.bs + (int64_t)n0 * KB);
@@ -355,8 +361,20 @@ __global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
   auto sc_dma = [&](int g, int t) {
     __builtin_amdgcn_sched_barrier(0);
     dma_b128(base_sc, sc_at(t) + min(sc_byte + g * 32, KB - 16),
-             to_s + (g & 1) * S_B + (sc_to + t * 32 * SH) * 32);
+             to_s + (g & (NSB - 1)) * S_B + (sc_to + t * 32 * SH) * 32);
     __builtin_amdgcn_sched_barrier(0);
+  };
+  auto sc_words = [&](int g, int t) {
+    __builtin_amdgcn_sched_barrier(0);
+    const int e = t * SH + wid % SH;                       // the 8 rows
+    const uint32_t row = (uint32_t)min(e * 8 + lane / 8, sc_last) * (uint32_t)KB;
+    const int w = (lane % 8) ^ (4 * (e & 1));
+    dma_b32(base_sc, row + min(step0 * (KT / 32) + g * 32 + 4 * w, KB - 4),
+            to_s + (g & (NSB - 1)) * S_B + (wid / SH * C::BM + e * 8) * 32);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto sc_piece = [&](int g, int t) {
+    if constexpr (WORDS) sc_words(g, t); else sc_dma(g, t % P);
   };
   // else through registers: 16 bytes from the row's byte, or the row's last 16 where it ends
   // before, then shifted down by the bytes that it starts early. Rows of fewer than 16 blocks:
@@ -493,9 +511,9 @@ __global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
   constexpr bool SPREAD = SUB == 4 || ST > 2;
   constexpr int H1 = SPREAD ? (NQ + 1) / 2 : NQ, H2 = NQ - H1;
   auto step = [&](int kt, auto MORE, auto LAST, auto DMA, auto LATE, auto OUT) {
-    const int sg = (kt + 1) / SG + 1, st = (kt + 1) % SG % P;    // the scale piece on its way
+    const int u = kt + ST - 1, sg = u / SG + 1, st = u % SG;     // the scale piece on its way
     uint4 sv;
-    if constexpr (DMA() && !C::AL) sv = sc_load(sg, st);
+    if constexpr (DMA() && !C::AL) sv = sc_load(sg, st % P);
     static_for<SUB - 1>([&](auto s) {
       mfmas(s, [&](int n) {
         if (n == NM / 2 - 1) frags(kt, s() + 1, (s() + 1) & 1);
@@ -513,7 +531,7 @@ __global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
       }
       if constexpr (DMA()) {
         if (n == 1) {
-          if constexpr (C::AL) sc_dma(sg, st); else sc_store(sg, st, sv);
+          if constexpr (C::AL) sc_piece(sg, st); else sc_store(sg, st % P, sv);
         }
 #pragma unroll
         for (int q = n * H1 / NM; q < (n + 1) * H1 / NM; ++q) issue(kt + ST, q);
@@ -534,7 +552,8 @@ __global__ __launch_bounds__(64 * C::NW) void k_mx_tile(const MxArgs p) {
     }
   }
   if constexpr (C::AL) {
-    sc_dma(1, 0);
+#pragma unroll
+    for (int u = 0; u < ST - 1; ++u) sc_piece(1, u);
   } else {
     if (KB > 32) sc_store(1, 0, sc_load(1, 0));
   }

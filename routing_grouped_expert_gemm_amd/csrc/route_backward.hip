@@ -217,7 +217,7 @@ struct RbTile {
   float* dw;            // dW itself (one range) or the partial sums [ranges, E, d]
   int64_t T, Tp;
   int d, E, EP;
-  int tiles_d;          // tiles of 128 columns
+  int tiles_d;          // tiles of XC columns
   int tiles_e;          // tiles of EM experts
   int dw_tiles, dx_tiles;
   int dw_blocks;        // workgroups of dW (the first ones, a multiple of 8); the rest are dx's
