@@ -14,7 +14,8 @@
 //    values loaded into registers under the MFMAs. dl is written once in float32 (DL), or, where
 //    T d E < 2^27, built by each workgroup in LDS from the given dlogits and the picks, which saves
 //    a launch (float32, T 257, d 272, E 20: 12 against 15 us; T 508, d 4864, E 182: 63 against 46).
-//  k_route_bwd_tile  bf16 rows of d % 8 == 0: dl is written once as three bf16 planes that sum to
+//  k_route_bwd_tile  bf16 rows of d % 8 == 0, or of any d where there is much to do, x and the weight
+//    then copied to such rows (k_route_bwd_pad): dl is written once as three bf16 planes that sum to
 //    it (8 + 8 + 8 significant bits: 24, all of float32's), and both products run on the bf16
 //    MFMA with float32 sums: dW on all three planes, dx, which is rounded to 8 bits, on two.
 #include <algorithm>
@@ -211,12 +212,55 @@ __global__ __launch_bounds__(256) void k_route_bwd_dl(const RbArgs a, int EP, in
   }
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The n (at most 8) bf16 values at p, zeros behind them, and back: p on any value's address. Whole
+// pieces in one access (with 8 of 2 bytes each T 8192, d 2050, E 64 took 104 us, with these 57).
+MOK_DEV u32x4 load_part(const bf16_t* p, int n) {
+  u32x4 v = {0, 0, 0, 0};
+  if (n >= 8) {
+    __builtin_memcpy(&v, p, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+  }
+  return v;
+}
+MOK_DEV void store_part(bf16_t* p, int n, u32x4 v) {
+  if (n >= 8) {
+    __builtin_memcpy(p, &v, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e] = (bf16_t)(v[e / 2] >> (16 * (e & 1)));
+  }
+}
+
+// Rows of d bf16 values, d % 8 != 0, laid out in rows of ld = d rounded up to 8, zeros behind them:
+// x's T rows, then the router weight's E (either may be left out).
+__global__ __launch_bounds__(256) void k_route_bwd_pad(const bf16_t* __restrict__ x, int64_t T,
+                                                       const bf16_t* __restrict__ w, int E, int d,
+                                                       int ld, bf16_t* __restrict__ out) {
+  const int per = ld / 8;
+  const int64_t n = (T + E) * per;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per;
+    const int c = (int)(i - row * per) * 8;
+    const bf16_t* src = row < T ? x : w;
+    if (!src) continue;
+    src += (row < T ? row : row - T) * d;
+    *(u32x4*)(out + row * ld + c) = load_part(src + c, d - c);
+  }
+}
+
 struct RbTile {
   const bf16_t *x, *w, *dx_in, *planes;
   bf16_t* dx;
   float* dw;            // dW itself (one range) or the partial sums [ranges, E, d]
   int64_t T, Tp;
   int d, E, EP;
+  int ld;               // row of x and w: d, or d rounded up to 8 where x and w are padded copies
   int tiles_d;          // tiles of XC columns
   int tiles_e;          // tiles of EM experts
   int dw_tiles, dx_tiles;
@@ -274,6 +318,7 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
   constexpr std::integral_constant<int, XC / 8> CX{};
   const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
   const int h = lane >> 5, l = lane & 31;
+  const bool padded = a.ld != a.d;        // dx_in, dx and dW have rows of d
   // every wave's DMA has landed and its LDS reads are back
   auto publish = [&]() {
     __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
@@ -304,7 +349,7 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
     constexpr int QP = PB / 4096;
     static_assert(QP > 0 && QX > 0, "whole instructions a wave");
     constexpr std::integral_constant<int, EM / 8> CP{};
-    const uint32_t ldp = a.EP * 2, ldx = a.d * 2;
+    const uint32_t ldp = a.EP * 2, ldx = a.ld * 2;
     uint32_t offp[QP], offx[QX], colx[QX];
 #pragma unroll
     for (int q = 0; q < QP; ++q) {
@@ -314,7 +359,7 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
 #pragma unroll
     for (int q = 0; q < QX; ++q) {
       const int kr = row_of(CX, QX, q);
-      colx[q] = col_of(CX, kr, c0, a.d);
+      colx[q] = col_of(CX, kr, c0, a.ld);
       offx[q] = kr * ldx + colx[q];
     }
     auto issue = [&](int kt) {
@@ -326,7 +371,7 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
 #pragma unroll
         for (int q = 0; q < QP; ++q) dma_b128(base, offp[q], to + p * PB + q * 1024);
       }
-      const bf16_t* base = uniform_ptr(a.x + t0 * a.d);
+      const bf16_t* base = uniform_ptr(a.x + t0 * a.ld);
       const uint32_t tx = lds0 + (kt & 1) * WST + 3 * PB + wid * 1024 * QX;
       const int last = (int)min((int64_t)KT - 1, a.T - 1 - t0);
       if (last == KT - 1) {
@@ -368,10 +413,18 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int e = e0 + we + 32 * i + l, c = c0 + wc + 32 * j + 8 * q + 4 * h;
-          if (e < a.E && c < a.d)
-            *(float4*)(out + (int64_t)e * a.d + c) =
-                make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                            acc[i][j][4 * q + 3]);
+          float* at = out + (int64_t)e * a.d + c;
+          if (e < a.E && c < a.d) {
+            const float4 v = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                         acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+            if (c + 4 <= a.d) {
+              __builtin_memcpy(at, &v, 16);              // d % 4 != 0: not on 16 bytes
+            } else {
+              at[0] = v.x;
+              if (c + 1 < a.d) at[1] = v.y;
+              if (c + 2 < a.d) at[2] = v.z;
+            }
+          }
         }
     return;
   }
@@ -379,7 +432,6 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
   if (b >= a.dx_tiles) return;
   const int c0 = b % a.tiles_d * XC;
   const int64_t t0 = (int64_t)(b / a.tiles_d) * 128;
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   constexpr int TR = XC / 8, RP = RB_NT / TR, NI = 128 / RP;   // threads a row, rows a pass, passes
   u32x4 in[NI];                          // dx_in and dx pass once: non-temporal
 #pragma unroll
@@ -387,12 +439,14 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
     const int64_t t = t0 + i * RP + tid / TR;
     const int c = c0 + tid % TR * 8;
     in[i] = u32x4{0, 0, 0, 0};
-    if (a.dx_in && t < a.T && c < a.d)
-      in[i] = __builtin_nontemporal_load((const u32x4*)(a.dx_in + t * a.d + c));
+    if (a.dx_in && t < a.T && c < a.d) {
+      const bf16_t* at = a.dx_in + t * a.d + c;
+      in[i] = padded ? load_part(at, a.d - c) : __builtin_nontemporal_load((const u32x4*)at);
+    }
   }
   const int wt = (wid >> 1) * 64, wc = (wid & 1) * 32 * FC;
   const int nk = (a.E + 31) / 32;       // every step holds an expert
-  const uint32_t ldw = a.d * 2;
+  const uint32_t ldw = a.ld * 2;
   uint32_t offp[2], offw[QX], colw[QX];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -402,7 +456,7 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
 #pragma unroll
   for (int q = 0; q < QX; ++q) {
     const int kr = row_of(CX, QX, q);
-    colw[q] = col_of(CX, kr, c0, a.d);
+    colw[q] = col_of(CX, kr, c0, a.ld);
     offw[q] = kr * ldw + colw[q];
   }
   auto issue = [&](int kt) {
@@ -414,7 +468,7 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) dma_b128(base, offp[q], to + p * 8192 + q * 1024);
     }
-    const bf16_t* base = uniform_ptr(a.w + (int64_t)kt * 32 * a.d);
+    const bf16_t* base = uniform_ptr(a.w + (int64_t)kt * 32 * a.ld);
     const int last = min(31, a.E - 1 - kt * 32);
     if (last == 31) {
 #pragma unroll
@@ -485,7 +539,9 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
       for (int n = 0; n < 4; ++n)
         o[n] = pack_bf16x2(__uint_as_float(w[n] << 16) + s[2 * n],
                            __uint_as_float(w[n] & 0xFFFF0000u) + s[2 * n + 1]);
-      __builtin_nontemporal_store(o, (u32x4*)(a.dx + t * a.d + c));
+      bf16_t* at = a.dx + t * a.d + c;
+      if (padded) store_part(at, a.d - c, o);
+      else __builtin_nontemporal_store(o, (u32x4*)at);
     }
   }
 }
@@ -530,7 +586,8 @@ RbAny rb_any(int64_t T, int d, int E) {
 struct RbPlan {
   int EM, EP, XC;                     // XC: a tile's columns
   int64_t Tp, ranges, t_range;
-  size_t planes;                      // bytes; the partial sums follow
+  int ld;                             // a row of x and w, as the tiles read them
+  size_t planes, copies, total;       // bytes: dl's planes, padded x and w, then the partial sums
 };
 RbPlan rb_plan(int64_t T, int d, int E) {
   RbPlan p;
@@ -551,7 +608,17 @@ RbPlan rb_plan(int64_t T, int d, int E) {
   p.t_range = cdiv(cdiv(T, n), 64) * 64;
   p.ranges = cdiv(T, p.t_range);
   p.planes = (size_t)3 * p.Tp * p.EP * 2;
+  p.ld = (int)cdiv(d, 8) * 8;
+  p.copies = p.ld == d ? 0 : (size_t)(T + E) * p.ld * 2;
+  p.total = p.planes + p.copies + (p.ranges > 1 ? (size_t)p.ranges * E * d * sizeof(float) : 0);
   return p;
+}
+
+// bf16 rows that the plane form takes: whole pieces of 16 bytes, or, where the products outweigh a
+// launch more and a copy of x and the weight in such rows, any (T 257, d 275, E 20: 12.6 us in the
+// any-size form, 15.9 in this; T 512, d 1069, E 64: 19.4 and 18.8; T 5536, d 1069, E 212: 153 and 53).
+bool rb_tiled(int64_t T, int d, int E) {
+  return d % 8 == 0 || (double)T * d * E >= (double)(1 << 25);
 }
 
 int rb_check(int64_t T, int32_t d, int32_t E, int32_t k, int32_t io_dtype) {
@@ -572,10 +639,7 @@ int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t 
                                        size_t* bytes) {
   if (!bytes || rb_check(T, d, E, 1, io_dtype) != MOK_OK) return MOK_EINVAL;
   size_t need = rb_any(T, d, E).total;
-  if (io_dtype == MOK_BF16 && T > 0) {
-    const RbPlan p = rb_plan(T, d, E);
-    need = std::max(need, p.planes + (p.ranges > 1 ? (size_t)p.ranges * E * d * sizeof(float) : 0));
-  }
+  if (io_dtype == MOK_BF16 && T > 0 && rb_tiled(T, d, E)) need = std::max(need, rb_plan(T, d, E).total);
   *bytes = need;
   return MOK_OK;
 }
@@ -606,13 +670,14 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
   a.x = x; a.w = w_router; a.idx = topk_idx; a.tw = topk_w; a.dtw = dtopk_w; a.dlogits = dlogits;
   a.dx_in = dx_in; a.dx = dx; a.T = T; a.d = d; a.E = E; a.k = k;
   auto al16 = [](const void* p) { return (uintptr_t)p % 16 == 0; };
-  if (io_dtype == MOK_BF16 && d % 8 == 0 && al16(x) && al16(w_router) && al16(dx_in) && al16(dx) &&
-      al16(dw_router)) {
+  const bool aligned = al16(x) && al16(w_router) && al16(dx_in) && al16(dx) && al16(dw_router);
+  if (io_dtype == MOK_BF16 && rb_tiled(T, d, E) && (aligned || d % 8)) {
     const RbPlan p = rb_plan(T, d, E);
     RbTile t;
     t.x = (const bf16_t*)x; t.w = (const bf16_t*)w_router; t.dx_in = (const bf16_t*)dx_in;
     t.planes = (const bf16_t*)ws; t.dx = (bf16_t*)dx;
-    t.dw = p.ranges > 1 ? (float*)((char*)ws + p.planes) : dw_router;
+    t.dw = p.ranges > 1 ? (float*)((char*)ws + p.planes + p.copies) : dw_router;
+    t.ld = p.ld;
     t.T = T; t.Tp = p.Tp; t.d = d; t.E = E; t.EP = p.EP;
     t.tiles_d = (int)cdiv(d, p.XC);
     t.tiles_e = p.EP / p.EM;
@@ -627,6 +692,15 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
     launch_k(k_route_bwd_dl<true>, dim3((unsigned)n_pl), dim3(256), 0, s, nullptr, nullptr, a, p.EP,
              p.Tp, ws);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
+    if (p.copies) {
+      bf16_t* const to = (bf16_t*)((char*)ws + p.planes);
+      launch_k(k_route_bwd_pad, dim3((unsigned)std::min<int64_t>(cdiv((T + E) * (p.ld / 8), 256), 8192)),
+               dim3(256), 0, s, nullptr, nullptr, dw_router ? t.x : nullptr, T, dx ? t.w : nullptr, E,
+               d, p.ld, to);
+      if (hipGetLastError() != hipSuccess) return MOK_EHIP;
+      t.x = to;
+      t.w = to + T * p.ld;
+    }
     auto k = p.XC == 256 ? (p.EM == 64 ? k_route_bwd_tile<64, 256> : k_route_bwd_tile<128, 256>)
                          : (p.EM == 64 ? k_route_bwd_tile<64, 128> : k_route_bwd_tile<128, 128>);
     launch_k(k, dim3((unsigned)n), dim3(RB_NT), 0, s, nullptr, nullptr, t);

@@ -79,7 +79,10 @@ CASES = [  # T, d, E, k
 
 # enough tiles for the wide form of bf16: 768 of 128 tokens x 256 columns
 WIDE = [(16500, 1416, 20, 4), (16400, 1288, 130, 8), (98300, 8, 64, 6), (256, 98056, 100, 8),
-        (1024, 24584, 257, 8)]
+        (1024, 24584, 257, 8),
+        # rows that are copied to 16 bytes: 2^25 products or more of another d than whole pieces
+        (16500, 1417, 20, 4), (16400, 1283, 130, 8), (98300, 11, 64, 6), (5536, 1069, 212, 6),
+        (1030, 1020, 64, 6), (2100, 2047, 16, 2), (33000, 3, 1000, 4)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -132,7 +135,7 @@ def test_picks_outside_and_repeated(dtype):
     check(dx, dw, reference(i), T, E, k, TYPES[dtype])
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 50), ("fp32", 64)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 50), ("bf16", 13625), ("fp32", 64)])
 def test_dx_over_dx_in_and_rows_behind(dtype, d):
     import routing_grouped_expert_gemm_amd as mok
     T, E, k = 77, 64, 6
@@ -186,7 +189,29 @@ def test_gradient_against_differences():
         assert abs(num - float(part.sum())) <= 1e-4 * float(part.abs().sum())
 
 
-@pytest.mark.parametrize("d", [256, 100])
+@pytest.mark.parametrize("dtype,T,d,E", [("bf16", 90, 64, 32), ("bf16", 1100, 1001, 64),
+                                         ("bf16", 1100, 1024, 64), ("fp32", 90, 64, 32)])
+def test_any_address(dtype, T, d, E):
+    """Tensors that start one value behind a 16-byte address."""
+    import routing_grouped_expert_gemm_amd as mok
+    k = 5
+    i = inputs(T, d, E, k, dtype, seed=6)
+
+    def off(v):
+        b = torch.empty(v.numel() + 1, dtype=v.dtype, device=DEV)
+        b[1:] = v.to(DEV).flatten()
+        return b[1:].view(v.shape)
+
+    dx, dw = off(torch.full((T, d), 7.0).to(TYPES[dtype])), off(torch.full((E, d), 7.0))
+    ws = torch.empty(mok.mok_route_backward_workspace_bytes(T, d, E, TYPES[dtype]),
+                     dtype=torch.uint8, device=DEV)
+    mok.mok_route_backward(off(i["x"]), off(i["w"]), off(i["idx"]), off(i["tw"]), off(i["dtw"]), dx,
+                           dw, ws, dlogits=off(i["dl"]), dx_in=off(i["dx_in"]))
+    torch.cuda.synchronize()
+    check(dx, dw, reference(i), T, E, k, TYPES[dtype])
+
+
+@pytest.mark.parametrize("d", [256, 100, 1003])
 def test_graph_replays(d):
     import routing_grouped_expert_gemm_amd as mok
     T, E, k = 1100, 64, 6
