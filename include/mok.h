@@ -397,7 +397,8 @@ int mok_balance_loss_backward(const float* logits, const int32_t* counts, int64_
  * Outputs, each NULL where not wanted (one at least is): h [rows, d] and y [rows, d] in the
  * storage type, rstd [rows] float32, and y in MXFP8 (both or none): codes [rows, d] E4M3 and
  * scales [rows, d / 32] E8M0 in the layout and by the rules of mok_quantize_mxfp8_f32, from y
- * rounded once to float32. A 32-value block of y with an infinity or a NaN is all NaN (codes 0x7F, scale 0xFF).
+ * rounded once to float32. A 32-value block of y with an infinity or a NaN is all NaN (codes 0x7F,
+ * scale 0xFF).
  * x, residual, weight [d]: float32 or bf16 (io_dtype). h may be x or residual, and y may be x or
  * residual where h is not the same one; other overlaps are not allowed. d >= 1, d % 32 == 0 with
  * codes, d <= 2^24; rows < 2^31; eps >= 0. Rows of d % 8 == 0, d <= 16384, with 16-byte aligned
@@ -432,7 +433,8 @@ int mok_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const
  * dx may be dx_in, and overlaps nothing else. Sums in float32 (bf16 operands enter as they are,
  * dl with at least 16 significant bits for dx and 24 for dw_router); each output is rounded once;
  * no atomics: bit-identical reruns. Every token's row of x and every dtopk_w entry is read; infinite
- * or NaN values in them (or in w_router) make what they enter NaN. Sizes as mok_route, d <= 2^24, T k < 2^31.
+ * or NaN values in them (or in w_router) make what they enter NaN. Sizes as mok_route, d <= 2^24,
+ * T k < 2^31.
  * ws: device scratch of mok_route_backward_workspace_bytes(...) bytes, 16-byte aligned. */
 int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t io_dtype,
                                        size_t* bytes);
@@ -449,9 +451,9 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
  * once from float32 sums. Products are exact but for operands in MXFP8: the matrix instruction adds
  * a block's products on a grid 13 bits below the largest, which leaves 1.5e-5 of the result's norm
  * for two MXFP8 operands, 5e-6 for one with bf16 results, and less than 1e-7 with float32 ones
- * (which then take twice the instructions). K % 32 == 0, 32 <= K <= 2^22; M, N >= 0, < 2^31 (and fewer than 2^23
- * tiles of 128 x 128; up to 64 rows: N <= 2^27). Codes and c start on 16 bytes. A scale of 0xFF (NaN) or a NaN code makes what it enters
- * NaN. ws: device scratch of mok_mx_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned (0 bytes:
+ * (which then take twice the instructions). K % 32 == 0, 32 <= K <= 2^22; M, N >= 0, < 2^31
+ * (and fewer than 2^23 tiles of 128 x 128; up to 64 rows: N <= 2^27). Codes and c start on 16 bytes.
+ * A scale of 0xFF (NaN) or a NaN code makes what it enters NaN. ws: device scratch of mok_mx_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned (0 bytes:
  * may be NULL). Bit-identical reruns. */
 int mok_mx_gemm_workspace_bytes(int64_t M, int64_t N, int32_t K, size_t* bytes);
 int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype,

@@ -242,14 +242,15 @@ __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
 // ------------------------------------------------------------------------- LDS tiles
 // BM x BN tiles, WM x WN waves of BM/WM x BN/WN: 2 x 2 (two waves a SIMD were no faster: 2 x 4 and
 // 4 x 2 were within 2% at 256 x 256 and 10 to 20% slower at 128 x 128, where two groups of 2 x 2 that
-// share a step's K were 3 to 17% slower). K steps of KT values go to one of ST LDS buffers by LDS-DMA (16-byte chunks; chunk c of row r at slot c ^ swz(r), so that the 16 rows that a
-// quarter of a wave reads at one chunk hit distinct banks). A step's last sub-step follows the
+// share a step's K were 3 to 17% slower). K steps of KT values go to one of ST LDS buffers by
+// LDS-DMA (16-byte chunks; chunk c of row r at slot c ^ swz(r), so that the 16 rows that a quarter
+// of a wave reads at one chunk hit distinct banks). A step's last sub-step follows the
 // barrier that publishes the next step's buffer: its MFMAs cover the next step's first LDS reads,
 // and the DMA of the step ST steps on, into the buffer just read, is issued among them.
-// 128 x 128 tiles leave room for 4 buffers: their steps are shorter than a load's way from memory (3, 5
-// and 6 buffers took the same time). One tile a CU is bound by the issue of its loads: M 1000, N 4096,
-// K 7168 MXFP8 x MXFP4 takes 33 us, 26 without its code loads, 29 without its scale loads, 20 with
-// the MFMAs alone.
+// 128 x 128 tiles leave room for 4 buffers: their steps are shorter than a load's way from memory (3,
+// 5 and 6 buffers took the same time). One tile a CU pays for its loads beside its MFMAs: M 1000, N
+// 4096, K 7168 MXFP8 x MXFP4 takes 33 us, 26 without its code loads, 29 without its scale loads, 20
+// with the MFMAs alone.
 // AL: K % 512 == 0, so that 16-byte pieces of the scale rows are aligned and also go by DMA.
 template <int FA_, int FB_, int BM_, int BN_, int WM_, int WN_, bool AL_, bool X_>
 struct Tile {

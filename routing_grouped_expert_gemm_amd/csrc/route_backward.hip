@@ -300,17 +300,19 @@ MOK_DEV bf16x8_t frag_t(uint32_t tile, int blk, int s, int lane) {
 //      where EM is 64 (two steps) or XC 256 (LDS), two. The tile goes through LDS in float32, half of
 //      its rows at a time, so that dx_in is read and dx written in whole row segments; dx_in is
 //      loaded before the product. Both pass the caches by (T 8192, d 2048, E 64: 36 -> 33 us).
+// PAD: x and w are copies in rows of ld, dx_in, dx and dW have rows of d, d % 8 != 0 (a form of its
+// own: decided in the kernel it cost the aligned one 5%).
 // 40 to 80 KB of LDS: 2 or 3 workgroups a CU cover each other's loads (256 experts a workgroup and
 // steps of 64, 112 KB and one workgroup a CU, took 113 us at T 4096, d 7168, E 256 where this takes
 // 93). There the tiles do 75 GFLOP, and wait for L2 most: 24 to 31% of the cycles are MFMAs, 37%
 // waits for loads, a quarter of the reads miss L2.
-template <int EM, int XC>
+template <int EM, int XC, bool PAD>
 __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
   constexpr int KT = 32;
   constexpr int PB = KT * EM * 2, XB = KT * XC * 2, WST = 3 * PB + XB;      // bytes of a dW step
   constexpr int DST = 2 * 128 * 64 + XB;                                // bytes of a dx step
   constexpr int OLD = XC + 4;                                             // floats of a staged row
-  constexpr int DN = XC == 256 || EM == 64 ? 2 : 3;                                  // buffers of dx
+  constexpr int DN = XC == 256 || EM == 64 ? 2 : 3;               // buffers of dx
   constexpr int BYTES = std::max(std::max(2 * WST, DN * DST), 64 * OLD * 4);
   __shared__ __align__(1024) char lds[BYTES];
   const uint32_t lds0 = uniform(lds_addr(lds));
@@ -318,7 +320,6 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
   constexpr std::integral_constant<int, XC / 8> CX{};
   const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
   const int h = lane >> 5, l = lane & 31;
-  const bool padded = a.ld != a.d;        // dx_in, dx and dW have rows of d
   // every wave's DMA has landed and its LDS reads are back
   auto publish = [&]() {
     __builtin_amdgcn_s_waitcnt(0x70);   // vmcnt(0) lgkmcnt(0)
@@ -417,8 +418,10 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
           if (e < a.E && c < a.d) {
             const float4 v = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1],
                                          acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-            if (c + 4 <= a.d) {
-              __builtin_memcpy(at, &v, 16);              // d % 4 != 0: not on 16 bytes
+            if constexpr (!PAD) {
+              *(float4*)at = v;
+            } else if (c + 4 <= a.d) {
+              __builtin_memcpy(at, &v, 16);
             } else {
               at[0] = v.x;
               if (c + 1 < a.d) at[1] = v.y;
@@ -441,7 +444,8 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
     in[i] = u32x4{0, 0, 0, 0};
     if (a.dx_in && t < a.T && c < a.d) {
       const bf16_t* at = a.dx_in + t * a.d + c;
-      in[i] = padded ? load_part(at, a.d - c) : __builtin_nontemporal_load((const u32x4*)at);
+      if constexpr (PAD) in[i] = load_part(at, a.d - c);
+      else in[i] = __builtin_nontemporal_load((const u32x4*)at);
     }
   }
   const int wt = (wid >> 1) * 64, wc = (wid & 1) * 32 * FC;
@@ -540,7 +544,7 @@ __global__ __launch_bounds__(RB_NT, 2) void k_route_bwd_tile(const RbTile a) {
         o[n] = pack_bf16x2(__uint_as_float(w[n] << 16) + s[2 * n],
                            __uint_as_float(w[n] & 0xFFFF0000u) + s[2 * n + 1]);
       bf16_t* at = a.dx + t * a.d + c;
-      if (padded) store_part(at, a.d - c, o);
+      if constexpr (PAD) store_part(at, a.d - c, o);
       else __builtin_nontemporal_store(o, (u32x4*)at);
     }
   }
@@ -701,8 +705,13 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
       t.x = to;
       t.w = to + T * p.ld;
     }
-    auto k = p.XC == 256 ? (p.EM == 64 ? k_route_bwd_tile<64, 256> : k_route_bwd_tile<128, 256>)
-                         : (p.EM == 64 ? k_route_bwd_tile<64, 128> : k_route_bwd_tile<128, 128>);
+    auto pick = [&](auto PAD) {
+      constexpr bool pad = PAD();
+      return p.XC == 256
+                 ? (p.EM == 64 ? k_route_bwd_tile<64, 256, pad> : k_route_bwd_tile<128, 256, pad>)
+                 : (p.EM == 64 ? k_route_bwd_tile<64, 128, pad> : k_route_bwd_tile<128, 128, pad>);
+    };
+    auto k = p.copies ? pick(std::true_type{}) : pick(std::false_type{});
     launch_k(k, dim3((unsigned)n), dim3(RB_NT), 0, s, nullptr, nullptr, t);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
     if (dw_router && p.ranges > 1)
