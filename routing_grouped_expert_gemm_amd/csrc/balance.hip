@@ -290,14 +290,17 @@ __global__ __launch_bounds__(BAL_NT) void k_balance_bwd(
     const int64_t a = max(done, a0), b = min(hi, b0);
     if (a >= b) continue;
     zero(done, a);
+    // f counted from the mean count: sum_e p = 1, so the gradient is the same, but where the counts
+    // are nearly equal nothing cancels (all equal, k = E for one: zeros, not rounding errors of p)
     const float n = (float)(b0 - a0);
+    const int32_t mean = (int32_t)((b0 - a0) * k / E);
     float f[NC][W];
 #pragma unroll
     for (int q = 0; q < NC; ++q)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const int e = (q * L + l) * W + i;
-        f[q][i] = e < E ? (float)counts[(int64_t)s * E + e] * ((float)E / ((float)k * n)) : 0.0f;
+        f[q][i] = e < E ? (float)(counts[(int64_t)s * E + e] - mean) * ((float)E / ((float)k * n)) : 0.0f;
       }
     const float c = up / n;
     for (int64_t t0 = a + w * R; t0 < b; t0 += BAL_W * R) {

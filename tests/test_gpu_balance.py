@@ -98,6 +98,31 @@ def test_against_float64(T, E, k, off):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,E,off", [(512, 8, None), (300, 5, [0, 7, 7, 200, 290]), (33, 1, None),
+                                     (5000, 64, None)])
+def test_equal_counts_leave_no_gradient(T, E, off):
+    """k = E: every count is the mean one and the gradient zero, exactly. With one pick less it is
+    off by at most 4 u of c p (|g| + sum |g| p), g = f - E (mean count) / (k n): g is one rounding off
+    and nothing cancels but it."""
+    import routing_grouped_expert_gemm_amd as mok
+    g = torch.Generator().manual_seed(T + E)
+    logits = torch.randn(T, E, generator=g) * 2
+    idx = torch.stack([torch.randperm(E, generator=g) for _ in range(T)]).int()
+    assert not run(mok, logits, idx, off, E, 0.01)[3].any()
+    idx[3, 0] = -1
+    dl = run(mok, logits, idx, off, E, 0.01)[3].numpy()
+    _, counts, _, rd, _ = reference(logits, idx, off, E, 0.01)
+    bounds = [0, T] if off is None else off
+    p = torch.softmax(logits.double(), 1).numpy()
+    spread = float((logits.amax(1) - logits.amin(1)).max())
+    u = (16 + 2 * spread + 40) * 2.0 ** -24
+    for s, (a, b) in enumerate(zip(bounds, bounds[1:])):
+        if a < b:
+            gs = np.abs(counts[s] / (b - a) - 1.0)
+            scale = 0.01 / ((len(bounds) - 1) * (b - a)) * p[a:b] * (gs + (p[a:b] * gs).sum(1, keepdims=True))
+            assert (np.abs(dl[a:b] - rd[a:b]) <= 4 * u * scale + 1e-15 * 0.01 / (b - a)).all()
+
+
 def test_masked_logits_and_invalid_picks():
     """-inf logits, the type's lowest value, a row of nothing but -inf, picks outside [0, E) and a
     pick named twice; tokens of no sequence may hold anything, NaN included."""
