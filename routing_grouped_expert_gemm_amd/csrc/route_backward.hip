@@ -7,13 +7,14 @@
 //
 // (w = softmax over a token's picks, so its gradient is the softmax's.) The picks are held
 // fixed. dW's token sum is cut into ranges whose partial sums a last launch adds in order: no
-// atomics, the same bits every run. Two forms:
+// atomics, the same bits every run. Three forms:
 //
 //  k_route_bwd_any  any type, size and alignment: 64 x 64 tiles of both products on the float32 MFMA
 //    (operands and sums in float32), 4 waves of 32 x 32, K steps of 32 through LDS, the next step's
 //    values loaded into registers under the MFMAs. dl is written once in float32 (DL), or, where
 //    T d E < 2^27, built by each workgroup in LDS from the given dlogits and the picks, which saves
 //    a launch (float32, T 257, d 272, E 20: 12 against 15 us; T 508, d 4864, E 182: 63 against 46).
+//  k_route_bwd_few  up to 16 experts, large, where the plane form does not apply: a stream.
 //  k_route_bwd_tile  bf16 rows of d % 8 == 0, or of any d where there is much to do, x and the weight
 //    then copied to such rows (k_route_bwd_pad): dl is written once as three bf16 planes that sum to
 //    it (8 + 8 + 8 significant bits: 24, all of float32's), and both products run on the bf16
@@ -165,6 +166,68 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_any(const RbArgs a) {
       if (e < a.E && c < a.d) out[(int64_t)e * a.d + c] = acc[v];
     }
   }
+}
+
+// ------------------------------------------------------------------------- few experts
+// Up to EC experts: both products are a stream of x, dx_in and dx with E multiply-adds a value each,
+// so a thread holds a column (its E weights and E sums of dW) and walks over the tokens of range
+// blockIdx.y, 8 tokens' loads in flight; dl of 64 tokens at a time lies in LDS. (The 64 x 64 tiles
+// do a full tile's products for any E: T 3757, d 6119, float32 took 186 us in them for E 4 and 136 for
+// E 16, in this 71 and 98; T 1300, d 379, E 4: 12 and 16, hence T d >= 2^22.)
+template <class T, int EC>
+__global__ __launch_bounds__(RB_NT) void k_route_bwd_few(const RbArgs a) {
+  constexpr int U = 8;
+  __shared__ float dls[64][EC];
+  const int tid = threadIdx.x, c = blockIdx.x * RB_NT + tid;
+  const bool in = c < a.d;
+  const T* x = a.dw ? (const T*)a.x : nullptr;
+  const T* dx_in = a.dx ? (const T*)a.dx_in : nullptr;
+  T* dx = (T*)a.dx;
+  float wv[EC], acc[EC];
+#pragma unroll
+  for (int e = 0; e < EC; ++e) {
+    wv[e] = dx && in && e < a.E ? load_as_f32((const T*)a.w + (int64_t)e * a.d + c) : 0.0f;
+    acc[e] = 0.0f;
+  }
+  const int64_t tb = blockIdx.y * a.t_range, te = min(a.T, tb + a.t_range);
+  for (int64_t t0 = tb; t0 < te; t0 += 64) {
+    __syncthreads();                  // the last tokens' dl has been read
+    if (tid < 64) {
+      const int64_t t = t0 + tid;
+#pragma unroll
+      for (int e = 0; e < EC; ++e)
+        dls[tid][e] = a.dlogits && t < te && e < a.E ? a.dlogits[t * a.E + e] : 0.0f;
+      if (t < te) each_pick(a, t, [&](int e, float g) { dls[tid][e] += g; });
+    }
+    __syncthreads();
+    const int nt = (int)min((int64_t)64, te - t0);
+    for (int u0 = 0; u0 < nt; u0 += U) {
+      float xv[U], o[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool ok = in && u0 + u < nt;
+        const int64_t at = (t0 + u0 + u) * a.d + c;
+        xv[u] = x && ok ? load_as_f32(x + at) : 0.0f;
+        o[u] = dx_in && ok ? load_as_f32(dx_in + at) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < EC; ++e) {
+          const float g = dls[u0 + u][e];
+          acc[e] += g * xv[u];
+          s += g * wv[e];
+        }
+        if (dx && in && u0 + u < nt) dx[(t0 + u0 + u) * a.d + c] = f32_to<T>(o[u] + s);
+      }
+    }
+  }
+  if (!a.dw || !in) return;
+  float* out = a.dw + ((int64_t)blockIdx.y * a.E) * a.d + c;
+#pragma unroll
+  for (int e = 0; e < EC; ++e)
+    if (e < a.E) out[(int64_t)e * a.d] = acc[e];
 }
 
 // ------------------------------------------------------------------------- bf16 planes
@@ -567,6 +630,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // The any-size form's shapes: dl (if written) padded to whole tiles; dW's token ranges, as many as
 // give about two workgroups a CU, each of at least 64 tokens.
 struct RbAny {
+  bool few;                           // k_route_bwd_few
   bool write_dl;
   int EP;
   int64_t Tp, ranges, t_range;
@@ -577,10 +641,13 @@ RbAny rb_any(int64_t T, int d, int E) {
   p.EP = (int)cdiv(E, RB_TILE) * RB_TILE;
   p.Tp = cdiv(T, RB_TILE) * RB_TILE;
   const int64_t tiles = cdiv(d, RB_TILE) * cdiv(E, RB_TILE);
-  const int64_t n = std::max<int64_t>(1, std::min(cdiv(512, tiles), cdiv(T, 64)));
-  p.t_range = std::max<int64_t>(1, cdiv(cdiv(T, n), RB_K)) * RB_K;
+  p.few = E <= 16 && T * d >= (int64_t)1 << 22;
+  const int64_t n = std::max<int64_t>(
+      1, std::min(p.few ? cdiv(1024, cdiv(d, RB_NT)) : cdiv(512, tiles), cdiv(T, 64)));
+  const int unit = p.few ? 64 : RB_K;
+  p.t_range = std::max<int64_t>(1, cdiv(cdiv(T, n), unit)) * unit;
   p.ranges = std::max<int64_t>(1, cdiv(T, p.t_range));
-  p.write_dl = (double)T * d * E >= (double)(1 << 27);
+  p.write_dl = !p.few && (double)T * d * E >= (double)(1 << 27);
   p.dl = p.write_dl ? (size_t)p.Tp * p.EP * sizeof(float) : 0;
   p.total = std::max<size_t>(256, p.dl + (p.ranges > 1 ? (size_t)p.ranges * E * d * sizeof(float) : 0));
   return p;
@@ -728,6 +795,20 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
   a.t_range = p.t_range;
   float* const part = (float*)((char*)ws + p.dl);
   a.dw = p.ranges > 1 ? part : dw_router;
+  if (p.few) {
+    const bool bf = io_dtype == MOK_BF16;
+    if (!dw_router) a.dw = nullptr;
+    auto kern = E <= 4   ? (bf ? k_route_bwd_few<bf16_t, 4> : k_route_bwd_few<float, 4>)
+                : E <= 8 ? (bf ? k_route_bwd_few<bf16_t, 8> : k_route_bwd_few<float, 8>)
+                         : (bf ? k_route_bwd_few<bf16_t, 16> : k_route_bwd_few<float, 16>);
+    launch_k(kern, dim3((unsigned)cdiv(d, RB_NT), (unsigned)p.ranges), dim3(RB_NT), 0, s, nullptr,
+             nullptr, a);
+    if (hipGetLastError() != hipSuccess) return MOK_EHIP;
+    if (dw_router && p.ranges > 1)
+      launch_k(k_route_bwd_sum, dim3(sum_grid), dim3(256), 0, s, nullptr, nullptr,
+               (const float*)part, (int)p.ranges, elems, dw_router);
+    return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EHIP;
+  }
   const int64_t grid = a.dx_tiles + (dw_router ? p.ranges * a.tiles_e * a.tiles_d : 0);
   const int64_t n_dl = cdiv(p.Tp * (p.EP / 8), 256);
   if (grid * RB_NT >= (int64_t)1 << 32 || n_dl * 256 >= (int64_t)1 << 32) return MOK_EUNSUPPORTED;

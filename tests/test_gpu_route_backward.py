@@ -96,6 +96,22 @@ def test_against_float64(T, d, E, k, dtype):
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,d,E,k", [(2100, 2003, 7, 3), (70000, 61, 5, 5), (4200, 1000, 8, 8),
+                                     (65, 65539, 4, 2), (4195000, 1, 1, 1), (1100, 4001, 16, 4),
+                                     (4100, 1030, 1, 1)])
+def test_few_experts(T, d, E, k, dtype):
+    import routing_grouped_expert_gemm_amd as mok
+    i = inputs(T, d, E, k, dtype)
+    dx, dw = run(mok, i)
+    check(dx, dw, reference(i), T, E, k, TYPES[dtype])
+    for want in ("dx", "dw"):
+        a, b = run(mok, i, want=(want,))
+        assert torch.equal(a, dx) if want == "dx" else torch.equal(b, dw)
+    dx, dw = run(mok, i, False, False)
+    check(dx, dw, reference(i, False, False), T, E, k, TYPES[dtype])
+
+
 @pytest.mark.parametrize("T,d,E,k", WIDE)
 def test_wide_against_float64(T, d, E, k):
     import routing_grouped_expert_gemm_amd as mok
@@ -135,7 +151,8 @@ def test_picks_outside_and_repeated(dtype):
     check(dx, dw, reference(i), T, E, k, TYPES[dtype])
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 50), ("bf16", 13625), ("fp32", 64)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 50), ("bf16", 13625), ("fp32", 64),
+                                     ("fp32", 54473)])
 def test_dx_over_dx_in_and_rows_behind(dtype, d):
     import routing_grouped_expert_gemm_amd as mok
     T, E, k = 77, 64, 6
