@@ -14,7 +14,7 @@
 //    values loaded into registers under the MFMAs. dl is written once in float32 (DL), or, where
 //    T d E < 2^27, built by each workgroup in LDS from the given dlogits and the picks, which saves
 //    a launch (float32, T 257, d 272, E 20: 12 against 15 us; T 508, d 4864, E 182: 63 against 46).
-//  k_route_bwd_few  up to 16 experts, large, where the plane form does not apply: a stream.
+//  k_route_bwd_few  float32, up to 16 experts, large: a stream.
 //  k_route_bwd_tile  bf16 rows of d % 8 == 0, or of any d where there is much to do, x and the weight
 //    then copied to such rows (k_route_bwd_pad): dl is written once as three bf16 planes that sum to
 //    it (8 + 8 + 8 significant bits: 24, all of float32's), and both products run on the bf16
@@ -169,24 +169,24 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_any(const RbArgs a) {
 }
 
 // ------------------------------------------------------------------------- few experts
-// Up to EC experts: both products are a stream of x, dx_in and dx with E multiply-adds a value each,
+// Float32 rows, up to EC experts: both products are a stream of x, dx_in and dx with E multiply-adds a value each,
 // so a thread holds a column (its E weights and E sums of dW) and walks over the tokens of range
 // blockIdx.y, 8 tokens' loads in flight; dl of 64 tokens at a time lies in LDS. (The 64 x 64 tiles
 // do a full tile's products for any E: T 3757, d 6119, float32 took 186 us in them for E 4 and 136 for
 // E 16, in this 71 and 98; T 1300, d 379, E 4: 12 and 16, hence T d >= 2^22.)
-template <class T, int EC>
+template <int EC>
 __global__ __launch_bounds__(RB_NT) void k_route_bwd_few(const RbArgs a) {
   constexpr int U = 8;
   __shared__ float dls[64][EC];
   const int tid = threadIdx.x, c = blockIdx.x * RB_NT + tid;
   const bool in = c < a.d;
-  const T* x = a.dw ? (const T*)a.x : nullptr;
-  const T* dx_in = a.dx ? (const T*)a.dx_in : nullptr;
-  T* dx = (T*)a.dx;
+  const float* x = a.dw ? (const float*)a.x : nullptr;
+  const float* dx_in = a.dx ? (const float*)a.dx_in : nullptr;
+  float* dx = (float*)a.dx;
   float wv[EC], acc[EC];
 #pragma unroll
   for (int e = 0; e < EC; ++e) {
-    wv[e] = dx && in && e < a.E ? load_as_f32((const T*)a.w + (int64_t)e * a.d + c) : 0.0f;
+    wv[e] = dx && in && e < a.E ? ((const float*)a.w)[(int64_t)e * a.d + c] : 0.0f;
     acc[e] = 0.0f;
   }
   const int64_t tb = blockIdx.y * a.t_range, te = min(a.T, tb + a.t_range);
@@ -207,8 +207,8 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_few(const RbArgs a) {
       for (int u = 0; u < U; ++u) {
         const bool ok = in && u0 + u < nt;
         const int64_t at = (t0 + u0 + u) * a.d + c;
-        xv[u] = x && ok ? load_as_f32(x + at) : 0.0f;
-        o[u] = dx_in && ok ? load_as_f32(dx_in + at) : 0.0f;
+        xv[u] = x && ok ? x[at] : 0.0f;
+        o[u] = dx_in && ok ? dx_in[at] : 0.0f;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_few(const RbArgs a) {
           acc[e] += g * xv[u];
           s += g * wv[e];
         }
-        if (dx && in && u0 + u < nt) dx[(t0 + u0 + u) * a.d + c] = f32_to<T>(o[u] + s);
+        if (dx && in && u0 + u < nt) dx[(t0 + u0 + u) * a.d + c] = o[u] + s;
       }
     }
   }
@@ -636,12 +636,12 @@ struct RbAny {
   int64_t Tp, ranges, t_range;
   size_t dl, total;                   // bytes; the partial sums follow dl
 };
-RbAny rb_any(int64_t T, int d, int E) {
+RbAny rb_any(int64_t T, int d, int E, bool f32) {
   RbAny p;
   p.EP = (int)cdiv(E, RB_TILE) * RB_TILE;
   p.Tp = cdiv(T, RB_TILE) * RB_TILE;
   const int64_t tiles = cdiv(d, RB_TILE) * cdiv(E, RB_TILE);
-  p.few = E <= 16 && T * d >= (int64_t)1 << 22;
+  p.few = f32 && E <= 16 && T * d >= (int64_t)1 << 22;
   const int64_t n = std::max<int64_t>(
       1, std::min(p.few ? cdiv(1024, cdiv(d, RB_NT)) : cdiv(512, tiles), cdiv(T, 64)));
   const int unit = p.few ? 64 : RB_K;
@@ -687,9 +687,10 @@ RbPlan rb_plan(int64_t T, int d, int E) {
 
 // bf16 rows that the plane form takes: whole pieces of 16 bytes, or, where the products outweigh a
 // launch more and a copy of x and the weight in such rows, any (T 257, d 275, E 20: 12.6 us in the
-// any-size form, 15.9 in this; T 512, d 1069, E 64: 19.4 and 18.8; T 5536, d 1069, E 212: 153 and 53).
+// any-size form, 15.9 in this; T 512, d 1069, E 64: 19.4 and 18.8; T 5536, d 1069, E 212: 153 and 53;
+// T 2100, d 2003, E 1: 44 and 25).
 bool rb_tiled(int64_t T, int d, int E) {
-  return d % 8 == 0 || (double)T * d * E >= (double)(1 << 25);
+  return d % 8 == 0 || T * d >= 1 << 22 || (double)T * d * E >= (double)(1 << 25);
 }
 
 int rb_check(int64_t T, int32_t d, int32_t E, int32_t k, int32_t io_dtype) {
@@ -709,7 +710,7 @@ extern "C" {
 int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t io_dtype,
                                        size_t* bytes) {
   if (!bytes || rb_check(T, d, E, 1, io_dtype) != MOK_OK) return MOK_EINVAL;
-  size_t need = rb_any(T, d, E).total;
+  size_t need = rb_any(T, d, E, io_dtype == MOK_FP32).total;
   if (io_dtype == MOK_BF16 && T > 0 && rb_tiled(T, d, E)) need = std::max(need, rb_plan(T, d, E).total);
   *bytes = need;
   return MOK_OK;
@@ -786,7 +787,7 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
                (const float*)t.dw, (int)p.ranges, elems, dw_router);
     return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EHIP;
   }
-  const RbAny p = rb_any(T, d, E);
+  const RbAny p = rb_any(T, d, E, io_dtype == MOK_FP32);
   a.dl = (const float*)ws;
   a.EP = p.EP;
   a.tiles_d = (int)cdiv(d, RB_TILE);
@@ -796,11 +797,8 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
   float* const part = (float*)((char*)ws + p.dl);
   a.dw = p.ranges > 1 ? part : dw_router;
   if (p.few) {
-    const bool bf = io_dtype == MOK_BF16;
     if (!dw_router) a.dw = nullptr;
-    auto kern = E <= 4   ? (bf ? k_route_bwd_few<bf16_t, 4> : k_route_bwd_few<float, 4>)
-                : E <= 8 ? (bf ? k_route_bwd_few<bf16_t, 8> : k_route_bwd_few<float, 8>)
-                         : (bf ? k_route_bwd_few<bf16_t, 16> : k_route_bwd_few<float, 16>);
+    auto kern = E <= 4 ? k_route_bwd_few<4> : E <= 8 ? k_route_bwd_few<8> : k_route_bwd_few<16>;
     launch_k(kern, dim3((unsigned)cdiv(d, RB_NT), (unsigned)p.ranges), dim3(RB_NT), 0, s, nullptr,
              nullptr, a);
     if (hipGetLastError() != hipSuccess) return MOK_EHIP;
