@@ -450,10 +450,11 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
  * MOK_MXFP4, in any combination. c [M, N] bf16 or float32 (out_dtype: MOK_BF16, MOK_FP32), rounded
  * once from float32 sums. Products are exact but for operands in MXFP8: the matrix instruction adds
  * a block's products on a grid 13 bits below the largest, which leaves 1.5e-5 of the result's norm
- * for two MXFP8 operands, 5e-6 for one with bf16 results, and less than 1e-7 with float32 ones
- * (which then take twice the instructions). K % 32 == 0, 32 <= K <= 2^22; M, N >= 0, < 2^31
+ * for two MXFP8 operands and 5e-6 for one with bf16 results. With float32 results one MXFP8 operand's
+ * products are exact too (they take two instructions). K % 32 == 0, 32 <= K <= 2^22; M, N >= 0, < 2^31
  * (and fewer than 2^23 tiles of 128 x 128; up to 64 rows: N <= 2^27). Codes and c start on 16 bytes.
- * A scale of 0xFF (NaN) or a NaN code makes what it enters NaN. ws: device scratch of mok_mx_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned (0 bytes:
+ * A scale of 0xFF (NaN) or a NaN code makes what it enters NaN.
+ * ws: device scratch of mok_mx_gemm_workspace_bytes(M, N, K) bytes, 16-byte aligned (0 bytes:
  * may be NULL). Bit-identical reruns. */
 int mok_mx_gemm_workspace_bytes(int64_t M, int64_t N, int32_t K, size_t* bytes);
 int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype,

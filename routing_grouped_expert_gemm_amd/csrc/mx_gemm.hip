@@ -70,13 +70,19 @@ MOK_DEV f32x16_t mfma(const Frag<FB>& b, const Frag<FA>& a, f32x16_t acc, uint32
                                                          (int)bsc, SEL, (int)asc);
 }
 
-// The instruction adds the products of a 32-value block on a grid 13 bits below its largest one
-// (measured: 256 + 2^-5 is exact, 256 + 2^-6 gives 256) and rounds to float32 after that. E2M1
-// products span 8 bits and are exact. An E4M3 operand's span 18 binades: with an E2M1 one the
-// result is off by 4.6e-6 of its norm, far below bf16's 2^-9, but not below float32's. For float32
-// results (X) the E4M3 operand is therefore split at 8 into two, large values and small, each
-// within the grid but for values below 2^-7 of their scale, and the products are two instructions.
-// (Two E4M3 operands span 36 binades: 1.5e-5 of the norm, in either output type.)
+// The instruction adds the products of a 32-value block on a grid 13 bits below the largest sum of
+// two exponents (a subnormal has its type's least exponent) and cuts each product off there, towards
+// zero, then rounds to float32 (so measured for every pair of two values). A block thus loses less
+// than 32 2^-13 = 2^-8 of its largest product, subnormals counted as their type's smallest normal.
+// E2M1 products span 8 bits and are exact. An E4M3 operand spans 18 binades: on normal rows two of
+// them leave 1.5e-5 of the result's norm, one beside an E2M1 operand 5e-6, far below bf16's 2^-9, but
+// not below float32's. For float32 results (X) the E4M3 operand of a mixed pair is therefore split at
+// 4 into two, and the products are two instructions, both exact:
+//   below 4: exponents -6 .. 1, multiples of 2^-9; with E2M1 (exponents 0 .. 2, multiples of 1/2) the
+//     products are multiples of 2^-10 and the grid is at most 2^(1 + 2 - 13);
+//   4 to 448: exponents 2 .. 8, products multiples of 2^-2, the grid at most 2^(8 + 2 - 13).
+// (Split at 8, values below 2^-6 lost their last bit beside 4 to 7.5. Two E4M3 operands would need
+// twelve instructions.)
 MOK_DEV Frag<F8> large_of(const Frag<F8>& v) {
   Frag<F8> o;
 #pragma unroll
@@ -84,8 +90,8 @@ MOK_DEV Frag<F8> large_of(const Frag<F8>& v) {
     uint32_t w[4] = {v.q[i].x, v.q[i].y, v.q[i].z, v.q[i].w};
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      // per byte: all ones where the code without its sign is at least 0x50 (the value 8)
-      const uint32_t ge = (((w[n] & 0x7F7F7F7Fu) + 0x30303030u) >> 7) & 0x01010101u;
+      // per byte: all ones where the code without its sign is at least 0x48 (the value 4)
+      const uint32_t ge = (((w[n] & 0x7F7F7F7Fu) + 0x38383838u) >> 7) & 0x01010101u;
       w[n] &= (ge << 8) - ge;
     }
     o.q[i] = make_uint4(w[0], w[1], w[2], w[3]);
