@@ -63,3 +63,75 @@ def test_float32_results_of_mixed_pairs_lose_no_product(fa, fb):
     ref = s[:, None] * u[None, :]
     assert torch.equal(gemm(mok, a, one[0], b, one[1], torch.float32).double(), ref)
     assert torch.equal(gemm(mok, b, one[1], a, one[0], torch.float32).double(), ref.T)
+
+
+def rows(M, K, fmt, g, scales=(120, 134)):
+    """Any finite codes, the larger ones more often: (codes, scales, values, their u)."""
+    t, tiny = table(fmt)
+    if fmt == 4:
+        c = torch.randint(0, 16, (M, K), generator=g, device=DEV)
+    else:
+        c = torch.randint(0, 127, (M, K), generator=g, device=DEV)
+        c = torch.where(torch.rand(M, K, generator=g, device=DEV) < 0.3, c % 16 + 111, c)
+        c = c + 128 * torch.randint(0, 2, (M, K), generator=g, device=DEV)
+    sc = torch.randint(*scales, (M, K // 32), generator=g, device=DEV)
+    v = t[c]
+    f = torch.exp2(sc.double() - 127)[:, :, None]
+    u = torch.where(v == 0, 0.0, v.abs().clamp(min=tiny))
+    return (packed(c.to(torch.uint8), fmt), sc.to(torch.uint8),
+            (v.view(M, -1, 32) * f).view(M, K), (u.view(M, -1, 32) * f).view(M, K))
+
+
+@pytest.mark.parametrize("fa,fb", [(4, 4), (8, 4), (4, 8), (8, 8)])
+@pytest.mark.parametrize("M,N,K", [(40, 50, 32), (48, 40, 320), (90, 70, 32), (100, 70, 352), (70, 66, 2048)])
+def test_any_codes_within_the_blocks_grid(M, N, K, fa, fb):
+    """Every block may lose 2^-8 of its largest u(a) u(b) (nothing with an E2M1 operand and a
+    float32 result); K / 32 sums in float32 and the output type's half step come on top. The
+    instruction takes two blocks, whose sums are rounded, each to float32, into the accumulator:
+    (K / 32 + 8) 2^-23 of sum |a b|."""
+    import routing_grouped_expert_gemm_amd as mok
+    g = torch.Generator(device=DEV).manual_seed(M + N + K + fa * 3 + fb)
+    (a, asc, av, au), (b, bsc, bv, bu) = rows(M, K, fa, g), rows(N, K, fb, g)
+    b[1], bsc[1], bv[1], bu[1] = (t[0] for t in (b, bsc, bv, bu))
+    ref, mag = torch.zeros(M, N, dtype=torch.float64, device=DEV), torch.zeros(M, N, dtype=torch.float64, device=DEV)
+    lost = torch.zeros_like(ref)
+    for k in range(0, K, 32):
+        p = av[:, None, k:k + 32] * bv[None, :, k:k + 32]
+        ref += p.sum(2)
+        mag += p.abs().sum(2)
+        lost += (au[:, None, k:k + 32] * bu[None, :, k:k + 32]).amax(2) * 2.0 ** -8
+    sums = (K / 32 + 8) * 2.0 ** -23 * mag
+    for dtype in (torch.float32, torch.bfloat16):
+        exact = fa == fb == 4 or (dtype is torch.float32 and (fa == 4 or fb == 4))
+        got = gemm(mok, a, asc, b, bsc, dtype).double()
+        tol = sums + (0.0 if exact else lost)
+        if dtype is torch.bfloat16:
+            tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+        assert ((got - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fa,fb,most", [(8, 8, 1.5e-5), (8, 4, 1e-7), (4, 8, 1e-7), (4, 4, 1e-7)])
+def test_error_on_normal_rows(fa, fb, most):
+    """The documented errors' norms on quantised normal rows (float32 results), and how often a
+    bf16 result is not the rounded exact one: an error of 5e-6 moves it over a border of two values,
+    which lie 2^-8 of it apart or more, with a chance of 5e-6 2^8 = 0.13% at the norm, and more for
+    smaller results, whose steps are smaller: below 1%. (The float32 error of K / 32 sums: its random
+    roundings sqrt(K / 16) 2^-24 and as much again.)"""
+    import routing_grouped_expert_gemm_amd as mok
+    M, N, K = 400, 320, 4096
+    g = torch.Generator(device=DEV).manual_seed(fa * 10 + fb)
+    ops, vals = [], []
+    for n, f in ((M, fa), (N, fb)):
+        x = torch.randn(n, K, generator=g, device=DEV).to(torch.bfloat16)
+        c = torch.empty((n, K if f == 8 else K // 2), dtype=torch.uint8, device=DEV)
+        s = torch.empty((n, K // 32), dtype=torch.uint8, device=DEV)
+        (mok.mok_quantize_mxfp8 if f == 8 else mok.mok_quantize_mxfp4)(x, c, s)
+        ops += [c, s]
+        c = c.long() if f == 8 else torch.stack([c & 15, c >> 4], 2).view(n, K).long()
+        vals.append((table(f)[0][c].view(n, -1, 32) * torch.exp2(s.double() - 127)[:, :, None]).view(n, K))
+    ref = vals[0] @ vals[1].T.contiguous()
+    err = gemm(mok, *ops, torch.float32).double() - ref
+    assert float(err.norm() / ref.norm()) <= max(1.25 * most, 4 * (K / 16 + 8) ** 0.5 * 2.0 ** -24)
+    got = gemm(mok, *ops, torch.bfloat16)
+    off = float((got != ref.float().to(torch.bfloat16)).double().mean())
+    assert off <= (0.03 if fa == fb == 8 else 0.01)
