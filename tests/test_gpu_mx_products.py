@@ -135,3 +135,51 @@ def test_error_on_normal_rows(fa, fb, most):
     got = gemm(mok, *ops, torch.bfloat16)
     off = float((got != ref.float().to(torch.bfloat16)).double().mean())
     assert off <= (0.03 if fa == fb == 8 else 0.01)
+
+
+def exact_operand(M, K, fmt, g):
+    """Codes on the E2M1 grid under scales 1 and 2: products are multiples of 1/4 of at most 144, and
+    sums of up to 2^14.5 of them are below 2^24 quarters: exact in float32 in any order."""
+    nib = torch.randint(0, 16, (M, K), generator=g, device=DEV)
+    val = table(4)[0][nib]
+    sc = torch.randint(127, 129, (M, K // 32), generator=g, device=DEV)
+    if fmt == 4:
+        codes = packed(nib.to(torch.uint8), 4)
+    else:
+        by_nib = table(4)[0].float().cpu().to(torch.float8_e4m3fn).view(torch.uint8).to(DEV)
+        codes = by_nib[nib]
+    return codes, sc.to(torch.uint8), (val.view(M, -1, 32) * torch.exp2(sc.double() - 127)[:, :, None]).view(M, K)
+
+
+def moved(t):
+    """The same bytes one past a 16-byte address."""
+    b = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+    b[1:] = t.flatten()
+    return b[1:].view(t.shape)
+
+
+LONG = [  # M, N, K, scales off 16 bytes
+    # 196 tiles of 256 x 256: scales by DMA in 3 and 5 groups of 32 blocks, through registers (off 16
+    # bytes; K not a multiple of 512, with a ragged last step)
+    (3400, 3500, 2560, False), (3400, 3520, 4608, False), (3400, 3520, 2560, True),
+    (3400, 3500, 2592, False), (3390, 3520, 4128, False), (3400, 3500, 544, False),
+    # 48 tiles of 128 x 128, one range of K: 6 groups of scales by DMA (they turn over four buffers)
+    # and through registers
+    (700, 904, 5632, False), (700, 900, 5632, True), (700, 904, 5664, False), (700, 904, 1536, False),
+    # 30 tiles: 4 ranges of K of 5 and more groups each; 6 tiles: 7 and 16 ranges
+    (700, 600, 20480, False), (700, 600, 20512, False), (130, 260, 7168, True), (130, 260, 16384, False),
+    # up to 64 rows
+    (33, 40, 20480, True), (1, 100, 20512, False)]
+
+
+@pytest.mark.parametrize("fa,fb", [(4, 4), (8, 4), (4, 8), (8, 8)])
+@pytest.mark.parametrize("M,N,K,off", LONG)
+def test_long_k_in_every_tile_form(M, N, K, off, fa, fb):
+    import routing_grouped_expert_gemm_amd as mok
+    g = torch.Generator(device=DEV).manual_seed(M + N + K + fa * 3 + fb)
+    (a, asc, av), (b, bsc, bv) = exact_operand(M, K, fa, g), exact_operand(N, K, fb, g)
+    if off:
+        asc, bsc = moved(asc), moved(bsc)
+    ref = av @ bv.T.contiguous()
+    assert torch.equal(gemm(mok, a, asc, b, bsc, torch.float32).double(), ref)
+    assert torch.equal(gemm(mok, a, asc, b, bsc, torch.bfloat16), ref.float().to(torch.bfloat16))
