@@ -407,10 +407,12 @@ int mok_balance_loss_backward(const float* logits, const int32_t* counts, int64_
  * Backward, g = dy weight, n = h rstd:
  *   dx[t,i] = rstd[t] (g[t,i] - n[t,i] mean_j(g[t,j] n[t,j])) + dh[t,i]
  *   dweight[i] = sum_t dy[t,i] n[t,i]
- * h, rstd: the forward's. dh [rows, d]: the gradient that reaches h from the residual stream
- * (NULL: none). dx is the gradient of both x and residual. dx [rows, d] in the storage type; it
- * may be dy or dh. dweight [d] float32, overwritten (zeros with rows == 0), NULL: not wanted (then
- * ws may be NULL). No atomics: bit-identical reruns. ws: device scratch, 16-byte aligned. */
+ * h, rstd: the forward's. Where 1 / rms is past float32 (eps 0 and a root mean square below 3e-39) the
+ * forward's rstd is an infinity; the backward then takes it from h. dh [rows, d]: the gradient that
+ * reaches h from the residual stream (NULL: none). dx is the gradient of both x and residual. dx
+ * [rows, d] in the storage type; it may be dy or dh. dweight [d] float32, overwritten (zeros with
+ * rows == 0), NULL: not wanted (then ws may be NULL). No atomics: bit-identical reruns. ws: device
+ * scratch, 16-byte aligned. */
 int mok_rmsnorm(const void* x, const void* residual, const void* weight, int64_t rows, int32_t d,
                 int32_t io_dtype, float eps, void* h, float* rstd, void* y, uint8_t* codes,
                 uint8_t* scales, void* stream);

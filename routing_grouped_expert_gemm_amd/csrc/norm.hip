@@ -235,6 +235,20 @@ __global__ __launch_bounds__(NT) void k_rmsnorm_any(
     for (int i = threadIdx.x; i < d; i += NT) y[at + i] = f32_to<T>(y_at(i));
 }
 
+// The backward's rstd of a row: the forward's, or, where that is an infinity (a root mean square below
+// 3e-39, which needs eps 0), what the norm multiplied by, from sum(), the row's sum of squares in
+// float64: h is then taken times scale. Every thread that meets in sum() is given the same rstd.
+struct BwdScale {
+  float rs, scale;
+  template <class Sum> MOK_DEV BwdScale(float rstd, int d, Sum&& sum) : rs(rstd), scale(1.0f) {
+    if (rstd == INFINITY) {
+      const RowScale q(1.0 / sqrt(sum() / d));
+      rs = q.r;
+      scale = q.scale;
+    }
+  }
+};
+
 // Backward over rows blockIdx.x * RPB + ..., stepping by the whole grid: dweight's sums stay in
 // registers from row to row. part [gridDim.x, d]: this workgroup's share of dweight (NULL: none).
 template <class T, int TPR, int NC>
@@ -244,6 +258,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm_bwd(
     float* __restrict__ part) {
   constexpr int NT = TPR > NORM_NT ? TPR : NORM_NT, RPB = NT / TPR;
   __shared__ float sh[2][NT / 64];
+  __shared__ double shd[NT / 64];
   __shared__ float fold[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NC * 8 : 1];
   const int l = threadIdx.x % TPR, r = threadIdx.x / TPR;
   float w[NC][8], acc[NC][8];
@@ -277,7 +292,6 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm_bwd(
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += stride) {
     const int64_t row = r0 + r, at = row * d;
     const bool live = row < rows;
-    const float rs = rs_next;
     float n_[NC][8], g[NC][8], o[NC][8], dot = 0.0f;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
@@ -285,6 +299,20 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm_bwd(
       Piece<T>::widen(gq[n], g[n]);
       Piece<T>::widen(oq[n], o[n]);
     }
+    const BwdScale q(rs_next, d, [&] {
+      double ss = 0.0;
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fma((double)n_[n][i], (double)n_[n][i], ss);
+      return row_total<TPR>(ss, shd);         // the sum of dot lies between two uses of shd
+    });
+    const float rs = q.rs;
+    if (q.scale != 1.0f)
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n_[n][i] *= q.scale;
     rs_next = fetch(row + stride);
 #pragma unroll
     for (int n = 0; n < NC; ++n)
@@ -302,7 +330,10 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm_bwd(
       const int c = (n * TPR + l) * 8;
       if (live && c < d) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[n][i] += rs * (g[n][i] - n_[n][i] * dot);
+        for (int i = 0; i < 8; ++i) {
+          const float v = g[n][i] - n_[n][i] * dot;
+          o[n][i] = q.scale == 1.0f ? fmaf(rs, v, o[n][i]) : fmaf(q.scale, rs * v, o[n][i]);
+        }
         Piece<T>::store(dx + at + c, o[n]);
       }
     }
@@ -328,18 +359,41 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_rmsnorm_bwd(
   }
 }
 
+// A thread's share of a row's sum of squares, NT threads to a row.
+template <int NT, class T> MOK_DEV double squares(const T* h, int d) {
+  double ss = 0.0;
+  for (int i = threadIdx.x; i < d; i += NT) {
+    const double v = load_as_f32(h + i);
+    ss = fma(v, v, ss);
+  }
+  return ss;
+}
+
 // Any d and alignment, first launch: workgroup (x, y) sums dweight's columns 256 x .. over the
 // rows y, y + gridDim.y, ... It runs before dx is written, which may lie where dy does.
 template <class T>
 __global__ __launch_bounds__(NORM_NT) void k_rmsnorm_dw_any(const T* dy, const T* h,
                                                             const float* rstd, int64_t rows, int d,
                                                             float* part) {
-  const int c = blockIdx.x * NORM_NT + threadIdx.x;
-  if (c >= d) return;
-  float v = 0.0f;
-  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y)
-    v += load_as_f32(dy + row * d + c) * (load_as_f32(h + row * d + c) * rstd[row]);
-  part[(int64_t)blockIdx.y * d + c] = v;
+  __shared__ double shd[NORM_NT / 64];
+  const int c = blockIdx.x * NORM_NT + threadIdx.x, at = min(c, d - 1);
+  float v = 0.0f, top = 0.0f;                 // top: the largest rstd, the same in every thread
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const float rs = rstd[row];
+    top = fmaxf(top, rs);
+    v += load_as_f32(dy + row * d + at) * (load_as_f32(h + row * d + at) * rs);
+  }
+  if (top == INFINITY) {                      // once more, with rstd from h where it is an infinity
+    v = 0.0f;
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+      const BwdScale q(rstd[row], d, [&] {
+        __syncthreads();                      // shd of a row before has been read
+        return row_total<NORM_NT>(squares<NORM_NT>(h + row * d, d), shd);
+      });
+      v += load_as_f32(dy + row * d + at) * (load_as_f32(h + row * d + at) * q.scale * q.rs);
+    }
+  }
+  if (c < d) part[(int64_t)blockIdx.y * d + c] = v;
 }
 
 template <class T, int NT>
@@ -347,16 +401,30 @@ __global__ __launch_bounds__(NT) void k_rmsnorm_bwd_any(const T* dy, const T* h,
                                                              const float* rstd, const T* weight,
                                                              const T* dh, int d, T* dx) {
   __shared__ float sh[NT / 64];
+  __shared__ double shd[NT / 64];
   const int64_t row = blockIdx.x, at = row * d;
+  auto rest = [&](float rs, auto SCALED, float scale) {
+    auto h_at = [&](int i) {
+      const float v = load_as_f32(h + at + i);
+      return SCALED() ? v * scale : v;
+    };
+    float dot = 0.0f;
+    for (int i = threadIdx.x; i < d; i += NT)
+      dot += load_as_f32(dy + at + i) * load_as_f32(weight + i) * (h_at(i) * rs);
+    dot = row_total<NT>(dot, sh) / (float)d;
+    for (int i = threadIdx.x; i < d; i += NT) {
+      const float g = load_as_f32(dy + at + i) * load_as_f32(weight + i);
+      float o = rs * (g - h_at(i) * rs * dot);
+      if constexpr (SCALED()) o *= scale;
+      dx[at + i] = f32_to<T>(o + (dh ? load_as_f32(dh + at + i) : 0.0f));
+    }
+  };
   const float rs = rstd[row];
-  float dot = 0.0f;
-  for (int i = threadIdx.x; i < d; i += NT)
-    dot += load_as_f32(dy + at + i) * load_as_f32(weight + i) * (load_as_f32(h + at + i) * rs);
-  dot = row_total<NT>(dot, sh) / (float)d;
-  for (int i = threadIdx.x; i < d; i += NT) {
-    const float g = load_as_f32(dy + at + i) * load_as_f32(weight + i);
-    const float o = rs * (g - load_as_f32(h + at + i) * rs * dot);
-    dx[at + i] = f32_to<T>(o + (dh ? load_as_f32(dh + at + i) : 0.0f));
+  if (rs != INFINITY) {
+    rest(rs, std::integral_constant<bool, false>{}, 1.0f);
+  } else {
+    const BwdScale q(rs, d, [&] { return row_total<NT>(squares<NT>(h + at, d), shd); });
+    rest(q.rs, std::integral_constant<bool, true>{}, q.scale);
   }
 }
 
