@@ -435,8 +435,11 @@ int mok_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const
  * dx may be dx_in, and overlaps nothing else. Sums in float32 (bf16 operands enter as they are,
  * dl with at least 16 significant bits for dx and 24 for dw_router); each output is rounded once;
  * no atomics: bit-identical reruns. Every token's row of x and every dtopk_w entry is read; infinite
- * or NaN values in them (or in w_router) make what they enter NaN. Sizes as mok_route, d <= 2^24,
- * T k < 2^31.
+ * or NaN values in them (or in w_router) make what they enter NaN. mok_moe_backward of a share
+ * (E_l < E) writes dtopk_w at its local routes only: the others must be zeroed before (MoeBackward
+ * does). The outputs are linear in dtopk_w, dlogits and dx_in, so that the shares' dx and dw_router
+ * add up to the layer's, dlogits and dx_in given to one share or summed over all. Sizes as mok_route,
+ * d <= 2^24, T k < 2^31.
  * ws: device scratch of mok_route_backward_workspace_bytes(...) bytes, 16-byte aligned. */
 int mok_route_backward_workspace_bytes(int64_t T, int32_t d, int32_t E, int32_t io_dtype,
                                        size_t* bytes);

@@ -549,7 +549,9 @@ class MoeBackward:
     """Argument struct, workspace and outputs of one backward configuration (mok_moe_backward).
 
     Whole layer: pass dy [T_pool, d]. Share: dy_slots [T_pool*k, d] and dy_shared [T_own, d].
-    Outputs: dx_slots, dx_shared, dx (whole layer), dtopk_w, dw_* and dws_* (float32)."""
+    Outputs: dx_slots, dx_shared, dx (whole layer), dtopk_w, dw_* and dws_* (float32). A share's
+    dtopk_w is zero at the routes of other experts, so that mok_route_backward gives its part of the
+    gradients: the shares' parts add up to the layer's."""
 
     def __init__(self, *, d: int, E: int, k: int, I: int, e0: int, E_l: int,
                  tokens_per_rank: int, T_pool: int, own_begin: int, T_own: int, n_shared: int,
@@ -595,6 +597,12 @@ class MoeBackward:
         self.args = a
 
     def backward(self, stream=None) -> None:
+        if self.args.E_l < self.args.E:        # the call writes dtopk_w at its local routes only
+            import torch
+            at = stream if stream is None or isinstance(stream, torch.cuda.Stream) \
+                else torch.cuda.ExternalStream(stream)
+            with torch.cuda.stream(at):
+                self.dtopk_w.zero_()
         _check("mok_moe_backward", _lib.mok_moe_backward(ctypes.byref(self.args), _stream(stream)))
 
     def device_error(self, stream=None) -> int:
