@@ -14,7 +14,7 @@
 //    values loaded into registers under the MFMAs. dl is written once in float32 (DL), or, where
 //    T d E < 2^27, built by each workgroup in LDS from the given dlogits and the picks, which saves
 //    a launch (float32, T 257, d 272, E 20: 12 against 15 us; T 508, d 4864, E 182: 63 against 46).
-//  k_route_bwd_few  float32, up to 16 experts, large: a stream.
+//  k_route_bwd_few  float32, up to 16 experts (8 of narrow rows), large: a stream.
 //  k_route_bwd_tile  bf16 rows of d % 8 == 0, or of any d where there is much to do, x and the weight
 //    then copied to such rows (k_route_bwd_pad): dl is written once as three bf16 planes that sum to
 //    it (8 + 8 + 8 significant bits: 24, all of float32's), and both products run on the bf16
@@ -169,11 +169,11 @@ __global__ __launch_bounds__(RB_NT) void k_route_bwd_any(const RbArgs a) {
 }
 
 // ------------------------------------------------------------------------- few experts
-// Float32 rows, up to EC experts: both products are a stream of x, dx_in and dx with E multiply-adds a value each,
-// so a thread holds a column (its E weights and E sums of dW) and walks over the tokens of range
-// blockIdx.y, 8 tokens' loads in flight; dl of 64 tokens at a time lies in LDS. (The 64 x 64 tiles
-// do a full tile's products for any E: T 3757, d 6119, float32 took 186 us in them for E 4 and 136 for
-// E 16, in this 71 and 98; T 1300, d 379, E 4: 12 and 16, hence T d >= 2^22.)
+// Float32 rows, up to EC experts: both products are a stream of x, dx_in and dx with E multiply-adds
+// a value each, so a thread holds a column (its E weights and E sums of dW) and walks over the tokens
+// of range blockIdx.y, 8 tokens' loads in flight; dl of 64 tokens at a time lies in LDS. (The 64 x 64
+// tiles do a full tile's products for any E: T 3757, d 6119, float32 took 186 us in them for E 4 and
+// 136 for E 16, in this 71 and 98; T 1300, d 379, E 4: 12 and 16, hence T d >= 2^22.)
 template <int EC>
 __global__ __launch_bounds__(RB_NT) void k_route_bwd_few(const RbArgs a) {
   constexpr int U = 8;
@@ -641,7 +641,10 @@ RbAny rb_any(int64_t T, int d, int E, bool f32) {
   p.EP = (int)cdiv(E, RB_TILE) * RB_TILE;
   p.Tp = cdiv(T, RB_TILE) * RB_TILE;
   const int64_t tiles = cdiv(d, RB_TILE) * cdiv(E, RB_TILE);
-  p.few = f32 && E <= 16 && T * d >= (int64_t)1 << 22;
+  // a column a thread: narrow rows leave threads idle, which costs the form of 16 experts most
+  // (float32, few and any-size form: T 70,000, d 61, E 5: 57 and 56 us, E 16: 85 and 56; T 40,000, d 128,
+  // E 4: 46 and 52, E 16: 65 and 53; T 24,000, d 192, E 16: 40 and 50; T 300,000, d 16, E 4: 110 and 139)
+  p.few = f32 && (E <= 8 || (E <= 16 && d > 128)) && T * d >= (int64_t)1 << 22;
   const int64_t n = std::max<int64_t>(
       1, std::min(p.few ? cdiv(1024, cdiv(d, RB_NT)) : cdiv(512, tiles), cdiv(T, 64)));
   const int unit = p.few ? 64 : RB_K;

@@ -73,6 +73,8 @@ def run(mok, i, dx_in=True, dlogits=True, dtw=None):
 CASES = [  # T, d, E
     # few experts
     (2100, 2003, 7), (70000, 61, 5), (4195000, 1, 1), (1100, 4001, 16), (16383, 257, 1), (40001, 129, 4),
+    # 9 to 16 experts, narrow and wider rows
+    (70001, 61, 16), (40000, 128, 9), (40001, 129, 16),
     # the plane form, tiles of 128 and 256 columns, rows that are copied
     (8192, 512, 64), (8190, 520, 130), (98300, 8, 64), (16500, 1416, 20), (16400, 1288, 130),
     (98300, 11, 64), (33000, 3, 1000), (16500, 1417, 20), (16400, 1283, 130), (1030, 1020, 64),
