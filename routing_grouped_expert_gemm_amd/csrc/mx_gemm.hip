@@ -75,14 +75,17 @@ MOK_DEV f32x16_t mfma(const Frag<FB>& b, const Frag<FA>& a, f32x16_t acc, uint32
 // zero, then rounds to float32 (so measured for every pair of two values). A block thus loses less
 // than 32 2^-13 = 2^-8 of its largest product, subnormals counted as their type's smallest normal.
 // E2M1 products span 8 bits and are exact. An E4M3 operand spans 18 binades: on normal rows two of
-// them leave 1.5e-5 of the result's norm, one beside an E2M1 operand 5e-6, far below bf16's 2^-9, but
-// not below float32's. For float32 results (X) the E4M3 operand of a mixed pair is therefore split at
-// 4 into two, and the products are two instructions, both exact:
+// them leave 1.5e-5 of the result's norm, one beside an E2M1 operand 5e-6. In the mixed pair (X) the
+// E4M3 operand can be split at 4 into two, and the products are two instructions, both exact:
 //   below 4: exponents -6 .. 1, multiples of 2^-9; with E2M1 (exponents 0 .. 2, multiples of 1/2) the
 //     products are multiples of 2^-10 and the grid is at most 2^(1 + 2 - 13);
 //   4 to 448: exponents 2 .. 8, products multiples of 2^-2, the grid at most 2^(8 + 2 - 13).
 // (Split at 8, values below 2^-6 lost their last bit beside 4 to 7.5. Two E4M3 operands would need
-// twelve instructions.)
+// twelve instructions.) That is done for float32 results, and for up to 64 rows, where it costs next to
+// nothing (MXFP8 x MXFP4, bf16 results, N 4096, K 7168, M 64: 20.5 and 21.4 us, M 1, N 7168, K 2048: 8.3
+// and 8.4). Above, bf16 results take one instruction: two double the time (M 1000: 32 and 65 us, M 8192:
+// 175 and 327), and 5e-6 is a 300th of what the rounding to bf16 leaves (0.4% of the results are the
+// neighbour of the exact sum's rounding).
 MOK_DEV Frag<F8> large_of(const Frag<F8>& v) {
   Frag<F8> o;
 #pragma unroll
@@ -173,8 +176,9 @@ MOK_DEV void store4(const MxArgs& p, void* c, bool f32, int m, int n, float4 v) 
 // order. B is read once over the grid.
 constexpr int KS = 8;
 
-template <int FA, int FB, int MT, bool X>
+template <int FA, int FB, int MT>
 __global__ __launch_bounds__(64 * KS) void k_mx_rows(const MxArgs p) {
+  constexpr bool X = FA != FB;
   __shared__ float4 red[KS][MT][4][64];
   const int lane = lane_id(), w = uniform(threadIdx.x >> 6), h = lane >> 5, r = lane & 31;
   const int n0 = blockIdx.x * 32, m0 = blockIdx.y * 32 * MT;
@@ -696,7 +700,7 @@ template <int FA, int FB, bool X>
 hipError_t run_mx(MxArgs p, const Plan& t, float* part, void* c, hipStream_t s) {
   if (t.rows) {
     p.c = c;
-    auto k = p.M <= 32 ? k_mx_rows<FA, FB, 1, X> : k_mx_rows<FA, FB, 2, X>;
+    auto k = p.M <= 32 ? k_mx_rows<FA, FB, 1> : k_mx_rows<FA, FB, 2>;
     launch_k(k, dim3((unsigned)cdiv(p.N, 32)), dim3(64 * KS), 0, s, nullptr, nullptr, p);
     return hipGetLastError();
   }
