@@ -599,9 +599,8 @@ class MoeBackward:
     def backward(self, stream=None) -> None:
         if self.args.E_l < self.args.E:        # the call writes dtopk_w at its local routes only
             import torch
-            at = stream if stream is None or isinstance(stream, torch.cuda.Stream) \
-                else torch.cuda.ExternalStream(stream)
-            with torch.cuda.stream(at):
+            with torch.cuda.stream(stream if stream is None
+                                   else torch.cuda.ExternalStream(_stream(stream))):
                 self.dtopk_w.zero_()
         _check("mok_moe_backward", _lib.mok_moe_backward(ctypes.byref(self.args), _stream(stream)))
 

@@ -39,11 +39,11 @@ def into_router(mok, v, dtopk_w):
     return dx, dw
 
 
-@pytest.mark.parametrize("how", ["current", "stream", "handle"])
+@pytest.mark.parametrize("how", ["current", "stream", "handle", "default"])
 def test_shares_add_up(how):
     import routing_grouped_expert_gemm_amd as mok
     side = torch.cuda.Stream()
-    stream = dict(current=None, stream=side, handle=side.cuda_stream)[how]
+    stream = dict(current=None, stream=side, handle=side.cuda_stream, default=0)[how]
     v = layer(1)
     parts = [(0, 5), (5, 6), (6, 16)]
     shares = [experts(mok, v, *p) for p in parts]
