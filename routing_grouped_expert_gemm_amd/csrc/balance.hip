@@ -290,10 +290,11 @@ __global__ __launch_bounds__(BAL_NT) void k_balance_bwd(
     const int64_t a = max(done, a0), b = min(hi, b0);
     if (a >= b) continue;
     zero(done, a);
-    // f counted from the mean count: sum_e p = 1, so the gradient is the same, but where the counts
-    // are nearly equal nothing cancels (all equal, k = E for one: zeros, not rounding errors of p)
+    // f counted from the mean count, to the nearest: sum_e p = 1, so the gradient is the same, but
+    // where the counts are nearly equal nothing cancels (all equal, k = E for one: zeros, not rounding
+    // errors of p; one token, 5 of 6 experts: counted from 0, 1 - p of the sixth lost p's bits)
     const float n = (float)(b0 - a0);
-    const int32_t mean = (int32_t)((b0 - a0) * k / E);
+    const int32_t mean = (int32_t)(((b0 - a0) * k + E / 2) / E);
     float f[NC][W];
 #pragma unroll
     for (int q = 0; q < NC; ++q)
