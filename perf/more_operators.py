@@ -168,7 +168,8 @@ def prepare(case, seed):
         st["w_pre"] = (1.0 + normal(d, scale=0.1)).to(t) if case["pre"] else None
         st["gate"] = None
         if case["gate"] != "none":
-            st["gate"] = torch.sigmoid(normal(T if case["gate"] == "row" else 1, d)).to(t)
+            shape = (T, d) if case["gate"] == "row" else (d,)     # one value a token, or for all
+            st["gate"] = torch.sigmoid(normal(*shape)).to(t)
         if case["train"]:
             st["dh"] = normal(T, d, dtype=t)
             st["dn"] = normal(T, d, dtype=t) if case["pre"] else None
@@ -360,7 +361,7 @@ def _own_gnorm(mok, st):
             st["dres"], st["dy"] = torch.empty_like(y), torch.empty_like(y)
             st["dgate"] = None
             if c["gate"] != "none":
-                st["dgate"] = torch.empty_like(y) if c["gate"] == "row" else _empty(1, d)
+                st["dgate"] = torch.empty_like(y) if c["gate"] == "row" else _empty(d)
             st["dw_post"] = _empty(d) if c["post"] else None
             st["dw_pre"] = _empty(d) if c["pre"] else None
             st["ws"] = _empty(mok.mok_gated_norm_backward_workspace_bytes(T, d),
@@ -382,7 +383,7 @@ def _own_gnorm(mok, st):
         out["dw_pre"] = st["dw_pre"]
     out["dres"] = st["dres"]
     if st["gate"] is not None:
-        out["dgate"] = st["dgate"] if c["gate"] == "row" else st["dgate"][0]
+        out["dgate"] = st["dgate"]
     if c["post"]:
         out["dw_post"] = st["dw_post"]
     out["dy"] = st["dy"]
@@ -503,7 +504,7 @@ def exact(case, seed):
         return v / torch.sqrt(torch.linalg.vector_norm(v, dim=1) ** 2 / c["d"] + EPS)[:, None]
 
     wp = torch.ones(c["d"], dtype=D, device=DEV) if not c["post"] else st["w_post"].to(D)
-    gate = torch.ones(1, c["d"], dtype=D, device=DEV) if st["gate"] is None else st["gate"].to(D)
+    gate = torch.ones(c["d"], dtype=D, device=DEV) if st["gate"] is None else st["gate"].to(D)
     leaves = [v.detach().requires_grad_(c["train"]) for v in (y, res, wp, gate)]
     with torch.enable_grad():
         a = unit(leaves[0]) if c["post"] else leaves[0]
@@ -524,7 +525,7 @@ def exact(case, seed):
         up = up + dh
     dy, out["dres"], dwp, dgate = torch.autograd.grad(hs, leaves, up)
     if st["gate"] is not None:
-        out["dgate"] = dgate if c["gate"] == "row" else dgate[0]
+        out["dgate"] = dgate
     if c["post"]:
         out["dw_post"] = dwp
     out["dy"] = dy
