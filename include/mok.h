@@ -432,6 +432,8 @@ int mok_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const
  * [T, d]: float32 or bf16 (io_dtype); topk_idx [T, k] int32, topk_w, dtopk_w [T, k] and dlogits
  * (NULL: none) float32; dw_router [E, d] float32, overwritten (zeros with T == 0). dx or dw_router
  * may be NULL where not wanted. Picks outside [0, E) take no part; an expert named twice adds up.
+ * topk_idx, topk_w and dtopk_w all NULL, with dlogits: dl is dlogits alone (a gradient that has gone
+ * through the picks already, as mok_topk_scored_backward's).
  * dx may be dx_in, and overlaps nothing else. Sums in float32 (bf16 operands enter as they are,
  * dl with at least 16 significant bits for dx and 24 for dw_router); each output is rounded once;
  * no atomics: bit-identical reruns. Every token's row of x and every dtopk_w entry is read; infinite
@@ -471,6 +473,133 @@ int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype
                 const uint8_t* b_codes, const uint8_t* b_scales, int32_t b_dtype, int64_t M,
                 int64_t N, int32_t K, int32_t out_dtype, void* c, void* ws, size_t ws_bytes,
                 void* stream);
+
+/* ---------------------------------------------------------------- routing by scores
+ * The choice of experts from scores, with a bias for balance and groups of experts: the rule beside
+ * mok_topk's. For each token, with l its logits:
+ *   s[e] = 1 / (1 + exp(-l[e]))  (MOK_SCORE_SIGMOID)  or  softmax(l)[e]  (MOK_SCORE_SOFTMAX)
+ *   c[e] = s[e] + bias[e]        (bias [E] float32, NULL: none; it decides the choice alone)
+ * The experts form n_groups groups of E / n_groups neighbours. A group's worth is the sum of its
+ * group_top (1 or 2) largest c; the topk_groups groups of most worth are kept, and the picks are the
+ * k largest c in them, in descending order. Ties, of groups as of experts, go to the lower id.
+ *   w[j] = scale s[idx[j]]            renorm: scale s[idx[j]] / sum_i s[idx[i]] (0 where the sum is 0)
+ * Scores, c and worths are those of float64 arithmetic; w is rounded once. An expert with l or bias
+ * -inf is left out: it adds nothing to its group's worth and is picked only where fewer than k others
+ * are left in the kept groups (a row that leaves nothing picks the lowest ids, with weights 0 where l
+ * is -inf). NaN counts as larger than any number, in c and in a worth, so that it reaches the
+ * weights; +inf logits make a softmax row NaN.
+ *   logits [T, E] float32, topk_idx [T, k] int32, topk_w [T, k] float32
+ * Requires 1 <= k <= E <= 1024, k <= 64, T k < 2^31, E % n_groups == 0, 1 <= topk_groups <= n_groups,
+ * k <= topk_groups E / n_groups, a finite scale.
+ * mok_route_scored: the router projection of mok_route (the same logits, bit for bit), then the
+ * choice. */
+#define MOK_SCORE_SOFTMAX 0
+#define MOK_SCORE_SIGMOID 1
+int mok_topk_scored(const float* logits, int64_t T, int32_t E, int32_t k, int32_t score,
+                    const float* bias, int32_t n_groups, int32_t topk_groups, int32_t group_top,
+                    int32_t renorm, float scale, int32_t* topk_idx, float* topk_w, void* stream);
+int mok_route_scored(const void* x, const void* w_router, int64_t T, int32_t d, int32_t E,
+                     int32_t k, int32_t io_dtype, int32_t score, const float* bias,
+                     int32_t n_groups, int32_t topk_groups, int32_t group_top, int32_t renorm,
+                     float scale, float* logits, int32_t* topk_idx, float* topk_w, void* stream);
+/* The gradient for the logits with the picks held fixed:
+ *   dlogits[t,e] = dlogits_in[t,e] + sum_j dtopk_w[t,j] d w[t,j] / d l[t,e]
+ * dlogits_in [T, E] (NULL: zeros; the balance loss's gradient): dlogits may be the same buffer, and
+ * overlaps nothing else. Picks outside [0, E) take no part, neither in a renormalising sum; an expert
+ * named twice adds up. A row whose scores sum to 0 has a zero gradient. Feed the result to
+ * mok_route_backward as its dlogits, without picks. No atomics: bit-identical reruns. */
+int mok_topk_scored_backward(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
+                             const float* dlogits_in, int64_t T, int32_t E, int32_t k,
+                             int32_t score, int32_t renorm, float scale, float* dlogits,
+                             void* stream);
+
+/* ---------------------------------------------------------------- gated norm
+ * The join of a block's output y to the residual stream, and the norm that the next block reads:
+ *   u = y rstd_y w_post    rstd_y = 1 / sqrt(mean_i y[t,i]^2 + eps)    (w_post NULL: u = y)
+ *   h = alpha residual + beta gate u, rounded to the storage type      (gate NULL: 1)
+ *   n = h rstd_h w_pre     rstd_h = 1 / sqrt(mean_i h[t,i]^2 + eps)    (w_pre NULL: no n)
+ * gate: [d], one for all tokens, or, gate_per_row, [rows, d]. y, residual, gate, w_post [d], w_pre
+ * [d], h, n: float32 or bf16 (io_dtype); rstd_y, rstd_h [rows] float32, for the backward (NULL: not
+ * wanted). n NULL with w_pre: rstd_h alone. h may be y or residual, n may be y or residual where h is
+ * not the same one; other overlaps are not allowed. Statistics in float64. d, rows, eps and the
+ * read-once forms as mok_rmsnorm; rows past 2^21 take the slower form. alpha, beta finite.
+ *
+ * Backward, from dh (what reaches h from the residual stream) and dn (either may be NULL: none):
+ *   dt = dh + rstd_h (g - nh mean(g nh)),  g = dn w_pre, nh = h rstd_h;    dw_pre[i] = sum_t dn nh
+ *   dres = alpha dt;   dgate = beta dt u;   q = beta dt gate
+ *   dw_post[i] = sum_t q v,  v = y rstd_y;   dy = rstd_y (p - v mean(p v)),  p = q w_post
+ * (w_post NULL: dy = q). dgate: of a gate per row [rows, d] in the storage type, of one for all its
+ * sum over the rows, [d] float32. dw_post, dw_pre [d] float32 (zeros with rows == 0; dw_pre zeros
+ * without dn). Outputs that are NULL are not wanted; they overlap neither inputs nor each other.
+ * rstd_y, rstd_h, h: the forward's (an infinite rstd as in mok_rmsnorm_backward); needed with w_post,
+ * with dn, with dn. No atomics: bit-identical reruns. ws: device scratch, 16-byte aligned, of
+ * mok_gated_norm_backward_workspace_bytes(rows, d) bytes (NULL with none of the sums wanted). */
+int mok_gated_norm(const void* y, const void* w_post, const void* gate, int32_t gate_per_row,
+                   const void* residual, const void* w_pre, int64_t rows, int32_t d,
+                   int32_t io_dtype, float eps, float alpha, float beta, void* h, void* n,
+                   float* rstd_y, float* rstd_h, void* stream);
+int mok_gated_norm_backward_workspace_bytes(int64_t rows, int32_t d, size_t* bytes);
+int mok_gated_norm_backward(const void* dh, const void* dn, const void* y, const void* h,
+                            const void* w_post, const void* gate, int32_t gate_per_row,
+                            const void* w_pre, const float* rstd_y, const float* rstd_h,
+                            int64_t rows, int32_t d, int32_t io_dtype, float alpha, float beta,
+                            void* dres, void* dy, void* dgate, float* dw_post, float* dw_pre,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- 4-bit weights in groups
+ * A weight W [N, K] as unsigned 4-bit codes with a scale, and optionally a zero point, for each group
+ * of 32, 64 or 128 neighbours along K:
+ *   W[n,k] = (q[n,k] - z[n, k / group]) s[n, k / group]
+ *   codes [N, K / 2]: two a byte, element 2i in the low nibble of byte i
+ *   scales [N, K / group] bf16;  zeros [N, K / group] uint8, NULL: 8 throughout
+ *
+ * mok_quantize_int4: rows of bf16 (16-byte aligned), in float32 arithmetic, each operation rounded to
+ * nearest even. Without zeros: s = bf16(max |w| / 7), q = clamp(rint(w / s) + 8, 0, 15). With zeros,
+ * hi and lo the largest and least of the group and 0: s = bf16(hi / 15 - lo / 15), z = clamp(rint(-lo
+ * / s), 0, 15), q = clamp(rint(w / s) + z, 0, 15). Where s is 0 the codes are z (8, or 0 with zeros).
+ * A group with an infinity or a NaN has scale NaN. */
+int mok_quantize_int4(const void* src_bf16, int64_t rows, int32_t K, int32_t group, uint8_t* codes,
+                      void* scales, uint8_t* zeros, void* stream);
+
+/* C[m,n] = sum_k x[m,k] W[n,k]: x [M, K] bf16, C [M, N] bf16 or float32 (out_dtype), rounded once.
+ * Made for few rows: the weight is streamed once for every 16. The products x (q - z) are exact,
+ * their sums and the scaling float32. An infinite or NaN x[m,k] makes row m NaN.
+ * K % group == 0, K <= 2^22, M <= 2^20, N <= 2^26 (MOK_EUNSUPPORTED past the last two, below 2^31).
+ * x and codes start on 16 bytes. Bit-identical reruns; no workspace. */
+int mok_w4_gemm(const void* x, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                int64_t M, int64_t N, int32_t K, int32_t group, int32_t out_dtype, void* c,
+                void* stream);
+
+/* The routed experts' FFNs of the layer on such weights, for the few tokens of a decoding step (each
+ * weight that some token picks is streamed once for every 16 of its tokens, 8 for the down
+ * projection; the others are not read):
+ *   y[t] = y_in[t] + sum_{j: local} w[t,j] W_down[e] (silu(W_gate[e] x[t]) * (W_up[e] x[t])),
+ *   e = topk_idx[t,j], local: e0 <= e < e0 + E_l, j ascending
+ * A share of the experts (E_l < E) gives its part of the sum. y_in: the shared experts' output or the
+ * residual stream (NULL: none). The hidden values stay float32 between the products (the down
+ * projection reads 16 bits of their significand), sums are float32, y is rounded once. Every route is
+ * computed; ids outside the local experts are skipped, an expert named twice counts twice. */
+typedef struct mok_moe_w4_args {
+  int64_t T;               /* tokens                                                        */
+  int32_t d, I;            /* model dim and expert intermediate: multiples of group         */
+  int32_t E, k;            /* routed experts in the layer, picks a token (k <= E, k <= 64)  */
+  int32_t e0, E_l;         /* local experts [e0, e0+E_l), E_l <= 1024                       */
+  int32_t group;           /* 32, 64 or 128, of all three weights                           */
+  const void* x;           /* [T, d] bf16, 16-byte aligned                                  */
+  const int32_t* topk_idx; /* [T, k]                                                        */
+  const float* topk_w;     /* [T, k]                                                        */
+  const uint8_t *gate_codes, *up_codes, *down_codes;   /* [E_l, I, d/2] (2x), [E_l, d, I/2]  */
+  const void *gate_scales, *up_scales, *down_scales;   /* bf16 [E_l, I, d/group] (2x),
+                                                          [E_l, d, I/group]                 */
+  const uint8_t *gate_zeros, *up_zeros, *down_zeros;   /* uint8, the scales' shapes; all NULL
+                                                          or none                           */
+  const void* y_in;        /* [T, d] bf16 or NULL                                           */
+  void* y;                 /* [T, d] bf16; may be x or y_in                                 */
+  void* workspace;         /* device, 16-byte aligned, >= mok_moe_w4_workspace_bytes        */
+  size_t workspace_bytes;
+} mok_moe_w4_args;
+int mok_moe_w4_workspace_bytes(const mok_moe_w4_args* args, size_t* bytes);
+int mok_moe_w4_forward(const mok_moe_w4_args* args, void* stream);
 
 /* ---------------------------------------------------------------- device error word
  * The persistent work loop bounds every wait; a wait that runs out sets a nonzero error word

@@ -28,6 +28,7 @@ MOK_N_STAGES = 7
  MOK_REGION_WD_CODES, MOK_REGION_WD_SCALES, MOK_REGION_SG_CODES, MOK_REGION_SG_SCALES,
  MOK_REGION_SU_CODES, MOK_REGION_SU_SCALES, MOK_REGION_SD_CODES, MOK_REGION_SD_SCALES) = range(17)
 MOK_DEVERR_OVERFLOW, MOK_DEVERR_WAIT = 1, 2
+MOK_SCORE_SOFTMAX, MOK_SCORE_SIGMOID = 0, 1
 
 EXPORTS = ["mok_status_string", "mok_version", "mok_route", "mok_topk",
            "mok_dispatch_plan_workspace_bytes", "mok_dispatch_plan", "mok_dispatch_plan_noalloc",
@@ -39,7 +40,10 @@ EXPORTS = ["mok_status_string", "mok_version", "mok_route", "mok_topk",
            "mok_balance_loss_workspace_bytes", "mok_balance_loss", "mok_balance_loss_backward",
            "mok_rmsnorm", "mok_rmsnorm_backward_workspace_bytes", "mok_rmsnorm_backward",
            "mok_route_backward_workspace_bytes", "mok_route_backward",
-           "mok_mx_gemm_workspace_bytes", "mok_mx_gemm"]
+           "mok_mx_gemm_workspace_bytes", "mok_mx_gemm",
+           "mok_topk_scored", "mok_route_scored", "mok_topk_scored_backward",
+           "mok_gated_norm", "mok_gated_norm_backward_workspace_bytes", "mok_gated_norm_backward",
+           "mok_quantize_int4", "mok_w4_gemm", "mok_moe_w4_workspace_bytes", "mok_moe_w4_forward"]
 
 
 class MokError(RuntimeError):
@@ -91,6 +95,18 @@ class BwdArgs(ctypes.Structure):
     ]
 
 
+class MoeW4Args(ctypes.Structure):
+    """Mirror of struct mok_moe_w4_args."""
+    _fields_ = [
+        ("T", _I64), ("d", _I32), ("I", _I32), ("E", _I32), ("k", _I32), ("e0", _I32),
+        ("E_l", _I32), ("group", _I32), ("x", _P), ("topk_idx", _P), ("topk_w", _P),
+        ("gate_codes", _P), ("up_codes", _P), ("down_codes", _P),
+        ("gate_scales", _P), ("up_scales", _P), ("down_scales", _P),
+        ("gate_zeros", _P), ("up_zeros", _P), ("down_zeros", _P),
+        ("y_in", _P), ("y", _P), ("workspace", _P), ("workspace_bytes", _SZ),
+    ]
+
+
 _lib.mok_status_string.argtypes = [ctypes.c_int]
 _lib.mok_status_string.restype = ctypes.c_char_p
 _lib.mok_version.argtypes = []
@@ -128,6 +144,18 @@ _lib.mok_route_backward_workspace_bytes.argtypes = [_I64, _I32, _I32, _I32, ctyp
 _lib.mok_route_backward.argtypes = [_P] * 7 + [_I64] + [_I32] * 4 + [_P, _P, _P, _SZ, _P]
 _lib.mok_mx_gemm_workspace_bytes.argtypes = [_I64, _I64, _I32, ctypes.POINTER(_SZ)]
 _lib.mok_mx_gemm.argtypes = [_P, _P, _I32, _P, _P, _I32, _I64, _I64, _I32, _I32, _P, _P, _SZ, _P]
+_RULE = [_I32, _P, _I32, _I32, _I32, _I32, _F32]     # score, bias, groups, renorm, scale
+_lib.mok_topk_scored.argtypes = [_P, _I64, _I32, _I32] + _RULE + [_P, _P, _P]
+_lib.mok_route_scored.argtypes = [_P, _P, _I64] + [_I32] * 4 + _RULE + [_P] * 4
+_lib.mok_topk_scored_backward.argtypes = [_P] * 4 + [_I64] + [_I32] * 4 + [_F32, _P, _P]
+_lib.mok_gated_norm.argtypes = ([_P, _P, _P, _I32, _P, _P, _I64, _I32, _I32] + [_F32] * 3 + [_P] * 5)
+_lib.mok_gated_norm_backward_workspace_bytes.argtypes = [_I64, _I32, ctypes.POINTER(_SZ)]
+_lib.mok_gated_norm_backward.argtypes = ([_P] * 6 + [_I32] + [_P] * 3 + [_I64, _I32, _I32, _F32, _F32]
+                                         + [_P] * 6 + [_SZ, _P])
+_lib.mok_quantize_int4.argtypes = [_P, _I64, _I32, _I32, _P, _P, _P, _P]
+_lib.mok_w4_gemm.argtypes = [_P] * 4 + [_I64, _I64, _I32, _I32, _I32, _P, _P]
+_lib.mok_moe_w4_workspace_bytes.argtypes = [ctypes.POINTER(MoeW4Args), ctypes.POINTER(_SZ)]
+_lib.mok_moe_w4_forward.argtypes = [ctypes.POINTER(MoeW4Args), _P]
 _lib.mok_get_device_error.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32), _P]
 for _n in EXPORTS:
     if _n not in ("mok_status_string", "mok_version"):
@@ -430,12 +458,13 @@ def mok_route_backward(x, w_router, topk_idx, topk_w, dtopk_w, dx=None, dw_route
                        dlogits=None, dx_in=None, stream=None) -> None:
     """Gradients through mok_route with the picks held fixed: dx [T, d] (dx_in added) and
     dw_router [E, d] float32 (with ws of mok_route_backward_workspace_bytes(T, d, E, x.dtype)
-    bytes), from dtopk_w [T, k] and, where given, dlogits [T, E]."""
+    bytes), from dtopk_w [T, k] and, where given, dlogits [T, E]; with topk_idx, topk_w and dtopk_w
+    None from dlogits alone."""
     import torch
     fn, f32 = "mok_route_backward", torch.float32
-    if x.dim() != 2 or w_router.dim() != 2 or topk_idx.dim() != 2:
+    if x.dim() != 2 or w_router.dim() != 2 or (topk_idx is not None and topk_idx.dim() != 2):
         _refuse(fn)
-    (T, d), E, k = x.shape, w_router.shape[0], topk_idx.shape[1]
+    (T, d), E, k = x.shape, w_router.shape[0], 1 if topk_idx is None else topk_idx.shape[1]
     t, dev, io = x.dtype, x.get_device(), _io_of(fn, x)
     _enqueue(fn, dev, _lib.mok_route_backward,
              (_arg(fn, x, t, (T, d), dev), _arg(fn, w_router, t, (E, d), dev),
@@ -471,6 +500,180 @@ def mok_mx_gemm(a_codes, a_scales, b_codes, b_scales, c, ws=None, *, stream=None
               MOK_MXFP8 if ca == K else MOK_MXFP4, _arg(fn, b_codes, u8, (N, cb), dev),
               _arg(fn, b_scales, u8, (N, nb), dev), MOK_MXFP8 if cb == K else MOK_MXFP4, M, N, K,
               out, _arg(fn, c, c.dtype, (M, N), dev), *_scratch(fn, ws, dev)), stream)
+
+
+def _score_of(fn: str, score: str) -> int:
+    if score == "sigmoid":
+        return MOK_SCORE_SIGMOID
+    if score != "softmax":
+        _refuse(fn)
+    return MOK_SCORE_SOFTMAX
+
+
+def mok_topk_scored(logits, k: int, topk_idx, topk_w, *, score: str = "sigmoid", bias=None,
+                    n_groups: int = 1, topk_groups: int = 1, group_top: int = 2,
+                    renorm: bool = True, scale: float = 1.0, stream=None) -> None:
+    """The k experts of each row of logits [T, E] float32 by their scores ("sigmoid" or "softmax")
+    plus bias [E] float32, out of the topk_groups best of n_groups groups: topk_idx [T, k] int32 and
+    topk_w [T, k] float32 (scores, renormalised over the picks if renorm, times scale)."""
+    import torch
+    fn, f32 = "mok_topk_scored", torch.float32
+    if logits.dim() != 2:
+        _refuse(fn)
+    (T, E), dev = logits.shape, logits.get_device()
+    _enqueue(fn, dev, _lib.mok_topk_scored,
+             (_arg(fn, logits, f32, (T, E), dev), T, E, k, _score_of(fn, score),
+              _arg(fn, bias, f32, (E,), dev), n_groups, topk_groups, group_top, renorm, scale,
+              _arg(fn, topk_idx, torch.int32, (T, k), dev), _arg(fn, topk_w, f32, (T, k), dev)),
+             stream)
+
+
+def mok_route_scored(x, w_router, k: int, logits, topk_idx, topk_w, *, score: str = "sigmoid",
+                     bias=None, n_groups: int = 1, topk_groups: int = 1, group_top: int = 2,
+                     renorm: bool = True, scale: float = 1.0, stream=None) -> None:
+    """Router projection of x [T, d] and w_router [E, d] (float32 or bf16), as mok_route's, into
+    logits [T, E] float32, then the choice of mok_topk_scored."""
+    import torch
+    fn, f32 = "mok_route_scored", torch.float32
+    if x.dim() != 2 or w_router.dim() != 2:
+        _refuse(fn)
+    (T, d), E, t, dev, io = x.shape, w_router.shape[0], x.dtype, x.get_device(), _io_of(fn, x)
+    _enqueue(fn, dev, _lib.mok_route_scored,
+             (_arg(fn, x, t, (T, d), dev), _arg(fn, w_router, t, (E, d), dev), T, d, E, k, io,
+              _score_of(fn, score), _arg(fn, bias, f32, (E,), dev), n_groups, topk_groups, group_top,
+              renorm, scale, _arg(fn, logits, f32, (T, E), dev),
+              _arg(fn, topk_idx, torch.int32, (T, k), dev), _arg(fn, topk_w, f32, (T, k), dev)),
+             stream)
+
+
+def mok_topk_scored_backward(logits, topk_idx, dtopk_w, dlogits, *, score: str = "sigmoid",
+                             renorm: bool = True, scale: float = 1.0, dlogits_in=None,
+                             stream=None) -> None:
+    """Gradient of mok_topk_scored's weights for the logits with the picks held fixed: dlogits
+    [T, E] float32 (overwritten; dlogits_in, which may be the same tensor, added) from dtopk_w
+    [T, k] float32."""
+    import torch
+    fn, f32 = "mok_topk_scored_backward", torch.float32
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        _refuse(fn)
+    (T, E), k, dev = logits.shape, topk_idx.shape[1], logits.get_device()
+    _enqueue(fn, dev, _lib.mok_topk_scored_backward,
+             (_arg(fn, logits, f32, (T, E), dev), _arg(fn, topk_idx, torch.int32, (T, k), dev),
+              _arg(fn, dtopk_w, f32, (T, k), dev), _arg(fn, dlogits_in, f32, (T, E), dev), T, E, k,
+              _score_of(fn, score), renorm, scale, _arg(fn, dlogits, f32, (T, E), dev)), stream)
+
+
+def _gate_shape(fn: str, gate, rows):
+    """(gate_per_row, shape) of a gate [d] for all rows or [T, d] of its own for each."""
+    if gate is not None and gate.dim() == 2:
+        return 1, rows
+    return 0, rows[1:]
+
+
+def mok_gated_norm(y, residual, eps: float, h, *, w_post=None, gate=None, w_pre=None, n=None,
+                   rstd_y=None, rstd_h=None, alpha: float = 1.0, beta: float = 1.0,
+                   stream=None) -> None:
+    """h = alpha residual + beta gate norm(y) w_post and n = norm(h) w_pre, for rows y [T, d] float32
+    or bf16; gate [d] or [T, d]; w_post None: y itself, gate None: 1, w_pre None: no n. rstd_y,
+    rstd_h [T] float32: for the backward."""
+    import torch
+    fn, f32 = "mok_gated_norm", torch.float32
+    if y.dim() != 2:
+        _refuse(fn)
+    rows, t, dev, io = tuple(y.shape), y.dtype, y.get_device(), _io_of(fn, y)
+    (T, d), (per, shape) = rows, _gate_shape(fn, gate, rows)
+    _enqueue(fn, dev, _lib.mok_gated_norm,
+             (_arg(fn, y, t, rows, dev), _arg(fn, w_post, t, (d,), dev),
+              _arg(fn, gate, t, shape, dev), per, _arg(fn, residual, t, rows, dev),
+              _arg(fn, w_pre, t, (d,), dev), T, d, io, eps, alpha, beta,
+              _arg(fn, h, t, rows, dev), _arg(fn, n, t, rows, dev), _arg(fn, rstd_y, f32, (T,), dev),
+              _arg(fn, rstd_h, f32, (T,), dev)), stream)
+
+
+def mok_gated_norm_backward_workspace_bytes(T: int, d: int) -> int:
+    out = _SZ(0)
+    _check("mok_gated_norm_backward_workspace_bytes",
+           _lib.mok_gated_norm_backward_workspace_bytes(T, d, ctypes.byref(out)))
+    return out.value
+
+
+def mok_gated_norm_backward(dh, y, dres=None, dy=None, ws=None, *, dn=None, h=None, gate=None,
+                            w_post=None, w_pre=None, rstd_y=None, rstd_h=None, dgate=None,
+                            dw_post=None, dw_pre=None, alpha: float = 1.0, beta: float = 1.0,
+                            stream=None) -> None:
+    """Backward of mok_gated_norm from dh (None: nothing reaches h but through n) and dn: dres, dy
+    [T, d], dgate ([T, d] in the rows' type for such a gate, [d] float32 for one of all rows), dw_post
+    and dw_pre [d] float32, those that are given; ws: mok_gated_norm_backward_workspace_bytes(T, d)
+    bytes where a sum over the rows is wanted."""
+    import torch
+    fn, f32 = "mok_gated_norm_backward", torch.float32
+    if y.dim() != 2:
+        _refuse(fn)
+    rows, t, dev, io = tuple(y.shape), y.dtype, y.get_device(), _io_of(fn, y)
+    (T, d), (per, shape) = rows, _gate_shape(fn, gate, rows)
+    _enqueue(fn, dev, _lib.mok_gated_norm_backward,
+             (_arg(fn, dh, t, rows, dev), _arg(fn, dn, t, rows, dev), _arg(fn, y, t, rows, dev),
+              _arg(fn, h, t, rows, dev), _arg(fn, w_post, t, (d,), dev),
+              _arg(fn, gate, t, shape, dev), per, _arg(fn, w_pre, t, (d,), dev),
+              _arg(fn, rstd_y, f32, (T,), dev), _arg(fn, rstd_h, f32, (T,), dev), T, d, io, alpha, beta,
+              _arg(fn, dres, t, rows, dev), _arg(fn, dy, t, rows, dev),
+              _arg(fn, dgate, t if per else f32, shape, dev), _arg(fn, dw_post, f32, (d,), dev),
+              _arg(fn, dw_pre, f32, (d,), dev), *_scratch(fn, ws, dev)), stream)
+
+
+def _w4_args(fn: str, codes, scales, zeros, lead, dev: int):
+    """(N, K, group, three pointers) of a 4-bit weight: codes lead + [N, K / 2] uint8, scales lead +
+    [N, K / group] bf16 and, unless None, zeros uint8 of the scales' shape."""
+    import torch
+    n = len(lead)
+    if codes.dim() != n + 2 or scales.dim() != n + 2 or scales.shape[-1] < 1:
+        _refuse(fn)
+    N, K, ng = codes.shape[-2], 2 * codes.shape[-1], scales.shape[-1]
+    shape = (*lead, N, ng)
+    return (N, K, K // ng if K % ng == 0 else -1, _arg(fn, codes, torch.uint8, (*lead, N, K // 2), dev),
+            _arg(fn, scales, torch.bfloat16, shape, dev), _arg(fn, zeros, torch.uint8, shape, dev))
+
+
+def mok_quantize_int4(src_bf16, codes, scales, zeros=None, stream=None) -> None:
+    """4-bit codes [rows, K / 2] uint8 of rows [rows, K] bf16, two a byte, with scales
+    [rows, K / group] bf16 and, if given, zero points uint8 of the same shape; the group (32, 64 or
+    128) is read from the shapes."""
+    import torch
+    fn = "mok_quantize_int4"
+    if src_bf16.dim() != 2:
+        _refuse(fn)
+    (rows, K), dev = src_bf16.shape, src_bf16.get_device()
+    N, K4, g, c, s, z = _w4_args(fn, codes, scales, zeros, (), dev)
+    if (N, K4) != (rows, K):
+        _refuse(fn)
+    _enqueue(fn, dev, _lib.mok_quantize_int4,
+             (_arg(fn, src_bf16, torch.bfloat16, (rows, K), dev), rows, K, g, c, s, z), stream)
+
+
+def mok_w4_gemm(x, codes, scales, out, *, zeros=None, stream=None) -> None:
+    """out [M, N] (bf16 or float32) = x W^T for x [M, K] bf16 and a weight of 4-bit codes
+    [N, K / 2] uint8 with scales [N, K / group] bf16 and zeros (None: 8)."""
+    import torch
+    fn = "mok_w4_gemm"
+    io = {torch.bfloat16: MOK_BF16, torch.float32: MOK_FP32}.get(out.dtype)
+    if x.dim() != 2 or io is None:
+        _refuse(fn)
+    M, dev = x.shape[0], x.get_device()
+    N, K, g, c, s, z = _w4_args(fn, codes, scales, zeros, (), dev)
+    _enqueue(fn, dev, _lib.mok_w4_gemm,
+             (_arg(fn, x, torch.bfloat16, (M, K), dev), c, s, z, M, N, K, g, io,
+              _arg(fn, out, out.dtype, (M, N), dev)), stream)
+
+
+def mok_moe_w4_workspace_bytes(args: MoeW4Args) -> int:
+    out = _SZ(0)
+    _check("mok_moe_w4_workspace_bytes",
+           _lib.mok_moe_w4_workspace_bytes(ctypes.byref(args), ctypes.byref(out)))
+    return out.value
+
+
+def mok_moe_w4_forward(args: MoeW4Args, stream=None) -> None:
+    _check("mok_moe_w4_forward", _lib.mok_moe_w4_forward(ctypes.byref(args), _stream(stream)))
 
 
 # ------------------------------------------------------------------------ layer helper
@@ -610,3 +813,49 @@ class MoeBackward:
                _lib.mok_moe_backward_error(_ptr(self.workspace), ctypes.byref(self.args),
                                            ctypes.byref(err), _stream(stream)))
         return err.value
+
+
+class MoeW4Layer:
+    """The routed experts on 4-bit weights (mok_moe_w4_forward): holds the weights of the local
+    experts [e0, e0 + E_l) and a workspace for up to max_tokens tokens a call.
+
+    gate, up, down: (codes, scales, zeros or None), codes [E_l, I, d / 2] ([E_l, d, I / 2] for down)
+    uint8, scales [E_l, I, d / group] ([E_l, d, I / group]) bf16, zeros uint8 like the scales. Calls
+    share the workspace: they must be ordered on one stream (captured graphs of a layer too)."""
+
+    def __init__(self, gate, up, down, *, E: int, k: int, e0: int = 0, max_tokens: int):
+        import torch
+        fn = "MoeW4Layer"
+        if gate[0].dim() != 3:
+            _refuse(fn)
+        E_l, dev = gate[0].shape[0], gate[0].get_device()
+        a = MoeW4Args()
+        for name, w in (("gate", gate), ("up", up), ("down", down)):
+            N, K, g, c, s, z = _w4_args(fn, *w, (E_l,), dev)
+            if name == "gate":
+                a.I, a.d, a.group = N, K, g
+            if ((a.d, a.I) if name == "down" else (a.I, a.d)) != (N, K) or g != a.group:
+                _refuse(fn)
+            setattr(a, name + "_codes", c)
+            setattr(a, name + "_scales", s)
+            setattr(a, name + "_zeros", z)
+        a.E, a.k, a.e0, a.E_l, a.T = E, k, e0, E_l, max_tokens
+        self._keep, self._dev, self.max_tokens = (gate, up, down), dev, max_tokens
+        n = mok_moe_w4_workspace_bytes(a)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=gate[0].device)
+        a.workspace, a.workspace_bytes = _ptr(self.workspace), n
+        self.args = a
+
+    def forward(self, x, topk_idx, topk_w, y, *, y_in=None, stream=None) -> None:
+        """y [T, d] bf16 = y_in + the local experts' weighted FFNs of x [T, d] bf16, T <= max_tokens;
+        topk_idx [T, k] int32, topk_w [T, k] float32. y may be x or y_in."""
+        import torch
+        fn, a, dev, bf = "mok_moe_w4_forward", self.args, self._dev, torch.bfloat16
+        T = x.shape[0]
+        if T > self.max_tokens:
+            _refuse(fn)
+        a.T, rows, picks = T, (T, a.d), (T, a.k)
+        a.x, a.y, a.y_in = _arg(fn, x, bf, rows, dev), _arg(fn, y, bf, rows, dev), _arg(fn, y_in, bf, rows, dev)
+        a.topk_idx = _arg(fn, topk_idx, torch.int32, picks, dev)
+        a.topk_w = _arg(fn, topk_w, torch.float32, picks, dev)
+        _enqueue(fn, dev, _lib.mok_moe_w4_forward, (ctypes.byref(a),), stream)

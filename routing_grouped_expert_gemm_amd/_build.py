@@ -13,7 +13,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmok.so")
 SOURCES = ["route.hip", "plan.hip", "quant.hip", "expert_gemm.hip", "api.hip", "noalloc.hip",
            "dispatch.hip", "backward.hip", "balance.hip", "norm.hip",
-           "route_backward.hip", "mx_gemm.hip"]
+           "route_backward.hip", "mx_gemm.hip", "route_scored.hip", "gated_norm.hip", "w4.hip"]
 HEADERS = ["device_common.h", "launch.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -727,7 +727,8 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
   const int st = rb_check(T, d, E, k, io_dtype);
   if (st != MOK_OK) return st;
   if (!dx && !dw_router && T > 0) return MOK_EINVAL;
-  if (T > 0 && (!topk_idx || !topk_w || !dtopk_w || (dx && !w_router) || (dw_router && !x)))
+  const bool picks = topk_idx || topk_w || dtopk_w || !dlogits;     // else dl is dlogits alone
+  if (T > 0 && ((picks && (!topk_idx || !topk_w || !dtopk_w)) || (dx && !w_router) || (dw_router && !x)))
     return MOK_EINVAL;
   size_t need = 0;
   mok_route_backward_workspace_bytes(T, d, E, io_dtype, &need);
@@ -743,7 +744,7 @@ int mok_route_backward(const void* x, const void* w_router, const int32_t* topk_
   }
   RbArgs a = {};
   a.x = x; a.w = w_router; a.idx = topk_idx; a.tw = topk_w; a.dtw = dtopk_w; a.dlogits = dlogits;
-  a.dx_in = dx_in; a.dx = dx; a.T = T; a.d = d; a.E = E; a.k = k;
+  a.dx_in = dx_in; a.dx = dx; a.T = T; a.d = d; a.E = E; a.k = picks ? k : 0;
   auto al16 = [](const void* p) { return (uintptr_t)p % 16 == 0; };
   const bool aligned = al16(x) && al16(w_router) && al16(dx_in) && al16(dx) && al16(dw_router);
   if (io_dtype == MOK_BF16 && rb_tiled(T, d, E) && (aligned || d % 8)) {
