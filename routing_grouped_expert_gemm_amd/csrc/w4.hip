@@ -4,23 +4,28 @@
 //   W[n,k] = (q[n,k] - z[n,k / g]) s[n,k / g],  q 0 .. 15, two codes a byte, 2i in the low nibble
 //   C[m,n] = sum_groups s (sum_{k in group} x[m,k] (q - z))
 //
-// Bound by streaming the codes once. A weight's 16 rows and 128 columns are one 16-byte load a lane
-// (lane (kq, n): row n, 32 codes), and enter the 16x16x32 bf16 MFMA as integers: a nibble 0 .. 15 is,
-// as an E4M3 byte, q 2^-9 (its first two binades are evenly spaced), so one AND for four codes and a
-// conversion for two give exact bf16 integers, about one VALU operation a code. x is the other
-// operand. A second MFMA with the constant -z beside each takes the zero point off inside the same
-// float32 sum; the group's sum is scaled in float32. Rows of x past M are zero: up to 16 rows cost
-// what one does.
+// Bound by streaming the codes once, and close behind by the vector unit, which has to take every code
+// apart. A weight's 16 rows and 128 columns are one 16-byte load a lane (lane (kq, n): row n, 32 codes).
+// A wave takes one tile (16 weight rows; of the MoE's first product gate and up tiles in turn) and one of
+// KS parts of K and streams it in bodies of 512 columns: the loads of the next body are in flight while
+// this one's are used, each issued as its register becomes free. A workgroup is 8 waves: 8 / KS tiles by
+// KS parts, whose sums meet in LDS in a fixed order. (Streamed alone, the codes of T 1, d 7168, I 2048, k 8
+// come at 5.3 TB/s with one wave a tile and 32 KB a CU in flight, 4.7 with two and 64 KB.)
 //
-// A workgroup's waves split K (KC columns each), and keep their part of x in registers while they
-// walk the workgroup's tiles of 16 weight rows, so that only weights are loaded in the loop, up to R
-// tiles ahead; the waves' sums meet in LDS in a fixed order. K past 8 KC goes in rounds, whose sums
-// stay in LDS.
+//  k_w4_few   up to 4 rows of x a pass: integers. x is cut into 22-bit integers with one exponent for a
+//    row's group (what is lost is below 2^-22 of the group's largest value; bf16 values within 2^-14 of it
+//    are exact) and those into three signed bytes, which are rows 4 m, 4 m + 1, 4 m + 2 of the 16-row int8
+//    MFMA. A code less its zero point is a byte: 4 (with zero points 7) vector operations for 8 codes.
+//    The group's sums are exact; a lane's accumulators are the three bytes' sums of row kq and column n, so
+//    that scale and exponent are one fused multiply-add a group.
+//  k_w4_rows  up to 16 rows: the bf16 MFMA. A nibble 0 .. 15 is, as an E4M3 byte, q 2^-9 (its first two
+//    binades are evenly spaced), so one AND for four codes and a conversion for two give exact bf16
+//    integers. x's products with a constant (-8, or 1, times -z) begin a group's float32 sum, which takes
+//    the zero point off; the sum is scaled in float32.
 //
-// The MoE's first launch pairs the gate and up rows of a tile and writes H = silu(gate) up in
-// float32; its second reads H as two bf16 planes (16 significant bits) that take rows 0 .. 7 and
-// 8 .. 15 of the MFMA's 16, which keeps the result as exact as float32 H would to 2^-17; a third adds
-// a token's experts in the order of its picks.
+// The MoE's first launch writes H = silu(gate) up in float32, its second reads it (k_w4_rows: as two bf16
+// planes, 16 significant bits, in two rows of the MFMA); a third adds a token's experts in the order of
+// its picks.
 #include <algorithm>
 
 #include "device_common.h"
@@ -32,8 +37,10 @@ namespace {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
+constexpr int W4_BODY = 512;         // columns of a wave's step
+constexpr int W4_LOADS = W4_BODY / 128;
 constexpr int W4_MAXW = 8;           // waves of a workgroup
-constexpr int W4_TILES = 8;          // tiles of a workgroup
+constexpr int W4_LDS_FEW = 52 * 1024, W4_LDS_ROWS = 72 * 1024;   // for x: three and two workgroups a CU
 constexpr int W4_SCAN = 1024;        // routes up to which a workgroup finds its rows by itself
 enum { W4_DENSE = 0, W4_UP = 1, W4_DOWN = 2 };
 
@@ -49,7 +56,9 @@ struct W4Args {
   void* out;                         // dense: bf16 or float32 [M, N]; up: H; down: P float32
   int64_t M;                         // dense
   int N, K;
-  int tiles, tpw, waves, out_f32;
+  int tiles, tpw, ks;                // tiles of a workgroup, parts of K
+  int cap;                           // bytes of LDS for x
+  int out_f32;
   // MoE
   const int32_t* idx;                // [T k]
   const float* tw;
@@ -57,6 +66,13 @@ struct W4Args {
   int64_t routes;
   int k, e0, El;
 };
+
+// Orders the wave's LDS accesses before this point against those behind it.
+MOK_DEV void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // Lane groups of 16 <-> registers: afterwards w[j] of lane group q is what w[q] of group j was.
 MOK_DEV void transpose4(uint32_t (&w)[4]) {
@@ -72,6 +88,17 @@ MOK_DEV void transpose4(uint32_t (&w)[4]) {
   s32(w[1], w[3]);
   s16(w[0], w[1]);
   s16(w[2], w[3]);
+}
+
+// The same for halves of the wave: afterwards w[0], w[1] of every lane come from the first and second
+// lane group (columns 0 .. 63 of 128), w[2], w[3] from the others.
+MOK_DEV void swap2(uint32_t (&w)[4]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const auto r = __builtin_amdgcn_permlane32_swap(w[j], w[2 + j], false, false);
+    w[j] = r[0];
+    w[2 + j] = r[1];
+  }
 }
 
 // 8 codes of a word as bf16 integers, in the order 0 2 4 6 1 3 5 7.
@@ -96,40 +123,31 @@ MOK_DEV bf16x8_t order8(const uint4 v) {
 
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
-// One tile's weights of a wave: codes, scales and zero points of its KC columns.
-template <int G, bool Z, int KC>
-struct W4Unit {
-  static constexpr int NL = KC / 128, NS = KC / G;      // loads, groups
-  uint4 q[NL];
-  uint32_t s[NS / 2];
-  uint32_t z[Z ? (NS + 3) / 4 : 1];
-
-  // m: the matrix, its row n (of lane) at codes offset row_c; kb: the wave's first column
-  MOK_DEV void load(const W4Mat& m, int64_t row, int K, int kb, int kq) {
-    const uint8_t* c = m.codes + row * (K / 2);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int k = kb + 128 * i + 32 * kq;
-      q[i] = *(const uint4*)(c + (k < K ? k / 2 : 0));   // x is zero there
-    }
-    const int ng = K / G, g0 = kb / G;
+// The scales and zero points of a wave's tile row (of the lane) for one body.
+template <int G, bool Z>
+struct W4Groups {
+  static constexpr int NG = W4_BODY / G;
+  uint32_t s[NG / 2];
+  uint32_t z[Z ? NG / 4 : 1];
+  MOK_DEV void load(const W4Mat& m, int64_t row, int K, int k) {
+    const int ng = K / G, g0 = k / G;
     const uint16_t* sp = m.scales + row * ng + g0;
     const uint8_t* zp = Z ? m.zeros + row * ng + g0 : nullptr;
-    if (kb + KC <= K) {
+    if (k + W4_BODY <= K) {
 #pragma unroll
-      for (int i = 0; i < NS / 2; ++i) s[i] = ((const u32_any*)sp)[i];
+      for (int i = 0; i < NG / 2; ++i) s[i] = ((const u32_any*)sp)[i];
       if constexpr (Z)
 #pragma unroll
-        for (int i = 0; i < NS / 4; ++i) z[i] = ((const u32_any*)zp)[i];
+        for (int i = 0; i < NG / 4; ++i) z[i] = ((const u32_any*)zp)[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < NS / 2; ++i) {
+      for (int i = 0; i < NG / 2; ++i) {
         const uint32_t lo = g0 + 2 * i < ng ? sp[2 * i] : 0, hi = g0 + 2 * i + 1 < ng ? sp[2 * i + 1] : 0;
         s[i] = lo | (hi << 16);
       }
       if constexpr (Z)
 #pragma unroll
-        for (int i = 0; i < NS / 4; ++i) {
+        for (int i = 0; i < NG / 4; ++i) {
           z[i] = 0;
 #pragma unroll
           for (int b = 0; b < 4; ++b)
@@ -137,172 +155,466 @@ struct W4Unit {
         }
     }
   }
-
-  MOK_DEV f32x4_t product(const bf16x8_t (&a)[KC / 32]) const {
-    f32x4_t total = {0, 0, 0, 0}, acc = {0, 0, 0, 0};
-    bf16x8_t zb = __builtin_bit_cast(bf16x8_t, make_uint4(0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u));
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-      if constexpr (G < 128) transpose4(w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = 128 * i + 32 * j, g = k / G;
-        if constexpr (Z)
-          if (k % G == 0) {
-            const float zf = -(float)((z[g / 4] >> (8 * (g % 4))) & 0xFF);
-            const uint32_t zz = pack_bf16x2(zf, zf);
-            zb = __builtin_bit_cast(bf16x8_t, make_uint4(zz, zz, zz, zz));
-          }
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[4 * i + j], unpack8(w[j]), acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[4 * i + j], zb, acc, 0, 0, 0);
-        if ((k + 32) % G == 0) {
-          const float sc = __uint_as_float(g % 2 ? s[g / 2] & 0xFFFF0000u : s[g / 2] << 16);
-          total += acc * sc;
-          acc = f32x4_t{0, 0, 0, 0};
-        }
-      }
-    }
-    return total;
+  MOK_DEV float scale(int g) const {
+    return __uint_as_float(g % 2 ? s[g / 2] & 0xFFFF0000u : s[g / 2] << 16);
   }
+  MOK_DEV uint32_t zero_byte(int g) const { return (z[g / 4] >> (8 * (g % 4))) & 0xFF; }
+  MOK_DEV float zero(int g) const { return Z ? (float)zero_byte(g) : 8.0f; }
 };
 
-// Workgroup (x, y): tiles x tpw .., of M rows y 16 .. (dense) or of expert slot y (MoE).
-template <int G, bool Z, int KC, int MODE>
-__global__ __launch_bounds__(64 * W4_MAXW) void k_w4(const W4Args p) {
-  constexpr int S = MODE == W4_UP ? 2 : 1;             // matrices of a tile
-  constexpr int MR = MODE == W4_DOWN ? 8 : 16;         // rows of a pass
-  constexpr int R = S == 2 ? 2 : 3;                    // units in registers
-  __shared__ float red[2][W4_MAXW][S][256];
-  __shared__ float part[W4_TILES][S][256];
-  __shared__ int16_t list[MODE == W4_DENSE ? 1 : W4_SCAN];
-  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid >> 6), kq = lane >> 4, ln = lane & 15;
-  int64_t expert = 0, count, plan_at = 0;
-  if constexpr (MODE == W4_DENSE) {
-    count = min((int64_t)MR, p.M - (int64_t)blockIdx.y * MR);
-  } else if (p.offsets) {
-    expert = blockIdx.y;
-    plan_at = p.offsets[expert];
-    count = p.offsets[expert + 1] - plan_at;
-    if (count <= 0) return;
-  } else {
+// total += the products of 128 columns (load i of a body), whose x are a[0 .. 3].
+template <int G, bool Z, int S>
+MOK_DEV void w4_step(const uint4 (&q)[S], const W4Groups<G, Z> (&gr)[S], int i, const bf16x8_t (&a)[4],
+                     f32x4_t (&total)[S]) {
+  constexpr int J = G < 128 ? G / 32 : 4;            // instructions of a group
+  const uint32_t c = Z ? 0x3F803F80u : 0xC100C100u;  // 1 or -8
+  const bf16x8_t cv = __builtin_bit_cast(bf16x8_t, make_uint4(c, c, c, c));
+  uint32_t w[S][4];
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    w[s][0] = q[s].x; w[s][1] = q[s].y; w[s][2] = q[s].z; w[s][3] = q[s].w;
+    if constexpr (G < 128) transpose4(w[s]);
+  }
+#pragma unroll
+  for (int j0 = 0; j0 < 4; j0 += J) {
+    const int g = (128 * i + 32 * j0) / G;
+    f32x4_t x = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = j0; j < j0 + J; ++j) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], cv, x, 0, 0, 0);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      f32x4_t acc = x;
+      if constexpr (Z) acc *= -gr[s].zero(g);
+#pragma unroll
+      for (int j = j0; j < j0 + J; ++j)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], unpack8(w[s][j]), acc, 0, 0, 0);
+      const float sc = gr[s].scale(g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) total[s][e] = fmaf(acc[e], sc, total[s][e]);
+    }
+  }
+}
+
+// The rows of an expert slot (MoE), found by every wave for itself (the same values): false if none.
+struct W4Rows {
+  int64_t expert = 0, count = 0, plan_at = 0;
+  const int32_t* ids = nullptr;      // the plan's, or NULL: list
+  const int16_t* list = nullptr;
+  MOK_DEV bool find(const W4Args& p, int slot, int16_t* own) {
+    const int lane = lane_id();
+    if (p.offsets) {
+      expert = slot;
+      plan_at = p.offsets[expert];
+      count = p.offsets[expert + 1] - plan_at;
+      ids = p.route_ids;
+      return count > 0;
+    }
     // more local experts than routes: a slot is a route, and serves its expert if no earlier route
     // names it; otherwise a slot is an expert
     const bool by_route = p.routes < p.El;
-    int e = p.e0 + (int)blockIdx.y;
-    if (by_route) e = p.idx[blockIdx.y];
-    if (e < p.e0 || e >= p.e0 + p.El) return;
+    int e = by_route ? p.idx[slot] : p.e0 + slot;
+    e = uniform(e);
+    if (e < p.e0 || e >= p.e0 + p.El) return false;
     expert = e - p.e0;
     int n = 0;
-    for (int r0 = 0; r0 < (int)p.routes; r0 += 64) {
-      const int r = r0 + lane;
-      const bool hit = r < p.routes && p.idx[r] == e;
-      const uint64_t mask = ballot(hit);
-      if (by_route && n == 0 && mask && r0 + __ffsll((unsigned long long)mask) - 1 < (int)blockIdx.y) return;
-      if (hit && wv == 0) list[n + __popcll(mask & lanemask_lt())] = (int16_t)r;
-      n += __popcll(mask);
+    for (int r0 = 0; r0 < (int)p.routes; r0 += 256) {
+      bool hit[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = r0 + 64 * q + lane;
+        hit[q] = r < p.routes && p.idx[r] == e;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = r0 + 64 * q;
+        const uint64_t mask = ballot(hit[q]);
+        if (by_route && n == 0 && mask && r + __ffsll((unsigned long long)mask) - 1 < slot) return false;
+        if (hit[q]) own[n + __popcll(mask & lanemask_lt())] = (int16_t)(r + lane);
+        n += __popcll(mask);
+      }
     }
     count = n;
-    if (count == 0) return;
-    __syncthreads();
+    list = own;
+    wave_sync();
+    return n > 0;
   }
-  const int t0 = blockIdx.x * p.tpw, nt = min(p.tpw, p.tiles - t0);
-  const int span = p.waves * KC, rounds = (p.K + span - 1) / span;
-  const int units = nt * S;
-  int turn = 0;                        // the half of red that the next tile's sums take
-  auto route_of = [&](int64_t m) -> int64_t {
-    return p.offsets ? p.route_ids[plan_at + m] : (int64_t)list[m];
-  };
-  for (int64_t m0 = 0; m0 < count; m0 += MR) {
-    const int rows = (int)min((int64_t)MR, count - m0);
-    // the row of x that this lane's MFMA row is
-    const int am = ln % MR;
-    int64_t row = -1;
-    if (am < rows) {
-      if constexpr (MODE == W4_DENSE) row = (int64_t)blockIdx.y * MR + am;
-      else if constexpr (MODE == W4_UP) row = route_of(m0 + am) / p.k;
-      else row = route_of(m0 + am);
+  MOK_DEV int32_t route(int64_t m) const { return ids ? ids[plan_at + m] : (int32_t)list[m]; }
+};
+
+// Row of x of the pass's row m: a token, or a route.
+template <int MODE>
+MOK_DEV int64_t w4_x_row(const W4Args& p, const W4Rows& rows, int64_t m) {
+  if constexpr (MODE == W4_DENSE) return m;
+  else if constexpr (MODE == W4_UP) return rows.route(m) / p.k;
+  else return rows.route(m);
+}
+
+// A result v of row m (of rows) and column n.
+template <int MODE, int S>
+MOK_DEV void w4_store(const W4Args& p, const W4Rows& rows, int64_t m, int n, const float (&v)[S]) {
+  if constexpr (MODE == W4_DENSE) {
+    if (p.out_f32) ((float*)p.out)[m * p.N + n] = v[0];
+    else ((bf16_t*)p.out)[m * p.N + n] = f32_to_bf16(v[0]);
+  } else if constexpr (MODE == W4_UP) {
+    ((float*)p.out)[(int64_t)rows.route(m) * p.N + n] = silu(v[0]) * v[S - 1];
+  } else {
+    const int64_t r = rows.route(m);
+    ((float*)p.out)[r * p.N + n] = p.tw[r] * v[0];
+  }
+}
+
+// The parts' sums of the workgroup's tiles, in order: red [wave][S][16 rows][16 columns].
+template <int MODE, int S, int PL>
+MOK_DEV void w4_join(const W4Args& p, const W4Rows& rows, const float* red, int64_t m0, int n_rows,
+                     int lo_row, int t0, int nt) {
+  for (int o = threadIdx.x; o < n_rows * nt * 16; o += blockDim.x) {
+    const int m = o / (nt * 16), c = o - m * (nt * 16), n = t0 * 16 + c;
+    float v[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      v[s] = 0.0f;
+      for (int w = 0; w < p.ks; ++w) {
+        const float* r = red + (((c >> 4) * p.ks + w) * S + s) * 256 + m * 16 + (c & 15);
+        v[s] += r[0];
+        if constexpr (PL == 2) v[s] += r[lo_row * 16];
+      }
     }
-    for (int rd = 0; rd < rounds; ++rd) {
-      const int kb = rd * span + wv * KC;
-      W4Unit<G, Z, KC> u[R];
-      auto fetch = [&](W4Unit<G, Z, KC>& to, int i) {
-        const int n = min((t0 + i / S) * 16 + ln, p.N - 1);
-        to.load(p.w[S == 2 ? i % 2 : 0], expert * p.N + n, p.K, kb < p.K ? kb : 0, kq);
-      };
+    if (n < p.N) w4_store<MODE, S>(p, rows, m0 + m, n, v);
+  }
+}
+
+// A wave's place: its tile's codes and its lane's row in them.
+template <int S>
+struct W4Tile {
+  const uint8_t* code[S];
+  uint32_t row_at, row_end;          // the lane's first bytes of a body; the last 16 bytes of its row
+  int64_t row;
+  MOK_DEV W4Tile(const W4Args& p, int64_t expert, int n0) {
+    const int lane = lane_id(), lr = min(lane & 15, p.N - 1 - n0);
+    row = expert * p.N + n0 + lr;
 #pragma unroll
-      for (int q = 0; q + 1 < R; ++q)
-        if (q < units) fetch(u[q], q);
-      bf16x8_t a[KC / 32];
+    for (int s = 0; s < S; ++s) code[s] = p.w[s].codes + (expert * p.N + n0) * (int64_t)(p.K / 2);
+    row_at = lr * (uint32_t)(p.K / 2) + 16 * (lane >> 4);
+    row_end = lr * (uint32_t)(p.K / 2) + p.K / 2 - 16;
+  }
+  // load i of the body at column k; past K, where x is zero, the row's last codes
+  MOK_DEV uint4 load(int s, int i, int k) const {
+    return *(const uint4*)(code[s] + min(row_at + (uint32_t)(k / 2 + 64 * i), row_end));
+  }
+};
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// LDS of a body's columns of one row of x: three bytes each, and a float32 exponent a group.
+MOK_HOSTDEV int w4_few_bytes(int g) { return 3 * W4_BODY + W4_BODY / g * 4; }
+
+// 8 codes of a word less their zero point as bytes, the even ones, then the odd ones; without zero points
+// (z the constant 8) times 16.
+template <bool Z>
+MOK_DEV void code_bytes(uint32_t w, uint32_t zc, int& even, int& odd) {
+  if constexpr (Z) {                                   // 0x80 + q - z carries into no other byte
+    even = (int)(((w & 0x0F0F0F0Fu) + zc) ^ 0x80808080u);
+    odd = (int)((((w >> 4) & 0x0F0F0F0Fu) + zc) ^ 0x80808080u);
+  } else {                                             // q ^ 8 is q - 8 in two's complement
+    w ^= 0x88888888u;
+    even = (int)((w << 4) & 0xF0F0F0F0u);
+    odd = (int)(w & 0xF0F0F0F0u);
+  }
+}
+
+// Workgroup (x, y): tiles x tpw .., rows y MR .. (dense) or expert slot y (MoE).
+template <int G, bool Z, int MODE>
+__global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_few(const W4Args p) {
+  constexpr int S = MODE == W4_UP ? 2 : 1, MR = 4, XF = MODE == W4_DOWN ? 2 : 1;     // XF: 16 bytes of 8 values
+  extern __shared__ __attribute__((aligned(16))) int8_t xb[];   // x [rows][3][ck + 16], then exponents [rows][ck / G]
+  __shared__ float red[W4_MAXW * 64];
+  __shared__ int16_t list[MODE == W4_DENSE ? 1 : W4_SCAN];
+  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid >> 6), kq = lane >> 4, ln = lane & 15;
+  W4Rows rows;
+  if constexpr (MODE == W4_DENSE) rows.count = p.M;
+  else if (!rows.find(p, blockIdx.y, list)) return;
+  // S tiles, of gate and up, are a pair's; a workgroup has whole pairs
+  const int tile = wv / p.ks, part = wv - tile * p.ks, t0 = blockIdx.x * (p.tpw / S);
+  const int nt = min(p.tpw / S, p.tiles - t0);
+  const bool idle = tile >= nt * S;
+  W4Args one = p;
+  one.w[0] = p.w[S == 2 ? tile % 2 : 0];
+  const W4Tile<1> w(one, rows.expert, idle ? 0 : (t0 + tile / S) * 16);
+  const int64_t m_first = MODE == W4_DENSE ? (int64_t)blockIdx.y * MR : 0;
+  const int64_t m_end = MODE == W4_DENSE ? min(rows.count, m_first + MR) : rows.count;
+  for (int64_t m0 = m_first; m0 < m_end; m0 += MR) {
+    const int n_rows = (int)min((int64_t)MR, m_end - m0);
+    // bodies of a chunk and part; chunks
+    const int bodies = (p.K + W4_BODY - 1) / W4_BODY, bw = W4_BODY * p.ks;
+    const int bpc = min((bodies + p.ks - 1) / p.ks, max(1, p.cap / (w4_few_bytes(G) * n_rows * p.ks)));
+    const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck, ld = ck + 16, ng = ck / G;
+    auto column = [&](int c, int b) { return c * ck + (part * bpc + b) * W4_BODY; };
+    float* const ex = (float*)(xb + n_rows * 3 * ld);
+    // x's columns c ck .. , 8 at a time: loaded ...
+    constexpr int XU = 2;
+    const int cw = ck / 8, units = n_rows * cw;
+    uint4 xv[XU][XF];
+    auto x_load = [&](int c, int u0) {
 #pragma unroll
-      for (int f = 0; f < KC / 32; ++f) {
-        const int k = kb + 128 * (f / 4) + (G < 128 ? 32 * (f % 4) + 8 * kq : 32 * kq + 8 * (f % 4));
-        const bool ok = row >= 0 && k < p.K;
-        if constexpr (MODE != W4_DOWN) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (ok) v = *(const uint4*)((const bf16_t*)p.x + row * p.K + k);
-          a[f] = order8(v);
-        } else {
-          float4 v0 = make_float4(0, 0, 0, 0), v1 = v0;
-          if (ok) {
-            v0 = *(const float4*)((const float*)p.x + row * p.K + k);
-            v1 = *(const float4*)((const float*)p.x + row * p.K + k + 4);
+      for (int j = 0; j < XU; ++j) {
+        const int u = u0 + j * (int)blockDim.x, r = min(u / cw, n_rows - 1), k = c * ck + (u - r * cw) * 8;
+        const int64_t at = w4_x_row<MODE>(p, rows, m0 + r) * p.K + min(k, p.K - 8);
+#pragma unroll
+        for (int i = 0; i < XF; ++i) {
+          const uint4 v = XF == 1 ? *(const uint4*)((const bf16_t*)p.x + at) : *(const uint4*)((const float*)p.x + at + 4 * i);
+          xv[j][i] = k < p.K ? v : make_uint4(0, 0, 0, 0);
+        }
+      }
+    };
+    // ... and cut into bytes. A group is G / 8 neighbouring lanes (a row's units fill whole waves).
+    auto x_store = [&](int u0) {
+#pragma unroll
+      for (int j = 0; j < XU; ++j) {
+        const int u = u0 + j * (int)blockDim.x;
+        if (u >= units) break;
+        const int r = u / cw, o = (u - r * cw) * 8;
+        float v[8];
+        const uint4 q = xv[j][0];
+        if constexpr (XF == 1) {
+          const uint32_t t[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(t[i] << 16);
+            v[2 * i + 1] = __uint_as_float(t[i] & 0xFFFF0000u);
           }
-          const float v[8] = {v0.x, v0.z, v1.x, v1.z, v0.y, v0.w, v1.y, v1.w};
+        } else {
+          const uint4 h = xv[j][XF - 1];
+          const uint32_t t[8] = {q.x, q.y, q.z, q.w, h.x, h.y, h.z, h.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(t[i]);
+        }
+        uint32_t top = 0;                              // exponent field of the largest; 255: not finite
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int m = 1; m < G / 8; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
+        const int e = max((int)(top >> 23), 1);
+        if (u % (G / 8) == 0)
+          ex[r * ng + o / G] = e == 255 ? NAN : __builtin_amdgcn_ldexpf(1.0f, e - 148);
+        uint32_t d[3][2] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {                  // |v| < 2^22; bytes from the least, rounded to nearest
+          const int n0 = e == 255 ? 0 : (int)rintf(__builtin_amdgcn_ldexpf(v[i], 148 - e));
+          const int n1 = (n0 + 128) >> 8, n2 = (n1 + 128) >> 8;
+          const int h = i & 1, b = 8 * (i >> 1);       // the even ones, then the odd ones
+          d[2][h] |= (uint32_t)(n0 & 0xFF) << b;
+          d[1][h] |= (uint32_t)(n1 & 0xFF) << b;
+          d[0][h] |= (uint32_t)(n2 & 0xFF) << b;
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) *(uint2*)(xb + (r * 3 + q) * ld + o) = make_uint2(d[q][0], d[q][1]);
+      }
+    };
+    uint4 q[W4_LOADS];
+    W4Groups<G, Z> gr;
+    float total = 0.0f;
+    x_load(0, tid);                                    // x first: waiting for it must not wait for the codes
+    __builtin_amdgcn_sched_barrier(0);
+    if (!idle) {
+      gr.load(one.w[0], w.row, p.K, min(column(0, 0), p.K));
+#pragma unroll
+      for (int l = 0; l < W4_LOADS; ++l) q[l] = w.load(0, l, column(0, 0));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // the lane's row of the MFMA: byte ln % 4 of row ln / 4 (a fourth byte, and rows past the last, are not
+    // looked at), and where its columns lie in 128
+    const int8_t* const xl = xb + (min(ln >> 2, n_rows - 1) * 3 + min(ln & 3, 2)) * ld +
+                             (G == 128 ? 32 * kq : G == 64 ? 32 * (kq & 1) + 16 * (kq >> 1) : 8 * kq);
+    const float* const xe = ex + min(kq, n_rows - 1) * ng;
+    for (int c = 0; c < chunks; ++c) {
+      __syncthreads();                                 // the chunk before is done with
+      for (int u = tid;;) {
+        if (c > 0 || u != tid) x_load(c, u);
+        x_store(u);
+        u += XU * (int)blockDim.x;
+        if (u - tid >= units) break;
+      }
+      __syncthreads();
+      if (idle) continue;
+      for (int b = 0; b < bpc; ++b) {
+        // the next body (behind the last, and past K: the row's last codes once more)
+        const int kn = min(b + 1 < bpc ? column(c, b + 1) : column(c + 1, 0), p.K);
+        W4Groups<G, Z> gn;
+        gn.load(one.w[0], w.row, p.K, kn);
+        const int at = (part * bpc + b) * W4_BODY;
+#pragma unroll
+        for (int l = 0; l < W4_LOADS; ++l) {
+          uint32_t t[4] = {q[l].x, q[l].y, q[l].z, q[l].w};
+          if constexpr (G == 64) swap2(t);
+          if constexpr (G == 32) transpose4(t);
+          constexpr int NG = 128 / G, W = 4 / NG;      // groups of the load, words of a group
+          i32x4_t acc[NG];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const uint32_t zc = Z ? 0x80808080u - gr.zero_byte(l * NG + g) * 0x01010101u : 0;
+            acc[g] = i32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < W; j += W > 1 ? 2 : 1) {
+              int lo[2], hi[2];
+              code_bytes<Z>(t[W * g + j], zc, lo[0], hi[0]);
+              if constexpr (W > 1) {
+                code_bytes<Z>(t[W * g + j + 1], zc, lo[1], hi[1]);
+                const i32x4_t a = *(const i32x4_t*)(xl + at + 128 * l + (G == 128 ? 8 * j : 64 * g));
+                acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, i32x4_t{lo[0], hi[0], lo[1], hi[1]}, acc[g], 0, 0, 0);
+              } else {
+                const long a = *(const long*)(xl + at + 128 * l + 32 * g);
+                acc[g] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)(uint32_t)lo[0] | ((long)hi[0] << 32), acc[g], 0, 0, 0);
+              }
+            }
+          }
+          q[l] = w.load(0, l, kn);
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float v = fmaf((float)acc[g][0], 65536.0f, (float)((acc[g][1] << 8) + acc[g][2]));
+            total = fmaf(v * gr.scale(l * NG + g), xe[at / G + l * NG + g], total);
+          }
+        }
+        gr = gn;
+      }
+    }
+    // the parts' sums, in order
+    if (!idle) red[wv * 64 + lane] = Z ? total : total * 0.0625f;
+    __syncthreads();
+    for (int o = tid; o < n_rows * nt * 16; o += blockDim.x) {
+      const int m = o / (nt * 16), c = o - m * (nt * 16), n = t0 * 16 + c;
+      float v[S];
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        v[s] = 0.0f;
+        for (int j = 0; j < p.ks; ++j) v[s] += red[(((c >> 4) * S + s) * p.ks + j) * 64 + m * 16 + (c & 15)];
+      }
+      if (n < p.N) w4_store<MODE, S>(p, rows, m0 + m, n, v);
+    }
+  }
+}
+
+// The same for up to 16 rows of the MFMA, x in LDS for the whole workgroup.
+template <int G, bool Z, int MODE>
+__global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
+  constexpr int S = MODE == W4_UP ? 2 : 1, PL = MODE == W4_DOWN ? 2 : 1, MR = 16 / PL;
+  extern __shared__ __attribute__((aligned(16))) bf16_t xs[];   // [rows PL][ck + 8]; then the waves' sums
+  __shared__ int16_t list[MODE == W4_DENSE ? 1 : W4_SCAN];
+  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid >> 6), kq = lane >> 4, ln = lane & 15;
+  W4Rows rows;
+  if constexpr (MODE == W4_DENSE) rows.count = p.M;
+  else if (!rows.find(p, blockIdx.y, list)) return;
+  const int tile = wv / p.ks, part = wv - tile * p.ks, t0 = blockIdx.x * p.tpw;
+  const int nt = min(p.tpw, p.tiles - t0);
+  const bool idle = tile >= nt;
+  const W4Tile<S> w(p, rows.expert, idle ? 0 : (t0 + tile) * 16);
+  const int64_t m_first = MODE == W4_DENSE ? (int64_t)blockIdx.y * MR : 0;
+  const int64_t m_end = MODE == W4_DENSE ? min(rows.count, m_first + MR) : rows.count;
+  for (int64_t m0 = m_first; m0 < m_end; m0 += MR) {
+    const int n_rows = (int)min((int64_t)MR, m_end - m0), n_xr = n_rows * PL;
+    // bodies of a chunk and part; chunks
+    const int bodies = (p.K + W4_BODY - 1) / W4_BODY, bw = W4_BODY * p.ks;
+    const int bpc = min((bodies + p.ks - 1) / p.ks, max(1, p.cap / (2 * bw * n_xr)));
+    const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck, ld = ck + 8;
+    auto column = [&](int c, int b) { return c * ck + (part * bpc + b) * W4_BODY; };
+    // x's columns c ck .. to LDS, 8 at a time, in unpack8's order: XU loads of a thread in flight
+    constexpr int XU = 4 / PL;
+    const int cw = ck / 8, units = n_rows * cw;
+    uint4 xv[XU][PL];
+    auto x_load = [&](int c, int u0) {
+#pragma unroll
+      for (int j = 0; j < XU; ++j) {
+        const int u = u0 + j * (int)blockDim.x, r = min(u / cw, n_rows - 1), k = c * ck + (u - r * cw) * 8;
+        const int64_t at = w4_x_row<MODE>(p, rows, m0 + r) * p.K + min(k, p.K - 8);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+          const uint4 v = PL == 1 ? *(const uint4*)((const bf16_t*)p.x + at) : *(const uint4*)((const float*)p.x + at + 4 * i);
+          xv[j][i] = k < p.K ? v : make_uint4(0, 0, 0, 0);
+        }
+      }
+    };
+    auto x_store = [&](int u0) {
+#pragma unroll
+      for (int j = 0; j < XU; ++j) {
+        const int u = u0 + j * (int)blockDim.x, r = u / cw;
+        if (u >= units) break;
+        bf16_t* const to = xs + r * ld + (u - r * cw) * 8;
+        if constexpr (PL == 1) {
+          *(bf16x8_t*)to = order8(xv[j][0]);
+        } else {
+          const uint4 a = xv[j][0], b = xv[j][PL - 1];
+          const uint32_t w[8] = {a.x, a.z, b.x, b.z, a.y, a.w, b.y, b.w};
+          bf16x8_t hi, lo;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const __bf16 hi = (__bf16)v[i];
-            a[f][i] = ln < 8 ? hi : (__bf16)(v[i] - (float)hi);
+            hi[i] = (__bf16)__uint_as_float(w[i]);
+            lo[i] = (__bf16)(__uint_as_float(w[i]) - (float)hi[i]);
           }
+          *(bf16x8_t*)to = hi;
+          *(bf16x8_t*)(to + n_rows * ld) = lo;
         }
       }
-      f32x4_t sum[S];
-      for (int i0 = 0; i0 < units; i0 += R) {
+    };
+    // the row of xs that is this lane's of the MFMA's 16 (those past the rows are not looked at)
+    const bf16_t* const xl = xs + (PL == 2 ? min(ln & 7, n_rows - 1) + (ln >> 3) * n_rows : min(ln, n_rows - 1)) * ld;
+    uint4 q[W4_LOADS][S];
+    W4Groups<G, Z> gr[S];
+    f32x4_t total[S];
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-          const int i = i0 + q;
-          if (i >= units) break;
-          if (i + R - 1 < units) fetch(u[(q + R - 1) % R], i + R - 1);
-          __builtin_amdgcn_sched_barrier(0);
-          const int s = S == 2 ? q % 2 : 0, t = i / S;
-          sum[s] = u[q].product(a);
-          if (s + 1 < S) continue;
-          // the waves' sums, in their order
+    for (int s = 0; s < S; ++s) total[s] = f32x4_t{0, 0, 0, 0};
+    x_load(0, tid);                                    // x first: waiting for it must not wait for the codes
+    __builtin_amdgcn_sched_barrier(0);
+    if (!idle)
 #pragma unroll
-          for (int c = 0; c < S; ++c)
+      for (int s = 0; s < S; ++s) {
+        gr[s].load(p.w[s], w.row, p.K, min(column(0, 0), p.K));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) red[turn][wv][c][(4 * kq + e) * 16 + ln] = sum[c][e];
-          __syncthreads();
-          for (int o = tid; o < rows * 16; o += blockDim.x) {
-            float v[S];
+        for (int l = 0; l < W4_LOADS; ++l) q[l][s] = w.load(s, l, column(0, 0));
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    for (int c = 0; c < chunks; ++c) {
+      __syncthreads();                                 // the chunk (or the sums) before is done with
+      for (int u = tid;;) {
+        if (c > 0 || u != tid) x_load(c, u);
+        x_store(u);
+        u += XU * (int)blockDim.x;
+        if (u - tid >= units) break;
+      }
+      __syncthreads();
+      if (idle) continue;
+      for (int b = 0; b < bpc; ++b) {
+        // the next body (behind the last, and past K: the row's last codes once more)
+        const int kn = min(b + 1 < bpc ? column(c, b + 1) : column(c + 1, 0), p.K);
+        W4Groups<G, Z> gn[S];
 #pragma unroll
-            for (int c = 0; c < S; ++c) {
-              v[c] = 0.0f;
-              for (int w = 0; w < p.waves; ++w) {
-                v[c] += red[turn][w][c][o];
-                if constexpr (MR == 8) v[c] += red[turn][w][c][128 + o];
-              }
-              if (rounds > 1) {
-                if (rd > 0) v[c] += part[t][c][o];
-                part[t][c][o] = v[c];
-              }
-            }
-            const int m = o >> 4, n = (t0 + t) * 16 + (o & 15);
-            if (rd + 1 < rounds || n >= p.N) continue;
-            if constexpr (MODE == W4_DENSE) {
-              const int64_t at = ((int64_t)blockIdx.y * MR + m) * p.N + n;
-              if (p.out_f32) ((float*)p.out)[at] = v[0];
-              else ((bf16_t*)p.out)[at] = f32_to_bf16(v[0]);
-            } else {
-              const int64_t r = route_of(m0 + m);
-              if constexpr (MODE == W4_UP) ((float*)p.out)[r * p.N + n] = silu(v[0]) * v[S - 1];
-              else ((float*)p.out)[r * p.N + n] = p.tw[r] * v[0];
-            }
-          }
-          turn ^= 1;
+        for (int s = 0; s < S; ++s) gn[s].load(p.w[s], w.row, p.K, kn);
+        const bf16_t* const xb = xl + (part * bpc + b) * W4_BODY;
+        bf16x8_t a[2][4];
+        auto read = [&](int l) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            a[l & 1][j] = *(const bf16x8_t*)(xb + 128 * l + (G < 128 ? 32 * j + 8 * kq : 32 * kq + 8 * j));
+        };
+        read(0);
+#pragma unroll
+        for (int l = 0; l < W4_LOADS; ++l) {
+          if (l + 1 < W4_LOADS) read(l + 1);
+          w4_step<G, Z, S>(q[l], gr, l, a[l & 1], total);
+#pragma unroll
+          for (int s = 0; s < S; ++s) q[l][s] = w.load(s, l, kn);
         }
+#pragma unroll
+        for (int s = 0; s < S; ++s) gr[s] = gn[s];
       }
     }
+    __syncthreads();
+    float* const red = (float*)xs;
+    if (!idle)
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[(wv * S + s) * 256 + (4 * kq + e) * 16 + ln] = total[s][e];
+    __syncthreads();
+    w4_join<MODE, S, PL>(p, rows, red, m0, n_rows, 8, t0, nt);
   }
 }
 
@@ -390,21 +702,31 @@ __global__ __launch_bounds__(256) void k_quantize_int4(const bf16_t* __restrict_
 bool group_ok(int g) { return g == 32 || g == 64 || g == 128; }
 bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
+// most: the rows that an expert (or the product) can have; mean: how many it has on average.
 template <int MODE>
-hipError_t launch_w4(W4Args a, int g, unsigned slots, hipStream_t s) {
-  // KC columns a wave: 512, or 1024 where 8 waves of 512 do not cover K (groups of 32 would hold too
-  // many scales)
-  const bool wide = a.K > 512 * W4_MAXW && g >= 64;
-  const int kc = wide ? 1024 : 512;
-  a.waves = std::min(W4_MAXW, (a.K + kc - 1) / kc);
+hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t most, double mean, hipStream_t s) {
+  constexpr int S = MODE == W4_UP ? 2 : 1, PL = MODE == W4_DOWN ? 2 : 1;
+  const bool few = most <= 4 || mean <= 2.0;      // one in twenty experts of 2 rows has a second pass
   a.tiles = (a.N + 15) / 16;
-  // as many tiles a workgroup as leave one for every CU
-  a.tpw = (int)std::max<int64_t>(1, std::min<int64_t>(W4_TILES, (int64_t)a.tiles * slots / 256));
-  const dim3 grid((a.tiles + a.tpw - 1) / a.tpw, slots), block(64 * a.waves);
+  const int bodies = (a.K + W4_BODY - 1) / W4_BODY, mr = few ? 4 : 16 / PL;
+  const int xr = (int)std::min<int64_t>(most, mr);
+  if (MODE == W4_DENSE) slots = (a.M + mr - 1) / mr;
+  // LDS of a body's columns in all rows; the parts of K have to fit, and gate and up tiles come in pairs
+  const int bytes = few ? w4_few_bytes(g) * xr : 2 * W4_BODY * PL * xr;
+  const int lds_x = few ? W4_LDS_FEW : W4_LDS_ROWS, pair = few ? S : 1;
+  const int parts = std::min(std::min(W4_MAXW / pair, bodies), lds_x / bytes);
+  // as many parts of K as give every SIMD two waves
+  const int64_t waves = std::max<int64_t>(1, (int64_t)a.tiles * pair * slots);
+  a.ks = (int)std::min<int64_t>(parts, (2048 + waves - 1) / waves);
+  a.ks = (bodies + (bodies + a.ks - 1) / a.ks - 1) / ((bodies + a.ks - 1) / a.ks);
+  a.tpw = W4_MAXW / a.ks / pair * pair;
+  a.cap = bytes * a.ks * std::min((bodies + a.ks - 1) / a.ks, std::max(1, lds_x / (bytes * a.ks)));
+  // 16 bytes lie between rows (of each byte's plane)
+  const size_t lds = std::max((size_t)a.cap + 48 * xr, few ? (size_t)0 : (size_t)a.tpw * a.ks * S * 1024);
+  const dim3 grid((unsigned)((a.tiles * pair + a.tpw - 1) / a.tpw), (unsigned)slots), block(64 * a.tpw * a.ks);
   auto go = [&](auto G, auto Z) {
-    if constexpr (G() >= 64)
-      if (wide) return launch_k(k_w4<G(), Z(), 1024, MODE>, grid, block, 0, s, nullptr, nullptr, a);
-    launch_k(k_w4<G(), Z(), 512, MODE>, grid, block, 0, s, nullptr, nullptr, a);
+    launch_k(few ? k_w4_few<G(), Z(), MODE> : k_w4_rows<G(), Z(), MODE>, grid, block, (uint32_t)lds, s, nullptr,
+             nullptr, a);
   };
   auto pick = [&](auto G) {
     if (a.w[0].zeros) go(G, std::true_type{});
@@ -483,10 +805,8 @@ int mok_w4_gemm(const void* x, const uint8_t* codes, const void* scales, const u
   W4Args a = {};
   a.w[0] = {codes, (const uint16_t*)scales, zeros};
   a.x = x; a.out = c; a.M = M; a.N = (int)N; a.K = K; a.out_f32 = out_dtype == MOK_FP32;
-  const int64_t slots = (M + 15) / 16;
-  if (slots > 65535 || N > (int64_t)1 << 26) return MOK_EUNSUPPORTED;
-  return launch_w4<W4_DENSE>(a, group, (unsigned)slots, (hipStream_t)stream) == hipSuccess ? MOK_OK
-                                                                                          : MOK_EHIP;
+  if (M > 1 << 20 || N > 1 << 26) return MOK_EUNSUPPORTED;
+  return launch_w4<W4_DENSE>(a, group, 0, M, (double)M, (hipStream_t)stream) == hipSuccess ? MOK_OK : MOK_EHIP;
 }
 
 int mok_moe_w4_workspace_bytes(const mok_moe_w4_args* args, size_t* bytes) {
@@ -526,14 +846,15 @@ int mok_moe_w4_forward(const mok_moe_w4_args* args, void* stream) {
     w.offsets = (const int32_t*)(ws + p.offsets);
     w.route_ids = (const int32_t*)(ws + p.ids);
   }
-  const unsigned slots = (unsigned)(p.plan ? a.E_l : std::min<int64_t>(n, a.E_l));
+  const int64_t slots = p.plan ? a.E_l : std::min<int64_t>(n, a.E_l);
+  const double mean = (double)n / a.E;
   w.w[0] = {a.gate_codes, (const uint16_t*)a.gate_scales, a.gate_zeros};
   w.w[1] = {a.up_codes, (const uint16_t*)a.up_scales, a.up_zeros};
   w.x = a.x; w.out = ws + p.H; w.N = a.I; w.K = a.d;
-  if (launch_w4<W4_UP>(w, a.group, slots, s) != hipSuccess) return MOK_EHIP;
+  if (launch_w4<W4_UP>(w, a.group, slots, a.T, mean, s) != hipSuccess) return MOK_EHIP;
   w.w[0] = {a.down_codes, (const uint16_t*)a.down_scales, a.down_zeros};
   w.x = ws + p.H; w.out = ws + p.P; w.N = a.d; w.K = a.I;
-  if (launch_w4<W4_DOWN>(w, a.group, slots, s) != hipSuccess) return MOK_EHIP;
+  if (launch_w4<W4_DOWN>(w, a.group, slots, a.T, mean, s) != hipSuccess) return MOK_EHIP;
   launch_k(k_w4_combine, dim3((unsigned)blocks), dim3(256), 0, s, nullptr, nullptr,
            (const float*)(ws + p.P), a.topk_idx, (const uint2*)a.y_in, a.T, a.k, a.e0, a.E_l, a.d / 4,
            (uint2*)a.y);
