@@ -6,11 +6,11 @@
 //   most worth are kept, and the k largest c in them are the picks (ties: the lower id)
 //   w[j] = scale s[e_j] (/ sum_i s[e_i])
 //
-// Whole numbers hang on c, so c and the worths are float64 by definition. Few rows need it: c is
-// formed in float32 (or, where c grows with l alone, l itself is compared) with a bound on its
-// error, and a row in which two neighbours of the result's order lie closer than their bounds
-// allow is done again in float64 by its wave (row_exact). At T 65,536, E 256 of random logits that
-// is one row in a thousand.
+// Whole numbers hang on c, so c and the worths are float64 by definition. Few rows need it: k_topk_scored
+// orders a row by float32 values (c, or l itself where c grows with l alone) whose error is bounded, and a
+// row in which two neighbours of the result's order lie closer than that bound allows is done again in
+// float64 by its wave (row_exact): one row in some hundreds of random logits. T 65,536, E 256, 8 groups,
+// k 8: 25 us; every row in float64 527.
 #include <algorithm>
 
 #include "device_common.h"
@@ -63,13 +63,26 @@ MOK_DEV double wave_sum(double v) {
   return v;
 }
 
-// The lane's best (key, id) -> the wave's: the largest key, of equal ones the least id.
+template <int CTRL> MOK_DEV uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+// The lane's best (key, id) -> the wave's: the largest key, of equal ones the least id. Within the rows of
+// 16 lanes by rotations, then across them.
 MOK_DEV void wave_best(uint64_t& key, int& id) {
+  auto step = [&](uint32_t lo, uint32_t hi, int oi) {
+    const uint64_t ok = ((uint64_t)hi << 32) | lo;
+    const bool better = ok > key || (ok == key && oi < id);
+    key = better ? ok : key;
+    id = better ? oi : id;
+  };
+  step(dpp<0x128>((uint32_t)key), dpp<0x128>((uint32_t)(key >> 32)), (int)dpp<0x128>((uint32_t)id));
+  step(dpp<0x124>((uint32_t)key), dpp<0x124>((uint32_t)(key >> 32)), (int)dpp<0x124>((uint32_t)id));
+  step(dpp<0x122>((uint32_t)key), dpp<0x122>((uint32_t)(key >> 32)), (int)dpp<0x122>((uint32_t)id));
+  step(dpp<0x121>((uint32_t)key), dpp<0x121>((uint32_t)(key >> 32)), (int)dpp<0x121>((uint32_t)id));
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
+  for (int m = 16; m < 64; m <<= 1) {
     const uint64_t ok = shfl_xor_u64(key, m);
-    const int oi = __shfl_xor(id, m, kWave);
-    if (ok > key || (ok == key && oi < id)) { key = ok; id = oi; }
+    step((uint32_t)ok, (uint32_t)(ok >> 32), __shfl_xor(id, m, kWave));
   }
 }
 
@@ -151,6 +164,262 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored_exact(const RsArgs a) {
   const int wv = threadIdx.x >> 6;
   const int64_t t = blockIdx.x * (int64_t)(RS_NT / 64) + wv;
   if (t < a.T) row_exact(a, t, key[wv], worth[wv]);
+}
+
+// ----------------------------------------------------------------------- float32, four rows a wave
+// A row is 16 lanes, lane l with the C = ceil(E / 16) <= Q values from l C on. Every value becomes a key:
+// the float32's bits in the order of unsigned numbers, the lowest four or five of them replaced by its
+// place in the lane. A lane sorts its 8 largest; k rounds then take the row's largest of 16 heads.
+
+// Over the row's 16 lanes, the result in each (rotations by 8, 4, 2, 1).
+MOK_DEV uint32_t row_max(uint32_t v) {
+  v = max(v, dpp<0x128>(v));
+  v = max(v, dpp<0x124>(v));
+  v = max(v, dpp<0x122>(v));
+  return max(v, dpp<0x121>(v));
+}
+MOK_DEV float row_maxf(float v) {
+  v = fmaxf(v, __uint_as_float(dpp<0x128>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp<0x124>(__float_as_uint(v))));
+  v = fmaxf(v, __uint_as_float(dpp<0x122>(__float_as_uint(v))));
+  return fmaxf(v, __uint_as_float(dpp<0x121>(__float_as_uint(v))));
+}
+MOK_DEV double row_sum(double v) {
+#pragma unroll
+  for (int m = 1; m < RS_LPR; m <<= 1) v += __shfl_xor(v, m, kWave);
+  return v;
+}
+
+MOK_DEV uint32_t key_of(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+MOK_DEV float value_of(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+constexpr uint32_t kLeftOut = 0x007FFFFFu;         // key_of(-inf): keys up to this are left-out experts'
+
+MOK_DEV void order2(uint32_t& a, uint32_t& b) {    // the larger first
+  const uint32_t m = max(a, b);
+  b = min(a, b);
+  a = m;
+}
+// Sorts K[0 .. 8) (N = 8) or [0 .. 4), largest first.
+template <int N> MOK_DEV void sort_keys(uint32_t* K) {
+  auto c = [&](int i, int j) { order2(K[i], K[j]); };
+  if constexpr (N == 4) {
+    c(0, 1); c(2, 3); c(0, 2); c(1, 3); c(1, 2);
+  } else {
+    c(0, 1); c(2, 3); c(4, 5); c(6, 7); c(0, 2); c(1, 3); c(4, 6); c(5, 7); c(1, 2); c(5, 6);
+    c(0, 4); c(1, 5); c(2, 6); c(3, 7); c(2, 4); c(3, 5); c(1, 2); c(3, 4); c(5, 6);
+  }
+}
+// A = the 8 largest of two sorted eights, sorted: the larger of A[i] and B[7 - i] are they, a bitonic row.
+MOK_DEV void merge8(uint32_t* A, const uint32_t* B) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) A[i] = max(A[i], B[7 - i]);
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) order2(A[i], A[i + d]);
+}
+
+template <int Q>
+__global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_logit) {
+  constexpr int H = Q < 8 ? Q : 8;                 // heads a lane keeps
+  constexpr uint32_t PLACE = Q > 16 ? 31u : 15u;
+  __shared__ int picks[RS_NT / RS_LPR][8];
+  // a wave's: float64 keys of a row, or the values of its four rows
+  __shared__ uint64_t xkey[RS_NT / 64][32 * Q], xworth[RS_NT / 64][RS_LPR];
+  const int l = threadIdx.x & 15, row = threadIdx.x >> 4, wv = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x * (int64_t)(RS_NT / RS_LPR) + row;
+  const bool live = t < a.T;
+  const float* lg = a.logits + min(t, a.T - 1) * a.E;
+  const int C = (a.E + RS_LPR - 1) / RS_LPR, e0 = l * C, n = max(0, min(C, a.E - e0));
+  float v[Q];
+  if (C == Q && a.E == RS_LPR * Q && ((uintptr_t)a.logits & 15) == 0) {
+#pragma unroll
+    for (int q = 0; q < Q; q += 4) {
+      const float4 u = *(const float4*)(lg + e0 + q);
+      v[q] = u.x; v[q + 1] = u.y; v[q + 2] = u.z; v[q + 3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) v[q] = q < n ? lg[e0 + q] : -INFINITY;
+  }
+  // c, or l. A row with NaN or +inf is done in float64.
+  bool redo = false;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) redo |= !(v[q] < INFINITY);
+  float top = -INFINITY;
+  double sum = 1.0;                                // softmax that is not renormalised: its sum
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) top = fmaxf(top, v[q]);
+    top = row_maxf(top);
+    if (!a.renorm && top > -INFINITY) {
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) s += expf(v[q] - top);
+      sum = row_sum((double)s);
+    }
+  }
+  // margin of a value x, m0 + m1 |x|: pairs further apart than this are in the order of float64. The bits
+  // that make room for the place count less than 2^-19 (2^-18) of x, both ways the same; c is rounded by
+  // 2^-24. A sigmoid is off by 1 unit of 2^-24 for its argument and exponential, 1 for 1 + x and 2 for the
+  // reciprocal: two of them by less than 6e-7. A softmax by 2^-24 of its argument (d e^-d < 0.4), 2 for the
+  // exponential, and by a factor of the sum's, common to the row, of less than 1.5e-6.
+  float m0 = by_logit ? 1e-6f : a.sigmoid ? 6e-7f : 3e-6f, m1 = Q > 16 ? 4.4e-6f : 2.4e-6f;
+  if (!by_logit) {
+    if (a.sigmoid) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) v[q] = v[q] == -INFINITY ? v[q] : __builtin_amdgcn_rcpf(1.0f + __expf(-v[q]));
+    } else {
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const float x = __expf(v[q] - top);
+        s += x;
+        v[q] = v[q] == -INFINITY ? v[q] : x;
+      }
+      const float inv = (float)(1.0 / row_sum((double)s));
+#pragma unroll
+      for (int q = 0; q < Q; ++q) v[q] *= inv;
+      if (!a.bias) { m0 = 0.0f; m1 += 4e-5f; }
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) v[q] += q < n ? a.bias[e0 + q] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) redo |= !(v[q] < INFINITY);
+    }
+  }
+  uint32_t kept = 0xFFFFFFFFu;                     // lane's values that are available
+  if (a.Gk < a.G) {
+    const int gs = a.E / a.G, L = gs / C;
+    float w1 = -INFINITY, w2 = -INFINITY;
+    const bool aligned = a.E == RS_LPR * C && gs % C == 0 && (L & (L - 1)) == 0;
+    int g;                                         // the group whose worth this lane has (G: none)
+    if (aligned) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (q < C) {
+          w2 = fmaxf(w2, fminf(w1, v[q]));
+          w1 = fmaxf(w1, v[q]);
+        }
+      for (int m = 1; m < L; m <<= 1) {
+        const float o1 = __shfl_xor(w1, m, kWave), o2 = __shfl_xor(w2, m, kWave);
+        w2 = fmaxf(fminf(w1, o1), fmaxf(w2, o2));
+        w1 = fmaxf(w1, o1);
+      }
+      g = l / L;
+    } else {
+      // through LDS: lane g goes over group g
+      float* const f = (float*)xkey[wv] + (row & 3) * (16 * Q);
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (q < n) f[e0 + q] = v[q];
+      wave_sync();
+      g = l < a.G ? l : a.G;
+      if (l < a.G)
+        for (int e = l * gs; e < (l + 1) * gs; ++e) {
+          w2 = fmaxf(w2, fminf(w1, f[e]));
+          w1 = fmaxf(w1, f[e]);
+        }
+      wave_sync();
+    }
+    const float w = a.top == 1 || w2 == -INFINITY ? w1 : w1 + w2;
+    const int step = aligned ? L : 1;
+    int rank = 0;
+    for (int r = 1; r < a.G; ++r) {
+      // group (g + r) % G
+      const int og = g + r >= a.G ? g + r - a.G : g + r;
+      const float o = __shfl(w, min(og * step, 15), RS_LPR);
+      rank += o > w || (o == w && og < g);
+    }
+    const bool in = g < a.G && rank < a.Gk, out = g < a.G && !in;
+    const float least = -row_maxf(in ? -w : -INFINITY), most = row_maxf(out ? w : -INFINITY);
+    redo |= most > -INFINITY && least - most < 2.0f * m0 + 2.0f * m1 * fabsf(least);
+    if (by_logit && most > -INFINITY)              // where float64 scores may be equal
+      redo |= a.sigmoid ? most > 20.0f || least < -700.0f : least - top < -700.0f;
+    if (aligned) {
+      kept = in ? kept : 0;
+    } else {
+      const uint32_t mask = (uint32_t)(ballot(in) >> (threadIdx.x & 48)) & 0xFFFFu;
+      kept = 0;
+      int gg = e0 / gs, left = (gg + 1) * gs - e0;           // group of value q, values left of it
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        kept |= ((mask >> min(gg, 31)) & 1u) << q;
+        if (--left == 0) { ++gg; left = gs; }
+      }
+    }
+  }
+  uint32_t K[Q < 8 ? 8 : Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    K[q] = q < n && ((kept >> q) & 1u) ? (key_of(v[q]) & ~PLACE) | (uint32_t)q : 0u;
+#pragma unroll
+  for (int q = 0; q < Q; q += H) sort_keys<H>(K + q);
+#pragma unroll
+  for (int q = 8; q < Q; q += 8) merge8(K, K + q);
+  // rounds: the last one only for its distance from pick k - 1
+  float prev = INFINITY;
+  int used = 0;
+  for (int j = 0; j <= a.k; ++j) {
+    const uint32_t m = row_max(K[0]);
+    const bool mine = K[0] == m;
+    const uint32_t hits = (uint32_t)(ballot(mine) >> (threadIdx.x & 48)) & 0xFFFFu;
+    const float x = value_of(m | PLACE);
+    const bool left_out = (m & ~PLACE) <= kLeftOut;
+    if (j < a.k) {
+      redo |= (hits & (hits - 1)) != 0;            // two of one key (or nothing left in the heads)
+      if (by_logit && !left_out)                   // where float64 scores may be equal
+        redo |= a.sigmoid ? x > 20.0f || x < -700.0f : x - top < -700.0f;
+      if (mine) picks[row][j] = e0 + (int)(m & PLACE);
+    }
+    if (m0 == 0.0f) redo |= !left_out && x < 1e-30f;         // near float32's end
+    redo |= !left_out && j > 0 && !(prev - x > (by_logit ? m0 * fmaxf(1.0f, fabsf(prev)) : m0) + m1 * fabsf(prev));
+    prev = x;
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i + 1 < H; ++i) K[i] = K[i + 1];
+      K[H - 1] = 0;
+      ++used;
+    }
+  }
+  if (H < Q) redo |= used >= H;                    // a lane may have had more
+  redo &= live;
+  wave_sync();
+  // weights: lane j has pick j
+  const bool has = l < a.k;
+  const int e = has ? picks[row][l] : 0;
+  const bool any = ((ballot(redo) >> (threadIdx.x & 48)) & 0xFFFFu) != 0;
+  const float x = has && !any ? lg[e] : -INFINITY;
+  double s;
+  if (a.sigmoid) {
+    s = 1.0 / (1.0 + exp(-(double)x));
+  } else {
+    const float base = a.renorm ? row_maxf(x) : top;
+    s = base > -INFINITY ? exp((double)x - (double)base) / sum : 0.0;
+  }
+  if (!has) s = 0.0;
+  if (a.renorm) {
+    const double all = row_sum(s);
+    s = all == 0.0 ? 0.0 : s / all;
+  }
+  if (has && live && !any) {
+    a.idx[t * a.k + l] = e;
+    a.w[t * a.k + l] = (float)(a.scale * s);
+  }
+  uint64_t rows = ballot(any);
+  while (rows) {
+    const int r = (__ffsll((unsigned long long)rows) - 1) >> 4;
+    rows &= ~(0xFFFFull << (16 * r));
+    row_exact(a, blockIdx.x * (int64_t)(RS_NT / RS_LPR) + 4 * wv + r, xkey[wv], xworth[wv]);
+    wave_sync();
+  }
 }
 
 // ------------------------------------------------------------------------------- gradient
@@ -296,8 +565,17 @@ int rs_check_groups(int32_t E, int32_t k, int32_t G, int32_t Gk, int32_t top, fl
 }
 
 hipError_t launch_scored(const RsArgs& a, hipStream_t s) {
-  launch_k(k_topk_scored_exact, dim3((unsigned)((a.T + 3) / 4)), dim3(RS_NT), 0, s, nullptr,
-           nullptr, a);
+  if (a.E > 512 || a.k > 8 || (a.G > RS_LPR && a.Gk < a.G)) {
+    launch_k(k_topk_scored_exact, dim3((unsigned)((a.T + 3) / 4)), dim3(RS_NT), 0, s, nullptr, nullptr, a);
+  } else {
+    // c grows with l alone: no bias, and no sums of two
+    const bool by_logit = !a.bias && (a.Gk == a.G || a.top == 1);
+    const int C = (a.E + RS_LPR - 1) / RS_LPR;
+    auto k = C <= 4 ? k_topk_scored<4> : C <= 8 ? k_topk_scored<8> : C <= 16 ? k_topk_scored<16>
+             : C <= 24 ? k_topk_scored<24> : k_topk_scored<32>;
+    constexpr int rows = RS_NT / RS_LPR;
+    launch_k(k, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(RS_NT), 0, s, nullptr, nullptr, a, by_logit);
+  }
   return hipGetLastError();
 }
 
@@ -349,8 +627,8 @@ int mok_topk_scored_backward(const float* logits, const int32_t* topk_idx, const
   if (!logits || !topk_idx || !dtopk_w || !dlogits) return MOK_EINVAL;
   RsBwd a = {logits, topk_idx, dtopk_w, dlogits_in, dlogits, T, E, k, score == MOK_SCORE_SIGMOID,
              renorm != 0, 0, scale};
-  // rows of a workgroup: 16 KB of their place in LDS, at most 64
-  a.rows = std::max(1, std::min(64, 4096 / E));
+  // rows of a workgroup: at most 16 KB of their place in LDS, 64, and what leaves 1024 workgroups
+  a.rows = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(64, 4096 / E), T / 1024));
   const dim3 grid((unsigned)((T + a.rows - 1) / a.rows));
   const uint32_t lds = (uint32_t)(a.rows * E * sizeof(float));
   hipStream_t s = (hipStream_t)stream;
