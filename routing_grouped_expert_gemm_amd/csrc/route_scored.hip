@@ -7,10 +7,10 @@
 //   w[j] = scale s[e_j] (/ sum_i s[e_i])
 //
 // Whole numbers hang on c, so c and the worths are float64 by definition. Few rows need it: k_topk_scored
-// orders a row by float32 values (c, or l itself where c grows with l alone) whose error is bounded, and a
-// row in which two neighbours of the result's order lie closer than that bound allows is done again in
-// float64 by its wave (row_exact): one row in some hundreds of random logits. T 65,536, E 256, 8 groups,
-// k 8: 25 us; every row in float64 527.
+// orders a row by float32 values (c, or l itself where c grows with l alone) whose error is bounded. Where
+// neighbours of that order lie closer than the bound allows, c of those up to the next clear step (16 at
+// most) is formed in float64 and they are ordered by it; rows with groups that close, with NaN, with scores
+// at float64's ends or with nothing left are done in float64 from the start by their wave (row_exact).
 #include <algorithm>
 
 #include "device_common.h"
@@ -112,14 +112,24 @@ MOK_DEV void row_exact(const RsArgs& a, int64_t t, uint64_t* key, uint64_t* wort
   }
   wave_sync();
   if (a.Gk < a.G) {
-    for (int g = lane; g < a.G; g += 64) {
+    // P lanes a group: each its share of the members, then the best two of all
+    const int P = a.G > 32 ? 1 : 64 >> (32 - __clz(a.G - 1));
+    for (int g0 = 0; g0 < a.G; g0 += 64 / P) {
+      const int g = g0 + lane / P;
       uint64_t m1 = 1, m2 = 1;
-      for (int e = g * gs; e < (g + 1) * gs; ++e) {
-        const uint64_t c = key[e];
-        if (c > m1) { m2 = m1; m1 = c; }
-        else if (c > m2) m2 = c;
+      if (g < a.G)
+        for (int e = g * gs + lane % P; e < (g + 1) * gs; e += P) {
+          const uint64_t c = key[e];
+          m2 = max(m2, min(m1, c));
+          m1 = max(m1, c);
+        }
+      for (int m = 1; m < P; m <<= 1) {
+        const uint64_t o1 = shfl_xor_u64(m1, m), o2 = shfl_xor_u64(m2, m);
+        m2 = max(min(m1, o1), max(m2, o2));
+        m1 = max(m1, o1);
       }
-      worth[g] = m1 == 1 || m2 == 1 || a.top == 1 ? m1 : order_key(key_value(m1) + key_value(m2));
+      if (g < a.G && lane % P == 0)
+        worth[g] = m1 == 1 || m2 == 1 || a.top == 1 ? m1 : order_key(key_value(m1) + key_value(m2));
     }
     wave_sync();
     for (int r = 0; r < a.Gk; ++r) {
@@ -229,7 +239,7 @@ template <int Q>
 __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_logit) {
   constexpr int H = Q < 8 ? Q : 8;                 // heads a lane keeps
   constexpr uint32_t PLACE = Q > 16 ? 31u : 15u;
-  __shared__ int picks[RS_NT / RS_LPR][8];
+  __shared__ int picks[RS_NT / RS_LPR][RS_LPR];
   // a wave's: float64 keys of a row, or the values of its four rows
   __shared__ uint64_t xkey[RS_NT / 64][32 * Q], xworth[RS_NT / 64][RS_LPR];
   const int l = threadIdx.x & 15, row = threadIdx.x >> 4, wv = threadIdx.x >> 6;
@@ -237,17 +247,21 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_l
   const bool live = t < a.T;
   const float* lg = a.logits + min(t, a.T - 1) * a.E;
   const int C = (a.E + RS_LPR - 1) / RS_LPR, e0 = l * C, n = max(0, min(C, a.E - e0));
-  float v[Q];
-  if (C == Q && a.E == RS_LPR * Q && ((uintptr_t)a.logits & 15) == 0) {
+  float v[Q], bias[Q];
+  auto load = [&](const float* p, float (&to)[Q], float none) {
+    if (a.E == RS_LPR * Q && ((uintptr_t)p & 15) == 0) {
 #pragma unroll
-    for (int q = 0; q < Q; q += 4) {
-      const float4 u = *(const float4*)(lg + e0 + q);
-      v[q] = u.x; v[q + 1] = u.y; v[q + 2] = u.z; v[q + 3] = u.w;
+      for (int q = 0; q < Q; q += 4) {
+        const float4 u = *(const float4*)(p + e0 + q);
+        to[q] = u.x; to[q + 1] = u.y; to[q + 2] = u.z; to[q + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) to[q] = q < n ? p[e0 + q] : none;
     }
-  } else {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) v[q] = q < n ? lg[e0 + q] : -INFINITY;
-  }
+  };
+  load(lg, v, -INFINITY);
+  if (a.bias) load(a.bias, bias, 0.0f);
   // c, or l. A row with NaN or +inf is done in float64.
   bool redo = false;
 #pragma unroll
@@ -290,7 +304,7 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_l
     }
     if (a.bias) {
 #pragma unroll
-      for (int q = 0; q < Q; ++q) v[q] += q < n ? a.bias[e0 + q] : 0.0f;
+      for (int q = 0; q < Q; ++q) v[q] += bias[q];
 #pragma unroll
       for (int q = 0; q < Q; ++q) redo |= !(v[q] < INFINITY);
     }
@@ -340,7 +354,9 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_l
     }
     const bool in = g < a.G && rank < a.Gk, out = g < a.G && !in;
     const float least = -row_maxf(in ? -w : -INFINITY), most = row_maxf(out ? w : -INFINITY);
-    redo |= most > -INFINITY && least - most < 2.0f * m0 + 2.0f * m1 * fabsf(least);
+    // (worths carry no places: m0 of each member, and roundings; by_logit they are logits themselves)
+    const float near = by_logit ? m0 * fmaxf(1.0f, fabsf(least)) : 2.0f * m0 + (m0 == 0.0f ? 9e-5f : 4e-7f) * fabsf(least);
+    redo |= most > -INFINITY && least - most < near;
     if (by_logit && most > -INFINITY)              // where float64 scores may be equal
       redo |= a.sigmoid ? most > 20.0f || least < -700.0f : least - top < -700.0f;
     if (aligned) {
@@ -364,44 +380,66 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_l
   for (int q = 0; q < Q; q += H) sort_keys<H>(K + q);
 #pragma unroll
   for (int q = 8; q < Q; q += 8) merge8(K, K + q);
-  // rounds: the last one only for its distance from pick k - 1
+  // Rounds: the row's candidates in the order of their keys, k and on to the first that lies clear of the
+  // one before it. near: two of them do not, and their order has to be found.
   float prev = INFINITY;
-  int used = 0;
-  for (int j = 0; j <= a.k; ++j) {
+  int used = 0, n_cand = 0;
+  bool near = false;
+  for (int j = 0; j <= RS_LPR; ++j) {
     const uint32_t m = row_max(K[0]);
-    const bool mine = K[0] == m;
-    const uint32_t hits = (uint32_t)(ballot(mine) >> (threadIdx.x & 48)) & 0xFFFFu;
+    const uint32_t hits = (uint32_t)(ballot(K[0] == m) >> (threadIdx.x & 48)) & 0xFFFFu;
     const float x = value_of(m | PLACE);
     const bool left_out = (m & ~PLACE) <= kLeftOut;
-    if (j < a.k) {
-      redo |= (hits & (hits - 1)) != 0;            // two of one key (or nothing left in the heads)
-      if (by_logit && !left_out)                   // where float64 scores may be equal
-        redo |= a.sigmoid ? x > 20.0f || x < -700.0f : x - top < -700.0f;
-      if (mine) picks[row][j] = e0 + (int)(m & PLACE);
-    }
-    if (m0 == 0.0f) redo |= !left_out && x < 1e-30f;         // near float32's end
-    redo |= !left_out && j > 0 && !(prev - x > (by_logit ? m0 * fmaxf(1.0f, fabsf(prev)) : m0) + m1 * fabsf(prev));
-    prev = x;
-    if (mine) {
+    // (nothing left, and experts that are left out behind others, are clear)
+    const bool clear = m == 0 || j == 0 || prev - x > (by_logit ? m0 * fmaxf(1.0f, fabsf(prev)) : m0) + m1 * fabsf(prev);
+    if (j >= a.k && clear && n_cand == 0) n_cand = j;
+    if (ballot(n_cand == 0) == 0 || j == RS_LPR) break;
+    if (n_cand == 0) {
+      near |= !clear;
+      if (j < a.k) {
+        if (by_logit && !left_out)                 // where float64 scores may be equal
+          redo |= a.sigmoid ? x > 20.0f || x < -700.0f : x - top < -700.0f;
+        if (m0 == 0.0f) redo |= !left_out && x < 1e-30f;         // near float32's end
+      }
+      if (l == __ffs(hits) - 1) {
+        picks[row][j] = e0 + (int)(m & PLACE);
 #pragma unroll
-      for (int i = 0; i + 1 < H; ++i) K[i] = K[i + 1];
-      K[H - 1] = 0;
-      ++used;
+        for (int i = 0; i + 1 < H; ++i) K[i] = K[i + 1];
+        K[H - 1] = 0;
+        ++used;
+      }
+      prev = x;
     }
   }
+  redo |= n_cand == 0;                             // more than 16 that have to be told apart
   if (H < Q) redo |= used >= H;                    // a lane may have had more
+  redo |= near && !a.sigmoid && a.bias;            // c needs the softmax's sum in float64
   redo &= live;
   wave_sync();
-  // weights: lane j has pick j
-  const bool has = l < a.k;
-  const int e = has ? picks[row][l] : 0;
+  // lane j has candidate j; the picks are those of rank below k
   const bool any = ((ballot(redo) >> (threadIdx.x & 48)) & 0xFFFFu) != 0;
-  const float x = has && !any ? lg[e] : -INFINITY;
-  double s;
-  if (a.sigmoid) {
-    s = 1.0 / (1.0 + exp(-(double)x));
-  } else {
-    const float base = a.renorm ? row_maxf(x) : top;
+  const bool cand = l < n_cand && !any;
+  const int e = cand ? picks[row][l] : 0;
+  const float x = cand ? lg[e] : -INFINITY;
+  double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : 0.0;
+  int slot = l;
+  if (ballot(near && cand)) {
+    double c = a.sigmoid ? s : exp((double)x - (double)top);
+    if (a.bias) c += cand ? (double)a.bias[e] : 0.0;
+    if (x == -INFINITY) c = -INFINITY;
+    const int id = cand ? e : RS_MAXE + l;
+    int rank = 0;
+#pragma unroll
+    for (int r = 1; r < RS_LPR; ++r) {
+      const double o = __shfl(c, l + r, RS_LPR);
+      const int oi = __shfl(id, l + r, RS_LPR);
+      rank += o > c || (o == c && oi < id);
+    }
+    slot = rank;
+  }
+  const bool has = cand && slot < a.k;
+  if (!a.sigmoid) {
+    const float base = a.renorm ? row_maxf(has ? x : -INFINITY) : top;
     s = base > -INFINITY ? exp((double)x - (double)base) / sum : 0.0;
   }
   if (!has) s = 0.0;
@@ -409,9 +447,9 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_l
     const double all = row_sum(s);
     s = all == 0.0 ? 0.0 : s / all;
   }
-  if (has && live && !any) {
-    a.idx[t * a.k + l] = e;
-    a.w[t * a.k + l] = (float)(a.scale * s);
+  if (has && live) {
+    a.idx[t * a.k + slot] = e;
+    a.w[t * a.k + slot] = (float)(a.scale * s);
   }
   uint64_t rows = ballot(any);
   while (rows) {
@@ -504,25 +542,38 @@ MOK_DEV void scatter_picks(const RsBwd& a, int64_t t0, int n, float* st, const f
 }
 
 // Softmax renormalised over the picks, and sigmoid: the gradient is zero outside the picks.
-template <int LK>
+// V: 4 values a thread where rows and addresses allow, or 1. The loads of dlogits_in go first, over the
+// picks' work.
+template <int LK, int V>
 __global__ __launch_bounds__(RS_NT) void k_topk_scored_bwd(const RsBwd a) {
-  extern __shared__ float st[];
-  const int64_t t0 = blockIdx.x * (int64_t)a.rows;
-  const int n = (int)min((int64_t)a.rows, a.T - t0);
-  const int elems = n * a.E;
-  for (int i = threadIdx.x; i < elems; i += RS_NT) st[i] = 0.0f;
+  typedef float Vec __attribute__((ext_vector_type(V)));
+  extern __shared__ __attribute__((aligned(16))) float st[];
+  const int64_t t0 = blockIdx.x * (int64_t)a.rows, base = t0 * a.E;
+  const int n = (int)min((int64_t)a.rows, a.T - t0), elems = n * a.E / V;
+  constexpr int U = 4;
+  Vec in[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = threadIdx.x + u * RS_NT;
+    in[u] = a.in && i < elems ? ((const Vec*)(a.in + base))[i] : Vec(0.0f);
+  }
+  for (int i = threadIdx.x; i < elems; i += RS_NT) ((Vec*)st)[i] = Vec(0.0f);
   __syncthreads();
   scatter_picks<LK, false>(a, t0, n, st, nullptr, nullptr, nullptr);
   __syncthreads();
-  const int64_t base = t0 * a.E;
-  for (int i = threadIdx.x; i < elems; i += RS_NT)
-    a.out[base + i] = (a.in ? a.in[base + i] : 0.0f) + st[i];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = threadIdx.x + u * RS_NT;
+    if (i < elems) ((Vec*)(a.out + base))[i] = in[u] + ((Vec*)st)[i];
+  }
+  for (int i = threadIdx.x + U * RS_NT; i < elems; i += RS_NT)
+    ((Vec*)(a.out + base))[i] = (a.in ? ((const Vec*)(a.in + base))[i] : Vec(0.0f)) + ((Vec*)st)[i];
 }
 
 // Softmax as it is: dl = s (ds - sum_picks ds s) for every expert of the row.
 template <int LK>
 __global__ __launch_bounds__(RS_NT) void k_topk_scored_bwd_full(const RsBwd a) {
-  extern __shared__ float st[];
+  extern __shared__ __attribute__((aligned(16))) float st[];
   __shared__ float top[RS_NT], inv[RS_NT], dot[RS_NT];
   const int64_t t0 = blockIdx.x * (int64_t)a.rows, base = t0 * a.E;
   const int n = (int)min((int64_t)a.rows, a.T - t0);
@@ -633,9 +684,10 @@ int mok_topk_scored_backward(const float* logits, const int32_t* topk_idx, const
   const uint32_t lds = (uint32_t)(a.rows * E * sizeof(float));
   hipStream_t s = (hipStream_t)stream;
   const bool full = score == MOK_SCORE_SOFTMAX && !renorm;
+  const bool vec = E % 4 == 0 && (((uintptr_t)dlogits_in | (uintptr_t)dlogits) & 15) == 0;
   auto go = [&](auto LK) {
-    launch_k(full ? k_topk_scored_bwd_full<LK()> : k_topk_scored_bwd<LK()>, grid, dim3(RS_NT), lds,
-             s, nullptr, nullptr, a);
+    launch_k(full ? k_topk_scored_bwd_full<LK()> : vec ? k_topk_scored_bwd<LK(), 4> : k_topk_scored_bwd<LK(), 1>,
+             grid, dim3(RS_NT), lds, s, nullptr, nullptr, a);
   };
   if (k <= 8) go(std::integral_constant<int, 8>{});
   else go(std::integral_constant<int, 64>{});
