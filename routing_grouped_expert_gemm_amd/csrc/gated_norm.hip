@@ -14,7 +14,10 @@
 // float32, each output rounded once. HBM streams: a row stays in registers from its first sum to
 // its last output, each input read once and each output written once; TPR threads hold a row in NC
 // pieces of 8 values. The weights' gradients stay in registers from row to row of a workgroup, whose
-// shares a second launch adds in a fixed order: no atomics.
+// shares a second launch adds in a fixed order: no atomics. Rows that are not whole 16-byte pieces, or lie
+// at other addresses, take the same kernels with loads and stores of single values' alignment and a last
+// piece value by value (float32, T 1001, d 1111 both ways: one value a thread and step, three passes over
+// memory and four launches, 38 us; so 21 us).
 #include <algorithm>
 
 #include "device_common.h"
@@ -24,6 +27,40 @@
 
 namespace mok {
 namespace {
+
+// A row's piece of 8 values at p, of which the row has `left`. AL: whole 16-byte pieces at 16-byte addresses.
+typedef uint4 uint4_any __attribute__((aligned(2)));
+typedef float4 float4_any __attribute__((aligned(4)));
+template <class T, bool AL>
+MOK_DEV typename Piece<T>::Raw piece_load(const T* p, int left) {
+  if constexpr (AL) return Piece<T>::raw(p);
+  if (left >= 8) {
+    if constexpr (sizeof(T) == 2) return *(const uint4_any*)p;
+    else return {*(const float4_any*)p, *(const float4_any*)(p + 4)};
+  }
+  T v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : T(0);
+  return __builtin_bit_cast(typename Piece<T>::Raw, v);
+}
+template <class T, bool AL>
+MOK_DEV void piece_store(T* p, int left, const float (&v)[8]) {
+  if constexpr (AL) {
+    Piece<T>::store(p, v);
+  } else if (left >= 8) {
+    if constexpr (sizeof(T) == 2)
+      *(uint4_any*)p = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    else {
+      *(float4_any*)p = make_float4(v[0], v[1], v[2], v[3]);
+      *(float4_any*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = f32_to<T>(v[i]);
+  }
+}
 
 struct GnArgs {
   const void *y, *res, *w_post, *gate, *w_pre;
@@ -35,7 +72,7 @@ struct GnArgs {
   float eps, alpha, beta;
 };
 
-template <class T, int TPR, int NC>
+template <class T, int TPR, int NC, bool AL>
 __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm(const GnArgs a) {
   constexpr int NT = TPR > NORM_NT ? TPR : NORM_NT, RPB = NT / TPR;
   typedef Piece<T> P;
@@ -50,9 +87,9 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm(co
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     const int c = (n * TPR + l) * 8;
-    P::widen(ok(n) ? P::raw((const T*)a.y + at + c) : P::none(), u[n]);
-    rq[n] = ok(n) ? P::raw((const T*)a.res + at + c) : P::none();
-    gq[n] = ok(n) && a.gate ? P::raw((const T*)a.gate + row * a.gate_ld + c) : P::none();
+    P::widen(ok(n) ? piece_load<T, AL>((const T*)a.y + at + c, d - c) : P::none(), u[n]);
+    rq[n] = ok(n) ? piece_load<T, AL>((const T*)a.res + at + c, d - c) : P::none();
+    gq[n] = ok(n) && a.gate ? piece_load<T, AL>((const T*)a.gate + row * a.gate_ld + c, d - c) : P::none();
   }
   if (a.w_post) {
     double ss = 0.0;
@@ -66,7 +103,8 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm(co
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (ok(n)) P::load((const T*)a.w_post + (n * TPR + l) * 8, w);
+      const int c = (n * TPR + l) * 8;
+      if (ok(n)) P::widen(piece_load<T, AL>((const T*)a.w_post + c, d - c), w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[n][i] = norm_value<T>(u[n][i], w[i], rs);
     }
@@ -81,7 +119,8 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm(co
       const float v = a.gate ? g[i] * u[n][i] : u[n][i];
       u[n][i] = as_stored<T>(fmaf(a.beta, v, a.alpha * r[i]));
     }
-    if (ok(n)) P::store((T*)a.h + at + (n * TPR + l) * 8, u[n]);
+    const int c = (n * TPR + l) * 8;
+    if (ok(n)) piece_store<T, AL>((T*)a.h + at + c, d - c, u[n]);
   }
   if (!a.w_pre) return;
   double ss = 0.0;
@@ -98,10 +137,10 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm(co
     if (!ok(n)) continue;
     const int c = (n * TPR + l) * 8;
     float w[8];
-    P::load((const T*)a.w_pre + c, w);
+    P::widen(piece_load<T, AL>((const T*)a.w_pre + c, d - c), w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = norm_value<T>(u[n][i], w[i], rs);
-    P::store((T*)a.n + at + c, w);
+    piece_store<T, AL>((T*)a.n + at + c, d - c, w);
   }
 }
 
@@ -158,7 +197,7 @@ struct GnBwd {
 // A value of the norm that the backward multiplies by: v scale rs.
 MOK_DEV float unit(float v, const BwdScale& q) { return q.scale == 1.0f ? v * q.rs : v * q.scale * q.rs; }
 
-template <class T, int TPR, int NC>
+template <class T, int TPR, int NC, bool AL>
 __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bwd(const GnBwd a) {
   constexpr int NT = TPR > NORM_NT ? TPR : NORM_NT, RPB = NT / TPR;
   typedef Piece<T> P;
@@ -167,23 +206,25 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bw
   __shared__ double shd[2][NT / 64];
   __shared__ float fold[RPB > 1 ? RPB : 1][RPB > 1 ? TPR * NC * 8 : 1];
   const int l = threadIdx.x % TPR, r = threadIdx.x / TPR, d = a.d;
-  float wa[NC][8], wb[NC][8], wg[NC][8], aa[NC][8], ab[NC][8], ag[NC][8];
+  float aa[NC][8], ab[NC][8], ag[NC][8];
+  Raw wa[NC], wb[NC];
+  const T one = f32_to<T>(1.0f);
+  T ones[8] = {one, one, one, one, one, one, one, one};
+  // hq .. gq: the next row's, whose loads are issued before this row's sums (gq: or the gate of all rows)
+  constexpr bool AHEAD = TPR < 1024 || sizeof(T) == 2;      // float32 rows of 1024 threads: no registers for it
+  Raw hq[NC], nq[NC], oq[NC], yq[NC], gq[NC];
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     const int c = (n * TPR + l) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      wa[n][i] = wb[n][i] = wg[n][i] = 1.0f;
-      aa[n][i] = ab[n][i] = ag[n][i] = 0.0f;
-    }
+    for (int i = 0; i < 8; ++i) aa[n][i] = ab[n][i] = ag[n][i] = 0.0f;
+    wa[n] = wb[n] = gq[n] = __builtin_bit_cast(Raw, ones);
     if (c < d) {
-      if (a.w_post) P::load((const T*)a.w_post + c, wa[n]);
-      if (a.w_pre) P::load((const T*)a.w_pre + c, wb[n]);
-      if (a.gate && !a.gate_ld) P::load((const T*)a.gate + c, wg[n]);
+      if (a.w_post) wa[n] = piece_load<T, AL>((const T*)a.w_post + c, d - c);
+      if (a.w_pre) wb[n] = piece_load<T, AL>((const T*)a.w_pre + c, d - c);
+      if (a.gate && !a.gate_ld) gq[n] = piece_load<T, AL>((const T*)a.gate + c, d - c);
     }
   }
-  // the next row's loads are issued before this row's sums
-  Raw hq[NC], nq[NC], oq[NC], yq[NC], gq[NC];
   float ry = 0.0f, rh = 0.0f;
   auto fetch = [&](int64_t row) {
     const bool live = row < a.rows;
@@ -192,11 +233,11 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bw
       const int c = (n * TPR + l) * 8;
       const int64_t at = row * d + c;
       const bool ok = live && c < d;
-      oq[n] = ok && a.dh ? P::raw((const T*)a.dh + at) : P::none();
-      hq[n] = ok && a.dn ? P::raw((const T*)a.h + at) : P::none();
-      nq[n] = ok && a.dn ? P::raw((const T*)a.dn + at) : P::none();
-      yq[n] = ok ? P::raw((const T*)a.y + at) : P::none();
-      gq[n] = ok && a.gate && a.gate_ld ? P::raw((const T*)a.gate + at) : P::none();
+      oq[n] = ok && a.dh ? piece_load<T, AL>((const T*)a.dh + at, d - c) : P::none();
+      hq[n] = ok && a.dn ? piece_load<T, AL>((const T*)a.h + at, d - c) : P::none();
+      nq[n] = ok && a.dn ? piece_load<T, AL>((const T*)a.dn + at, d - c) : P::none();
+      yq[n] = ok ? piece_load<T, AL>((const T*)a.y + at, d - c) : P::none();
+      if (a.gate_ld) gq[n] = ok ? piece_load<T, AL>((const T*)a.gate + at, d - c) : P::none();
     }
     ry = live && a.w_post ? a.rstd_y[row] : 0.0f;
     rh = live && a.dn ? a.rstd_h[row] : 0.0f;
@@ -212,32 +253,38 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bw
   };
   int turn = 0;
   const int64_t stride = (int64_t)gridDim.x * RPB;
-  fetch((int64_t)blockIdx.x * RPB + r);
+  if (AHEAD) fetch((int64_t)blockIdx.x * RPB + r);
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += stride) {
     const int64_t row = r0 + r, at = row * d;
     const bool live = row < a.rows;
-    float h[NC][8], g[NC][8], o[NC][8], v[NC][8], gt[NC][8], dot = 0.0f;
+    float h[NC][8], g[NC][8], o[NC][8], v[NC][8], dot = 0.0f;
+    if (!AHEAD) fetch(row);
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       P::widen(hq[n], h[n]);
       P::widen(nq[n], g[n]);
       P::widen(oq[n], o[n]);
       P::widen(yq[n], v[n]);
-      P::widen(gq[n], gt[n]);
     }
     const float cy = ry, ch = rh;
-    fetch(row + stride);
+    Raw gc[NC];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) gc[n] = gq[n];
+    if (AHEAD) fetch(row + stride);
     if (a.dn) {
       const BwdScale q(ch, d, [&] { return squares_of(h, shd[0]); });
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
+      for (int n = 0; n < NC; ++n) {
+        float w[8];
+        P::widen(wb[n], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           h[n][i] = unit(h[n][i], q);
           ab[n][i] += g[n][i] * h[n][i];
-          g[n][i] *= wb[n][i];
+          g[n][i] *= w[i];
           dot += g[n][i] * h[n][i];
         }
+      }
       dot = row_total<TPR>(dot, sh[turn][0]) / (float)d;
 #pragma unroll
       for (int n = 0; n < NC; ++n)
@@ -255,7 +302,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bw
         float w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = a.alpha * o[n][i];
-        P::store((T*)a.dres + at + c, w);
+        piece_store<T, AL>((T*)a.dres + at + c, d - c, w);
       }
     }
     const BwdScale q(a.w_post ? cy : 1.0f, d, [&] { return squares_of(v, shd[1]); });
@@ -263,19 +310,21 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bw
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const int c = (n * TPR + l) * 8;
-      float dg[8];
+      float dg[8], w[8], gt[8];
+      P::widen(wa[n], w);
+      P::widen(gc[n], gt);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float b = a.beta * o[n][i];
         v[n][i] = unit(v[n][i], q);
-        dg[i] = b * (v[n][i] * wa[n][i]);
+        dg[i] = b * (v[n][i] * w[i]);
         ag[n][i] += dg[i];
-        o[n][i] = b * (a.gate_ld ? gt[n][i] : wg[n][i]);     // the gradient of u
+        o[n][i] = b * gt[i];                                  // the gradient of u
         aa[n][i] += o[n][i] * v[n][i];
-        o[n][i] *= wa[n][i];
+        o[n][i] *= w[i];
         dot += o[n][i] * v[n][i];
       }
-      if (a.dgate && live && c < d) P::store((T*)a.dgate + at + c, dg);
+      if (a.dgate && live && c < d) piece_store<T, AL>((T*)a.dgate + at + c, d - c, dg);
     }
     if (a.dy) {
       if (a.w_post) dot = row_total<TPR>(dot, sh[turn][1]) / (float)d;
@@ -290,7 +339,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bw
             o[n][i] = q.scale == 1.0f ? w : q.scale * w;
           }
         }
-        P::store((T*)a.dy + at + c, o[n]);
+        piece_store<T, AL>((T*)a.dy + at + c, d - c, o[n]);
       }
     }
     turn ^= 1;
@@ -302,7 +351,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bw
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
         const int c = (n * TPR + l) * 8;
-        if (c < d) Piece<float>::store(out + c, acc[n]);
+        if (c < d) piece_store<float, AL>(out + c, d - c, acc[n]);
       }
     } else {
       __syncthreads();
@@ -438,13 +487,13 @@ template <int TPR, int NC> struct Form {
 template <class T>
 hipError_t run_gated(const GnArgs& a, hipStream_t s) {
   const int d = a.d;
-  const bool vec = d % 8 == 0 && d <= 16384 && al16(a.y) && al16(a.res) && al16(a.w_post) &&
-                   al16(a.gate) && al16(a.w_pre) && al16(a.h) && al16(a.n);
+  const bool al = d % 8 == 0 && al16(a.y) && al16(a.res) && al16(a.w_post) && al16(a.gate) &&
+                  al16(a.w_pre) && al16(a.h) && al16(a.n);
   auto go = [&](auto F) {
-    launch_k(k_gated_norm<T, F.tpr, F.nc>, dim3((unsigned)((a.rows + F.rpb - 1) / F.rpb)),
-             dim3(F.nt), 0, s, nullptr, nullptr, a);
+    launch_k(al ? k_gated_norm<T, F.tpr, F.nc, true> : k_gated_norm<T, F.tpr, F.nc, false>,
+             dim3((unsigned)((a.rows + F.rpb - 1) / F.rpb)), dim3(F.nt), 0, s, nullptr, nullptr, a);
   };
-  if (!vec || a.rows > kMaxLaunchRows) {
+  if (d > 16384 || a.rows > kMaxLaunchRows) {
     const bool wide = d > 2048;
     for (int64_t r = 0; r < a.rows; r += kMaxLaunchRows)
       launch_k(wide ? k_gated_norm_any<T, 1024> : k_gated_norm_any<T, 256>,
@@ -466,7 +515,7 @@ template <class T>
 hipError_t run_gated_bwd(GnBwd a, float* dgate_all, float* dw_post, float* dw_pre, float* ws,
                          hipStream_t s) {
   const int d = a.d, blocks = bwd_blocks(a.rows);
-  const bool vec = d % 8 == 0 && d <= 8192 && al16(a.dh) && al16(a.dn) && al16(a.y) && al16(a.h) &&
+  const bool al = d % 8 == 0 && al16(a.dh) && al16(a.dn) && al16(a.y) && al16(a.h) &&
                    al16(a.w_post) && al16(a.gate) && al16(a.w_pre) && al16(a.dres) && al16(a.dy) &&
                    al16(a.dgate);
   const size_t part = (size_t)blocks * d;
@@ -484,10 +533,11 @@ hipError_t run_gated_bwd(GnBwd a, float* dgate_all, float* dw_post, float* dw_pr
   a.stat = n_sums ? ws + 3 * part : nullptr;
   auto go = [&](auto F) {
     n_part = (int)std::min<int64_t>(n_sums ? blocks : 1 << 16, (a.rows + F.rpb - 1) / F.rpb);
-    launch_k(k_gated_norm_bwd<T, F.tpr, F.nc>, dim3(n_part), dim3(F.nt), 0, s, nullptr, nullptr, a);
+    launch_k(al ? k_gated_norm_bwd<T, F.tpr, F.nc, true> : k_gated_norm_bwd<T, F.tpr, F.nc, false>,
+             dim3(n_part), dim3(F.nt), 0, s, nullptr, nullptr, a);
   };
   if (a.rows == 0) {
-  } else if (!vec) {
+  } else if (d > 8192) {
     const bool wide = d > 2048;
     for (int64_t r = 0; r < a.rows; r += kMaxLaunchRows)
       launch_k(wide ? k_gated_norm_bwd_any<T, 1024> : k_gated_norm_bwd_any<T, 256>,
@@ -499,7 +549,7 @@ hipError_t run_gated_bwd(GnBwd a, float* dgate_all, float* dw_post, float* dw_pr
   } else if (d <= 512) go(Form<64, 1>{});
   else if (d <= 1024) go(Form<64, 2>{});
   else if (d <= 2048) go(Form<256, 1>{});
-  else if (d <= 4096) go(Form<256, 2>{});
+  else if (d <= 4096) go(Form<512, 1>{});      // (256, 2) leaves one wave a SIMD
   else go(Form<1024, 1>{});
   if (n_sums)
     launch_k(k_gated_norm_sum, dim3((d + 15) / 16, n_sums), dim3(1024), 0, s, nullptr, nullptr,
