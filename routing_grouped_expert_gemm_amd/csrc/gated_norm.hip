@@ -17,7 +17,7 @@
 // shares a second launch adds in a fixed order: no atomics. Rows that are not whole 16-byte pieces, or lie
 // at other addresses, take the same kernels with loads and stores of single values' alignment and a last
 // piece value by value (float32, T 1001, d 1111 both ways: one value a thread and step, three passes over
-// memory and four launches, 38 us; so 21 us).
+// memory and four launches, 38 us; so 27 us).
 #include <algorithm>
 
 #include "device_common.h"
@@ -500,12 +500,13 @@ hipError_t run_gated(const GnArgs& a, hipStream_t s) {
                dim3((unsigned)std::min(a.rows - r, kMaxLaunchRows)), dim3(wide ? 1024 : 256), 0, s,
                nullptr, nullptr, a, r);
   } else if (d <= 512) go(Form<64, 1>{});
-  // few rows (fewer workgroups than CUs): more threads a row, for the row's latency
-  else if (a.rows <= 256 && d <= 2048) go(Form<256, 1>{});
-  else if (a.rows <= 256 && d <= 8192) go(Form<1024, 1>{});
+  // 256 threads a row beyond 1024 values (float32 T 1001, d 1111: 9.3 us, with 64 threads 12.8; bf16 T 8192,
+  // d 2048: 39 and 41), and for few rows (fewer workgroups than CUs) before that, for the row's latency
+  else if (d <= 2048 && (d > 1024 || a.rows <= 256)) go(Form<256, 1>{});
   else if (d <= 1024) go(Form<64, 2>{});
-  else if (d <= 2048) go(Form<64, 4>{});
+  else if (a.rows <= 256 && d <= 8192) go(Form<1024, 1>{});
   else if (d <= 4096) go(Form<256, 2>{});
+  // (bf16 T 8192, d 7168: 108 us, with 512 threads a row 109, with 1024 145)
   else if (d <= 8192) go(Form<256, 4>{});
   else go(Form<1024, 2>{});
   return hipGetLastError();
