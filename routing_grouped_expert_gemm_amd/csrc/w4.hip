@@ -18,10 +18,12 @@
 //    MFMA. A code less its zero point is a byte: 4 (with zero points 7) vector operations for 8 codes.
 //    The group's sums are exact; a lane's accumulators are the three bytes' sums of row kq and column n, so
 //    that scale and exponent are one fused multiply-add a group.
+//  k_w4_token the same, of all the experts of one token.
 //  k_w4_rows  up to 16 rows: the bf16 MFMA. A nibble 0 .. 15 is, as an E4M3 byte, q 2^-9 (its first two
 //    binades are evenly spaced), so one AND for four codes and a conversion for two give exact bf16
 //    integers. x's products with a constant (-8, or 1, times -z) begin a group's float32 sum, which takes
 //    the zero point off; the sum is scaled in float32.
+//  k_w4_split the same for at most a tile a CU: x from the caches, up to 16 parts of K.
 //
 // The MoE's first launch writes H = silu(gate) up in float32, its second reads it (k_w4_rows: as two bf16
 // planes, 16 significant bits, in two rows of the MFMA); a third adds a token's experts in the order of
@@ -40,7 +42,8 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 constexpr int W4_BODY = 512;         // columns of a wave's step
 constexpr int W4_LOADS = W4_BODY / 128;
 constexpr int W4_MAXW = 8;           // waves of a workgroup
-constexpr int W4_LDS_FEW = 52 * 1024, W4_LDS_ROWS = 72 * 1024;   // for x: three and two workgroups a CU
+constexpr int W4_LDS_FEW = 52 * 1024, W4_LDS_ROWS = 72 * 1024;   // for x: two workgroups a CU
+constexpr int W4_STEP = 256, W4_PARTS = 16;   // k_w4_split: columns of a wave's step, most parts of K
 constexpr int W4_SCAN = 1024;        // routes up to which a workgroup finds its rows by itself
 enum { W4_DENSE = 0, W4_UP = 1, W4_DOWN = 2 };
 
@@ -65,6 +68,7 @@ struct W4Args {
   const int32_t *offsets, *route_ids;   // the plan (more than W4_SCAN routes), else NULL
   int64_t routes;
   int k, e0, El;
+  const void* y_in;                  // k_w4_token: bf16 [T, N] or NULL; out: y bf16 [T, N]
 };
 
 // Orders the wave's LDS accesses before this point against those behind it.
@@ -122,23 +126,24 @@ MOK_DEV bf16x8_t order8(const uint4 v) {
 }
 
 typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
 
-// The scales and zero points of a wave's tile row (of the lane) for one body.
-template <int G, bool Z>
+// The scales and zero points of a wave's tile row (of the lane) for one step (of BODY columns).
+template <int G, bool Z, int BODY = W4_BODY>
 struct W4Groups {
-  static constexpr int NG = W4_BODY / G;
+  static constexpr int NG = BODY / G, ZW = (NG + 3) / 4;
   uint32_t s[NG / 2];
-  uint32_t z[Z ? NG / 4 : 1];
+  uint32_t z[Z ? ZW : 1];
   MOK_DEV void load(const W4Mat& m, int64_t row, int K, int k) {
     const int ng = K / G, g0 = k / G;
     const uint16_t* sp = m.scales + row * ng + g0;
     const uint8_t* zp = Z ? m.zeros + row * ng + g0 : nullptr;
-    if (k + W4_BODY <= K) {
+    if (k + BODY <= K) {
 #pragma unroll
       for (int i = 0; i < NG / 2; ++i) s[i] = ((const u32_any*)sp)[i];
       if constexpr (Z)
 #pragma unroll
-        for (int i = 0; i < NG / 4; ++i) z[i] = ((const u32_any*)zp)[i];
+        for (int i = 0; i < ZW; ++i) z[i] = NG < 4 ? *(const u16_any*)zp : ((const u32_any*)zp)[i];
     } else {
 #pragma unroll
       for (int i = 0; i < NG / 2; ++i) {
@@ -147,10 +152,10 @@ struct W4Groups {
       }
       if constexpr (Z)
 #pragma unroll
-        for (int i = 0; i < NG / 4; ++i) {
+        for (int i = 0; i < ZW; ++i) {
           z[i] = 0;
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int b = 0; b < 4 && 4 * i + b < NG; ++b)
             if (g0 + 4 * i + b < ng) z[i] |= (uint32_t)zp[4 * i + b] << (8 * b);
         }
     }
@@ -163,8 +168,8 @@ struct W4Groups {
 };
 
 // total += the products of 128 columns (load i of a body), whose x are a[0 .. 3].
-template <int G, bool Z, int S>
-MOK_DEV void w4_step(const uint4 (&q)[S], const W4Groups<G, Z> (&gr)[S], int i, const bf16x8_t (&a)[4],
+template <int G, bool Z, int S, int BODY>
+MOK_DEV void w4_step(const uint4 (&q)[S], const W4Groups<G, Z, BODY> (&gr)[S], int i, const bf16x8_t (&a)[4],
                      f32x4_t (&total)[S]) {
   constexpr int J = G < 128 ? G / 32 : 4;            // instructions of a group
   const uint32_t c = Z ? 0x3F803F80u : 0xC100C100u;  // 1 or -8
@@ -212,25 +217,37 @@ struct W4Rows {
     // more local experts than routes: a slot is a route, and serves its expert if no earlier route
     // names it; otherwise a slot is an expert
     const bool by_route = p.routes < p.El;
-    int e = by_route ? p.idx[slot] : p.e0 + slot;
-    e = uniform(e);
-    if (e < p.e0 || e >= p.e0 + p.El) return false;
-    expert = e - p.e0;
     int n = 0;
-    for (int r0 = 0; r0 < (int)p.routes; r0 += 256) {
-      bool hit[4];
+    if (p.routes <= 64) {                  // one load
+      const int32_t mine = lane < p.routes ? p.idx[lane] : -1;
+      const int e = by_route ? __builtin_amdgcn_readlane(mine, slot) : p.e0 + slot;
+      if (e < p.e0 || e >= p.e0 + p.El) return false;
+      expert = e - p.e0;
+      const bool hit = mine == e && lane < p.routes;
+      const uint64_t mask = ballot(hit);
+      if (by_route && __ffsll((unsigned long long)mask) - 1 < slot) return false;
+      // every wave writes the list for itself (the same values), so that none waits
+      if (hit) own[__popcll(mask & lanemask_lt())] = (int16_t)lane;
+      n = __popcll(mask);
+    } else {
+      const int e = by_route ? uniform(p.idx[slot]) : p.e0 + slot;
+      if (e < p.e0 || e >= p.e0 + p.El) return false;
+      expert = e - p.e0;
+      for (int r0 = 0; r0 < (int)p.routes; r0 += 256) {
+        bool hit[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = r0 + 64 * q + lane;
-        hit[q] = r < p.routes && p.idx[r] == e;
-      }
+        for (int q = 0; q < 4; ++q) {
+          const int r = r0 + 64 * q + lane;
+          hit[q] = r < p.routes && p.idx[r] == e;
+        }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = r0 + 64 * q;
-        const uint64_t mask = ballot(hit[q]);
-        if (by_route && n == 0 && mask && r + __ffsll((unsigned long long)mask) - 1 < slot) return false;
-        if (hit[q]) own[n + __popcll(mask & lanemask_lt())] = (int16_t)(r + lane);
-        n += __popcll(mask);
+        for (int q = 0; q < 4; ++q) {
+          const int r = r0 + 64 * q;
+          const uint64_t mask = ballot(hit[q]);
+          if (by_route && n == 0 && mask && r + __ffsll((unsigned long long)mask) - 1 < slot) return false;
+          if (hit[q]) own[n + __popcll(mask & lanemask_lt())] = (int16_t)(r + lane);
+          n += __popcll(mask);
+        }
       }
     }
     count = n;
@@ -289,13 +306,13 @@ struct W4Tile {
   const uint8_t* code[S];
   uint32_t row_at, row_end;          // the lane's first bytes of a body; the last 16 bytes of its row
   int64_t row;
-  MOK_DEV W4Tile(const W4Args& p, int64_t expert, int n0) {
-    const int lane = lane_id(), lr = min(lane & 15, p.N - 1 - n0);
-    row = expert * p.N + n0 + lr;
+  MOK_DEV W4Tile(const W4Mat* w, int N, int K, int64_t expert, int n0) {
+    const int lane = lane_id(), lr = min(lane & 15, N - 1 - n0);
+    row = expert * N + n0 + lr;
 #pragma unroll
-    for (int s = 0; s < S; ++s) code[s] = p.w[s].codes + (expert * p.N + n0) * (int64_t)(p.K / 2);
-    row_at = lr * (uint32_t)(p.K / 2) + 16 * (lane >> 4);
-    row_end = lr * (uint32_t)(p.K / 2) + p.K / 2 - 16;
+    for (int s = 0; s < S; ++s) code[s] = w[s].codes + (expert * N + n0) * (int64_t)(K / 2);
+    row_at = lr * (uint32_t)(K / 2) + 16 * (lane >> 4);
+    row_end = lr * (uint32_t)(K / 2) + K / 2 - 16;
   }
   // load i of the body at column k; past K, where x is zero, the row's last codes
   MOK_DEV uint4 load(int s, int i, int k) const {
@@ -322,24 +339,151 @@ MOK_DEV void code_bytes(uint32_t w, uint32_t zc, int& even, int& odd) {
   }
 }
 
-// Workgroup (x, y): tiles x tpw .., rows y MR .. (dense) or expert slot y (MoE).
+// x's rows in LDS, as bytes: [rows][3][ck + 16], then the groups' exponents [rows][ck / G]. XF: 16 bytes that
+// 8 values take (bf16: 1, float32: 2).
+template <int G, int XF>
+struct W4Bytes {
+  static constexpr int XU = 2;         // units of 8 values that a thread has in flight
+  int8_t* xb;
+  const void* x;
+  int K, n_rows, ck, ld, ng, cw, units;
+  float* ex;
+  uint4 xv[XU][XF];
+  MOK_DEV W4Bytes(int8_t* lds, const void* x_, int K_, int rows, int ck_)
+      : xb(lds), x(x_), K(K_), n_rows(rows), ck(ck_), ld(ck_ + 16), ng(ck_ / G), cw(ck_ / 8), units(rows * (ck_ / 8)),
+        ex((float*)(lds + rows * 3 * (ck_ + 16))) {}
+  // the columns c ck .. : row_of(r) is where row r lies in x, in rows
+  template <class Row> MOK_DEV void load(int c, int u0, Row&& row_of) {
+#pragma unroll
+    for (int j = 0; j < XU; ++j) {
+      const int u = u0 + j * (int)blockDim.x, r = min(u / cw, n_rows - 1), k = c * ck + (u - r * cw) * 8;
+      const int64_t at = (int64_t)row_of(r) * K + min(k, K - 8);
+#pragma unroll
+      for (int i = 0; i < XF; ++i) {
+        const uint4 v = XF == 1 ? *(const uint4*)((const bf16_t*)x + at) : *(const uint4*)((const float*)x + at + 4 * i);
+        xv[j][i] = k < K ? v : make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  // A group is G / 8 neighbouring lanes (a row's units fill whole waves).
+  MOK_DEV void store(int u0) {
+#pragma unroll
+    for (int j = 0; j < XU; ++j) {
+      const int u = u0 + j * (int)blockDim.x;
+      if (u >= units) break;
+      const int r = u / cw, o = (u - r * cw) * 8;
+      float v[8];
+      const uint4 q = xv[j][0];
+      if constexpr (XF == 1) {
+        const uint32_t t[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = __uint_as_float(t[i] << 16);
+          v[2 * i + 1] = __uint_as_float(t[i] & 0xFFFF0000u);
+        }
+      } else {
+        const uint4 h = xv[j][XF - 1];
+        const uint32_t t[8] = {q.x, q.y, q.z, q.w, h.x, h.y, h.z, h.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(t[i]);
+      }
+      uint32_t top = 0;                              // exponent field of the largest; 255: not finite
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+      for (int m = 1; m < G / 8; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
+      const int e = max((int)(top >> 23), 1);
+      if (u % (G / 8) == 0)
+        ex[r * ng + o / G] = e == 255 ? NAN : __builtin_amdgcn_ldexpf(1.0f, e - 148);
+      uint32_t d[3][2] = {};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {                  // |v| < 2^22; bytes from the least, rounded to nearest
+        const int n0 = e == 255 ? 0 : (int)rintf(__builtin_amdgcn_ldexpf(v[i], 148 - e));
+        const int n1 = (n0 + 128) >> 8, n2 = (n1 + 128) >> 8;
+        const int h = i & 1, b = 8 * (i >> 1);       // the even ones, then the odd ones
+        d[2][h] |= (uint32_t)(n0 & 0xFF) << b;
+        d[1][h] |= (uint32_t)(n1 & 0xFF) << b;
+        d[0][h] |= (uint32_t)(n2 & 0xFF) << b;
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) *(uint2*)(xb + (r * 3 + q) * ld + o) = make_uint2(d[q][0], d[q][1]);
+    }
+  }
+  // Chunk c into LDS; loaded: the first units are in xv.
+  template <class Row> MOK_DEV void fill(int c, bool loaded, Row&& row_of) {
+    for (int u = threadIdx.x;;) {
+      if (!loaded || u != (int)threadIdx.x) load(c, u, row_of);
+      store(u);
+      u += XU * (int)blockDim.x;
+      if (u - (int)threadIdx.x >= units) break;
+    }
+  }
+  // Where the lane's row of the MFMA lies: byte ln % 4 of row first + ln / 4 (a fourth byte, and rows past the
+  // last, are not looked at), with its columns' place in 128; and the exponents of row first + kq.
+  MOK_DEV const int8_t* fragment(int first) const {
+    const int kq = lane_id() >> 4, ln = lane_id() & 15;
+    return xb + (min(first + (ln >> 2), n_rows - 1) * 3 + min(ln & 3, 2)) * ld +
+           (G == 128 ? 32 * kq : G == 64 ? 32 * (kq & 1) + 16 * (kq >> 1) : 8 * kq);
+  }
+  MOK_DEV const float* exponents(int first) const { return ex + min(first + (lane_id() >> 4), n_rows - 1) * ng; }
+};
+
+// total += a body's products (for zero-point-less codes 16 times); xl, xe: x's place at its first column. The
+// registers q take the codes of the body at column kn of tile w as they become free.
+template <int G, bool Z>
+MOK_DEV void w4_few_body(uint4 (&q)[W4_LOADS], const W4Groups<G, Z>& gr, const int8_t* xl, const float* xe,
+                         const W4Tile<1>& w, int kn, float& total) {
+#pragma unroll
+  for (int l = 0; l < W4_LOADS; ++l) {
+    uint32_t t[4] = {q[l].x, q[l].y, q[l].z, q[l].w};
+    if constexpr (G == 64) swap2(t);
+    if constexpr (G == 32) transpose4(t);
+    constexpr int NG = 128 / G, W = 4 / NG;          // groups of the load, words of a group
+    i32x4_t acc[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const uint32_t zc = Z ? 0x80808080u - gr.zero_byte(l * NG + g) * 0x01010101u : 0;
+      acc[g] = i32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < W; j += W > 1 ? 2 : 1) {
+        int lo[2], hi[2];
+        code_bytes<Z>(t[W * g + j], zc, lo[0], hi[0]);
+        if constexpr (W > 1) {
+          code_bytes<Z>(t[W * g + j + 1], zc, lo[1], hi[1]);
+          const i32x4_t a = *(const i32x4_t*)(xl + 128 * l + (G == 128 ? 8 * j : 64 * g));
+          acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, i32x4_t{lo[0], hi[0], lo[1], hi[1]}, acc[g], 0, 0, 0);
+        } else {
+          const long a = *(const long*)(xl + 128 * l + 32 * g);
+          acc[g] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)(uint32_t)lo[0] | ((long)hi[0] << 32), acc[g], 0, 0, 0);
+        }
+      }
+    }
+    q[l] = w.load(0, l, kn);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float v = fmaf((float)acc[g][0], 65536.0f, (float)((acc[g][1] << 8) + acc[g][2]));
+      total = fmaf(v * gr.scale(l * NG + g), xe[l * NG + g], total);
+    }
+  }
+}
+
+// Workgroup (x, y): tpw tiles, rows y MR .. (dense) or expert slot y (MoE).
 template <int G, bool Z, int MODE>
 __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_few(const W4Args p) {
-  constexpr int S = MODE == W4_UP ? 2 : 1, MR = 4, XF = MODE == W4_DOWN ? 2 : 1;     // XF: 16 bytes of 8 values
-  extern __shared__ __attribute__((aligned(16))) int8_t xb[];   // x [rows][3][ck + 16], then exponents [rows][ck / G]
+  constexpr int S = MODE == W4_UP ? 2 : 1, MR = 4;
+  extern __shared__ __attribute__((aligned(16))) int8_t xb[];
   __shared__ float red[W4_MAXW * 64];
   __shared__ int16_t list[MODE == W4_DENSE ? 1 : W4_SCAN];
-  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid >> 6), kq = lane >> 4, ln = lane & 15;
+  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid >> 6);
   W4Rows rows;
   if constexpr (MODE == W4_DENSE) rows.count = p.M;
   else if (!rows.find(p, blockIdx.y, list)) return;
   // S tiles, of gate and up, are a pair's; a workgroup has whole pairs
   const int tile = wv / p.ks, part = wv - tile * p.ks, t0 = blockIdx.x * (p.tpw / S);
-  const int nt = min(p.tpw / S, p.tiles - t0);
+  const int nt = min(p.tpw / S, p.tiles - t0);                          // pairs of the workgroup
   const bool idle = tile >= nt * S;
-  W4Args one = p;
-  one.w[0] = p.w[S == 2 ? tile % 2 : 0];
-  const W4Tile<1> w(one, rows.expert, idle ? 0 : (t0 + tile / S) * 16);
+  const W4Mat& mat = p.w[S == 2 ? tile % 2 : 0];
+  const W4Tile<1> w(&mat, p.N, p.K, rows.expert, idle ? 0 : (t0 + tile / S) * 16);
   const int64_t m_first = MODE == W4_DENSE ? (int64_t)blockIdx.y * MR : 0;
   const int64_t m_end = MODE == W4_DENSE ? min(rows.count, m_first + MR) : rows.count;
   for (int64_t m0 = m_first; m0 < m_end; m0 += MR) {
@@ -347,149 +491,116 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_few(const W4Args p) {
     // bodies of a chunk and part; chunks
     const int bodies = (p.K + W4_BODY - 1) / W4_BODY, bw = W4_BODY * p.ks;
     const int bpc = min((bodies + p.ks - 1) / p.ks, max(1, p.cap / (w4_few_bytes(G) * n_rows * p.ks)));
-    const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck, ld = ck + 16, ng = ck / G;
-    auto column = [&](int c, int b) { return c * ck + (part * bpc + b) * W4_BODY; };
-    float* const ex = (float*)(xb + n_rows * 3 * ld);
-    // x's columns c ck .. , 8 at a time: loaded ...
-    constexpr int XU = 2;
-    const int cw = ck / 8, units = n_rows * cw;
-    uint4 xv[XU][XF];
-    auto x_load = [&](int c, int u0) {
-#pragma unroll
-      for (int j = 0; j < XU; ++j) {
-        const int u = u0 + j * (int)blockDim.x, r = min(u / cw, n_rows - 1), k = c * ck + (u - r * cw) * 8;
-        const int64_t at = w4_x_row<MODE>(p, rows, m0 + r) * p.K + min(k, p.K - 8);
-#pragma unroll
-        for (int i = 0; i < XF; ++i) {
-          const uint4 v = XF == 1 ? *(const uint4*)((const bf16_t*)p.x + at) : *(const uint4*)((const float*)p.x + at + 4 * i);
-          xv[j][i] = k < p.K ? v : make_uint4(0, 0, 0, 0);
-        }
-      }
-    };
-    // ... and cut into bytes. A group is G / 8 neighbouring lanes (a row's units fill whole waves).
-    auto x_store = [&](int u0) {
-#pragma unroll
-      for (int j = 0; j < XU; ++j) {
-        const int u = u0 + j * (int)blockDim.x;
-        if (u >= units) break;
-        const int r = u / cw, o = (u - r * cw) * 8;
-        float v[8];
-        const uint4 q = xv[j][0];
-        if constexpr (XF == 1) {
-          const uint32_t t[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(t[i] << 16);
-            v[2 * i + 1] = __uint_as_float(t[i] & 0xFFFF0000u);
-          }
-        } else {
-          const uint4 h = xv[j][XF - 1];
-          const uint32_t t[8] = {q.x, q.y, q.z, q.w, h.x, h.y, h.z, h.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(t[i]);
-        }
-        uint32_t top = 0;                              // exponent field of the largest; 255: not finite
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int m = 1; m < G / 8; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
-        const int e = max((int)(top >> 23), 1);
-        if (u % (G / 8) == 0)
-          ex[r * ng + o / G] = e == 255 ? NAN : __builtin_amdgcn_ldexpf(1.0f, e - 148);
-        uint32_t d[3][2] = {};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {                  // |v| < 2^22; bytes from the least, rounded to nearest
-          const int n0 = e == 255 ? 0 : (int)rintf(__builtin_amdgcn_ldexpf(v[i], 148 - e));
-          const int n1 = (n0 + 128) >> 8, n2 = (n1 + 128) >> 8;
-          const int h = i & 1, b = 8 * (i >> 1);       // the even ones, then the odd ones
-          d[2][h] |= (uint32_t)(n0 & 0xFF) << b;
-          d[1][h] |= (uint32_t)(n1 & 0xFF) << b;
-          d[0][h] |= (uint32_t)(n2 & 0xFF) << b;
-        }
-#pragma unroll
-        for (int q = 0; q < 3; ++q) *(uint2*)(xb + (r * 3 + q) * ld + o) = make_uint2(d[q][0], d[q][1]);
-      }
-    };
+    const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck;
+    auto column = [&](int c, int b) { return min(c * ck + (part * bpc + b) * W4_BODY, p.K); };
+    auto row_of = [&](int r) { return w4_x_row<MODE>(p, rows, m0 + r); };
+    W4Bytes<G, MODE == W4_DOWN ? 2 : 1> x(xb, p.x, p.K, n_rows, ck);
     uint4 q[W4_LOADS];
     W4Groups<G, Z> gr;
-    float total = 0.0f;
-    x_load(0, tid);                                    // x first: waiting for it must not wait for the codes
+    x.load(0, tid, row_of);                            // x first: waiting for it must not wait for the codes
     __builtin_amdgcn_sched_barrier(0);
     if (!idle) {
-      gr.load(one.w[0], w.row, p.K, min(column(0, 0), p.K));
+      gr.load(mat, w.row, p.K, column(0, 0));
 #pragma unroll
       for (int l = 0; l < W4_LOADS; ++l) q[l] = w.load(0, l, column(0, 0));
     }
     __builtin_amdgcn_sched_barrier(0);
-    // the lane's row of the MFMA: byte ln % 4 of row ln / 4 (a fourth byte, and rows past the last, are not
-    // looked at), and where its columns lie in 128
-    const int8_t* const xl = xb + (min(ln >> 2, n_rows - 1) * 3 + min(ln & 3, 2)) * ld +
-                             (G == 128 ? 32 * kq : G == 64 ? 32 * (kq & 1) + 16 * (kq >> 1) : 8 * kq);
-    const float* const xe = ex + min(kq, n_rows - 1) * ng;
+    const int8_t* const xl = x.fragment(0) + part * bpc * W4_BODY;
+    const float* const xe = x.exponents(0) + part * bpc * (W4_BODY / G);
+    float total = 0.0f;
     for (int c = 0; c < chunks; ++c) {
-      __syncthreads();                                 // the chunk before is done with
-      for (int u = tid;;) {
-        if (c > 0 || u != tid) x_load(c, u);
-        x_store(u);
-        u += XU * (int)blockDim.x;
-        if (u - tid >= units) break;
-      }
+      __syncthreads();                                 // the chunk (or the sums) before is done with
+      x.fill(c, c == 0, row_of);
       __syncthreads();
       if (idle) continue;
       for (int b = 0; b < bpc; ++b) {
         // the next body (behind the last, and past K: the row's last codes once more)
-        const int kn = min(b + 1 < bpc ? column(c, b + 1) : column(c + 1, 0), p.K);
+        const int kn = b + 1 < bpc ? column(c, b + 1) : column(c + 1, 0);
         W4Groups<G, Z> gn;
-        gn.load(one.w[0], w.row, p.K, kn);
-        const int at = (part * bpc + b) * W4_BODY;
-#pragma unroll
-        for (int l = 0; l < W4_LOADS; ++l) {
-          uint32_t t[4] = {q[l].x, q[l].y, q[l].z, q[l].w};
-          if constexpr (G == 64) swap2(t);
-          if constexpr (G == 32) transpose4(t);
-          constexpr int NG = 128 / G, W = 4 / NG;      // groups of the load, words of a group
-          i32x4_t acc[NG];
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const uint32_t zc = Z ? 0x80808080u - gr.zero_byte(l * NG + g) * 0x01010101u : 0;
-            acc[g] = i32x4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < W; j += W > 1 ? 2 : 1) {
-              int lo[2], hi[2];
-              code_bytes<Z>(t[W * g + j], zc, lo[0], hi[0]);
-              if constexpr (W > 1) {
-                code_bytes<Z>(t[W * g + j + 1], zc, lo[1], hi[1]);
-                const i32x4_t a = *(const i32x4_t*)(xl + at + 128 * l + (G == 128 ? 8 * j : 64 * g));
-                acc[g] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, i32x4_t{lo[0], hi[0], lo[1], hi[1]}, acc[g], 0, 0, 0);
-              } else {
-                const long a = *(const long*)(xl + at + 128 * l + 32 * g);
-                acc[g] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, (long)(uint32_t)lo[0] | ((long)hi[0] << 32), acc[g], 0, 0, 0);
-              }
-            }
-          }
-          q[l] = w.load(0, l, kn);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const float v = fmaf((float)acc[g][0], 65536.0f, (float)((acc[g][1] << 8) + acc[g][2]));
-            total = fmaf(v * gr.scale(l * NG + g), xe[at / G + l * NG + g], total);
-          }
-        }
+        gn.load(mat, w.row, p.K, kn);
+        w4_few_body<G, Z>(q, gr, xl + b * W4_BODY, xe + b * (W4_BODY / G), w, kn, total);
         gr = gn;
       }
     }
-    // the parts' sums, in order
-    if (!idle) red[wv * 64 + lane] = Z ? total : total * 0.0625f;
+    red[wv * 64 + lane] = total;
     __syncthreads();
+    // the parts' sums, in order
     for (int o = tid; o < n_rows * nt * 16; o += blockDim.x) {
-      const int m = o / (nt * 16), c = o - m * (nt * 16), n = t0 * 16 + c;
+      const int m = o / (nt * 16), c = o - m * (nt * 16), n = t0 * 16 + c, t = c >> 4;
       float v[S];
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         v[s] = 0.0f;
-        for (int j = 0; j < p.ks; ++j) v[s] += red[(((c >> 4) * S + s) * p.ks + j) * 64 + m * 16 + (c & 15)];
+        for (int j = 0; j < p.ks; ++j) v[s] += red[((t * S + s) * p.ks + j) * 64 + m * 16 + (c & 15)];
+        if (!Z) v[s] *= 0.0625f;
       }
       if (n < p.N) w4_store<MODE, S>(p, rows, m0 + m, n, v);
     }
+  }
+}
+
+// The down projection of a token whose experts hardly any other token shares: workgroup (x, y) takes tile x of
+// all the k <= 8 routes of token y, a wave a route (and part of K), and writes y itself, which saves P's way
+// through memory and a launch (T 1, d 7168, I 2048, k 8 of 256 experts: 56 -> 49 us; d 2048, I 1408, k 6 of
+// 64: 22 -> 19).
+template <int G, bool Z>
+__global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_token(const W4Args p) {
+  extern __shared__ __attribute__((aligned(16))) int8_t xb[];
+  __shared__ float red[W4_MAXW * 16];
+  const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid >> 6);
+  const int j = wv / p.ks, part = wv - j * p.ks;
+  const int64_t t = blockIdx.y;
+  const int n0 = blockIdx.x * 16;
+  // bodies of a chunk and part; chunks
+  const int bodies = (p.K + W4_BODY - 1) / W4_BODY, bw = W4_BODY * p.ks;
+  const int bpc = min((bodies + p.ks - 1) / p.ks, max(1, p.cap / (w4_few_bytes(G) * p.k * p.ks)));
+  const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck;
+  auto column = [&](int c, int b) { return min(c * ck + (part * bpc + b) * W4_BODY, p.K); };
+  auto row_of = [&](int r) { return t * p.k + r; };
+  const int e = uniform(p.idx[t * p.k + j]) - p.e0;
+  const bool idle = e < 0 || e >= p.El;
+  W4Bytes<G, 2> x(xb, p.x, p.K, p.k, ck);
+  x.load(0, tid, row_of);                              // (rows of routes to other experts hold anything)
+  __builtin_amdgcn_sched_barrier(0);
+  uint4 q[W4_LOADS];
+  W4Groups<G, Z> gr;
+  const W4Tile<1> w(p.w, p.N, p.K, idle ? 0 : e, n0);
+  if (!idle) {
+    gr.load(p.w[0], w.row, p.K, column(0, 0));
+#pragma unroll
+    for (int l = 0; l < W4_LOADS; ++l) q[l] = w.load(0, l, column(0, 0));
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  const int8_t* const xl = x.fragment(j) + part * bpc * W4_BODY;
+  const float* const xe = x.exponents(j) + part * bpc * (W4_BODY / G);
+  float total = 0.0f;
+  for (int c = 0; c < chunks; ++c) {
+    if (c > 0) __syncthreads();
+    x.fill(c, c == 0, row_of);
+    __syncthreads();
+    if (idle) continue;
+    for (int b = 0; b < bpc; ++b) {
+      const int kn = b + 1 < bpc ? column(c, b + 1) : column(c + 1, 0);
+      W4Groups<G, Z> gn;
+      gn.load(p.w[0], w.row, p.K, kn);
+      w4_few_body<G, Z>(q, gr, xl + b * W4_BODY, xe + b * (W4_BODY / G), w, kn, total);
+      gr = gn;
+    }
+  }
+  // the wave's route is row 0 of its MFMA: lanes 0 .. 15 have its columns
+  if (lane < 16) red[wv * 16 + lane] = idle ? 0.0f : Z ? total : total * 0.0625f;
+  __syncthreads();
+  const int n = n0 + tid;
+  if (tid < 16 && n < p.N) {
+    float v = p.y_in ? bf16_to_f32(((const bf16_t*)p.y_in)[t * p.N + n]) : 0.0f;
+    for (int r = 0; r < p.k; ++r) {
+      const int er = p.idx[t * p.k + r] - p.e0;
+      if (er < 0 || er >= p.El) continue;
+      float s = 0.0f;
+      for (int i = 0; i < p.ks; ++i) s += red[(r * p.ks + i) * 16 + tid];
+      v += p.tw[t * p.k + r] * s;
+    }
+    ((bf16_t*)p.out)[t * p.N + n] = f32_to_bf16(v);
   }
 }
 
@@ -506,7 +617,7 @@ __global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
   const int tile = wv / p.ks, part = wv - tile * p.ks, t0 = blockIdx.x * p.tpw;
   const int nt = min(p.tpw, p.tiles - t0);
   const bool idle = tile >= nt;
-  const W4Tile<S> w(p, rows.expert, idle ? 0 : (t0 + tile) * 16);
+  const W4Tile<S> w(p.w, p.N, p.K, rows.expert, idle ? 0 : (t0 + tile) * 16);
   const int64_t m_first = MODE == W4_DENSE ? (int64_t)blockIdx.y * MR : 0;
   const int64_t m_end = MODE == W4_DENSE ? min(rows.count, m_first + MR) : rows.count;
   for (int64_t m0 = m_first; m0 < m_end; m0 += MR) {
@@ -598,7 +709,7 @@ __global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
 #pragma unroll
         for (int l = 0; l < W4_LOADS; ++l) {
           if (l + 1 < W4_LOADS) read(l + 1);
-          w4_step<G, Z, S>(q[l], gr, l, a[l & 1], total);
+          w4_step<G, Z, S, W4_BODY>(q[l], gr, l, a[l & 1], total);
 #pragma unroll
           for (int s = 0; s < S; ++s) q[l][s] = w.load(s, l, kn);
         }
@@ -616,6 +727,58 @@ __global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
     __syncthreads();
     w4_join<MODE, S, PL>(p, rows, red, m0, n_rows, 8, t0, nt);
   }
+}
+
+// The dense product of up to 16 rows with few tiles: a workgroup is one tile in up to 16 parts of K, and every
+// wave loads its own x, whose fragments are 16 bytes a lane, from the caches: with one tile a workgroup LDS would
+// be read once as well. A wave's step is W4_STEP columns; the next step's codes are in flight meanwhile.
+template <int G, bool Z>
+__global__ __launch_bounds__(64 * W4_PARTS) void k_w4_split(const W4Args p) {
+  constexpr int L = W4_STEP / 128;
+  __shared__ float red[W4_PARTS * 256];
+  const int lane = lane_id(), part = uniform(threadIdx.x >> 6), kq = lane >> 4, ln = lane & 15;
+  const int64_t m0 = (int64_t)blockIdx.y * 16;
+  const int n_rows = (int)min((int64_t)16, p.M - m0), steps = (p.K + W4_STEP - 1) / W4_STEP;
+  const int t0 = blockIdx.x, per = (steps + p.ks - 1) / p.ks, last = min(steps, (part + 1) * per);
+  const W4Tile<1> w(p.w, p.N, p.K, 0, t0 * 16);
+  const bf16_t* const x = (const bf16_t*)p.x + (m0 + min(ln, n_rows - 1)) * p.K;   // rows past the last: not looked at
+  struct Codes {
+    uint4 q[L][1];
+    W4Groups<G, Z, W4_STEP> gr[1];
+  };
+  auto load = [&](Codes& t, int i) {                   // past K: the row's last codes once more
+    const int k0 = min(i * W4_STEP, p.K);
+    t.gr[0].load(p.w[0], w.row, p.K, k0);
+#pragma unroll
+    for (int l = 0; l < L; ++l) t.q[l][0] = w.load(0, l, k0);
+  };
+  f32x4_t total[1] = {{0, 0, 0, 0}};
+  Codes now, next;
+  if (part * per < last) load(now, part * per);
+  for (int i = part * per; i < last; ++i) {
+    uint4 v[L][4];
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = i * W4_STEP + 128 * l + (G < 128 ? 32 * j + 8 * kq : 32 * kq + 8 * j);
+        const uint4 u = *(const uint4*)(x + min(k, p.K - 8));
+        v[l][j] = k < p.K ? u : make_uint4(0, 0, 0, 0);
+      }
+    load(next, i + 1);
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      bf16x8_t a[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = order8(v[l][j]);
+      w4_step<G, Z, 1, W4_STEP>(now.q[l], now.gr, l, a, total);
+    }
+    now = next;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) red[part * 256 + (4 * kq + e) * 16 + ln] = total[0][e];
+  __syncthreads();
+  w4_join<W4_DENSE, 1, 1>(p, W4Rows{}, red, m0, n_rows, 0, t0, 1);
 }
 
 // y[t] = y_in[t] + sum of the local experts' P[t k + j], j ascending; 4 columns a thread.
@@ -702,6 +865,20 @@ __global__ __launch_bounds__(256) void k_quantize_int4(const bf16_t* __restrict_
 bool group_ok(int g) { return g == 32 || g == 64 || g == 128; }
 bool al16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
+hipError_t launch_w4_split(W4Args a, int g, int64_t slots, hipStream_t s) {
+  const int steps = (a.K + W4_STEP - 1) / W4_STEP;
+  const int per = (steps + W4_PARTS - 1) / W4_PARTS;
+  a.ks = (steps + per - 1) / per;
+  const dim3 grid((unsigned)a.tiles, (unsigned)slots), block(64 * a.ks);
+  auto go = [&](auto G) {
+    launch_k(a.w[0].zeros ? k_w4_split<G(), true> : k_w4_split<G(), false>, grid, block, 0, s, nullptr, nullptr, a);
+  };
+  if (g == 32) go(std::integral_constant<int, 32>{});
+  else if (g == 64) go(std::integral_constant<int, 64>{});
+  else go(std::integral_constant<int, 128>{});
+  return hipGetLastError();
+}
+
 // most: the rows that an expert (or the product) can have; mean: how many it has on average.
 template <int MODE>
 hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t most, double mean, hipStream_t s) {
@@ -711,6 +888,9 @@ hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t most, double mean, 
   const int bodies = (a.K + W4_BODY - 1) / W4_BODY, mr = few ? 4 : 16 / PL;
   const int xr = (int)std::min<int64_t>(most, mr);
   if (MODE == W4_DENSE) slots = (a.M + mr - 1) / mr;
+  // at most a tile a CU (13 and 5 rows, N 4096, K 7168, groups of 32 with zero points: 20.5 -> 12.2 and 11.1 ->
+  // 9.4 us; 13 rows, N 8192, with two: 21.8 -> 22.4, groups of 128 16.4 -> 19.3)
+  if (MODE == W4_DENSE && !few && a.tiles * slots <= 256) return launch_w4_split(a, g, slots, s);
   // LDS of a body's columns in all rows; the parts of K have to fit, and gate and up tiles come in pairs
   const int bytes = few ? w4_few_bytes(g) * xr : 2 * W4_BODY * PL * xr;
   const int lds_x = few ? W4_LDS_FEW : W4_LDS_ROWS, pair = few ? S : 1;
@@ -735,6 +915,23 @@ hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t most, double mean, 
   if (g == 32) pick(std::integral_constant<int, 32>{});
   else if (g == 64) pick(std::integral_constant<int, 64>{});
   else pick(std::integral_constant<int, 128>{});
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_token(W4Args a, int g, int64_t T, hipStream_t s) {
+  a.tiles = (a.N + 15) / 16;
+  const int bodies = (a.K + W4_BODY - 1) / W4_BODY, bytes = w4_few_bytes(g) * a.k;
+  a.ks = std::min(std::min(W4_MAXW / a.k, bodies), std::max(1, W4_LDS_FEW / bytes));
+  a.ks = (bodies + (bodies + a.ks - 1) / a.ks - 1) / ((bodies + a.ks - 1) / a.ks);
+  a.cap = bytes * a.ks * std::min((bodies + a.ks - 1) / a.ks, std::max(1, W4_LDS_FEW / (bytes * a.ks)));
+  const dim3 grid((unsigned)a.tiles, (unsigned)T), block(64 * a.k * a.ks);
+  auto go = [&](auto G) {
+    launch_k(a.w[0].zeros ? k_w4_token<G(), true> : k_w4_token<G(), false>, grid, block, (uint32_t)(a.cap + 48 * a.k), s,
+             nullptr, nullptr, a);
+  };
+  if (g == 32) go(std::integral_constant<int, 32>{});
+  else if (g == 64) go(std::integral_constant<int, 64>{});
+  else go(std::integral_constant<int, 128>{});
   return hipGetLastError();
 }
 
@@ -853,7 +1050,15 @@ int mok_moe_w4_forward(const mok_moe_w4_args* args, void* stream) {
   w.x = a.x; w.out = ws + p.H; w.N = a.I; w.K = a.d;
   if (launch_w4<W4_UP>(w, a.group, slots, a.T, mean, s) != hipSuccess) return MOK_EHIP;
   w.w[0] = {a.down_codes, (const uint16_t*)a.down_scales, a.down_zeros};
-  w.x = ws + p.H; w.out = ws + p.P; w.N = a.d; w.K = a.I;
+  w.x = ws + p.H; w.N = a.d; w.K = a.I;
+  // few routes an expert: nearly all of its tokens' products would be one row (mean 0.25: one in eight
+  // experts that are picked serves two); and all experts here, or waves would be idle
+  if (!p.plan && a.k <= W4_MAXW && a.E_l == a.E && mean <= 0.25) {
+    w.out = a.y;
+    w.y_in = a.y_in;
+    return launch_w4_token(w, a.group, a.T, s) == hipSuccess ? MOK_OK : MOK_EHIP;
+  }
+  w.out = ws + p.P;
   if (launch_w4<W4_DOWN>(w, a.group, slots, a.T, mean, s) != hipSuccess) return MOK_EHIP;
   launch_k(k_w4_combine, dim3((unsigned)blocks), dim3(256), 0, s, nullptr, nullptr,
            (const float*)(ws + p.P), a.topk_idx, (const uint2*)a.y_in, a.T, a.k, a.e0, a.E_l, a.d / 4,
