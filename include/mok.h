@@ -490,7 +490,8 @@ int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype
  * weights; +inf logits make a softmax row NaN.
  *   logits [T, E] float32, topk_idx [T, k] int32, topk_w [T, k] float32
  * Requires 1 <= k <= E <= 1024, k <= 64, T k < 2^31, E % n_groups == 0, 1 <= topk_groups <= n_groups,
- * k <= topk_groups E / n_groups, a finite scale.
+ * k <= topk_groups E / n_groups, a finite scale; more than 2^25 tokens are MOK_EUNSUPPORTED, here and in
+ * the gradient.
  * mok_route_scored: the router projection of mok_route (the same logits, bit for bit), then the
  * choice. */
 #define MOK_SCORE_SOFTMAX 0
@@ -521,8 +522,9 @@ int mok_topk_scored_backward(const float* logits, const int32_t* topk_idx, const
  * gate: [d], one for all tokens, or, gate_per_row, [rows, d]. y, residual, gate, w_post [d], w_pre
  * [d], h, n: float32 or bf16 (io_dtype); rstd_y, rstd_h [rows] float32, for the backward (NULL: not
  * wanted). n NULL with w_pre: rstd_h alone. h may be y or residual, n may be y or residual where h is
- * not the same one; other overlaps are not allowed. Statistics in float64. d, rows, eps and the
- * read-once forms as mok_rmsnorm; rows past 2^21 take the slower form. alpha, beta finite.
+ * not the same one; other overlaps are not allowed. Statistics in float64. d, rows and eps as
+ * mok_rmsnorm. Rows of d <= 16384 (backward: 8192) are read once, whatever their address (whole 16-byte
+ * pieces at 16-byte addresses are fastest); more than 2^21 of them take the slower form. alpha, beta finite.
  *
  * Backward, from dh (what reaches h from the residual stream) and dn (either may be NULL: none):
  *   dt = dh + rstd_h (g - nh mean(g nh)),  g = dn w_pre, nh = h rstd_h;    dw_pre[i] = sum_t dn nh
@@ -551,7 +553,8 @@ int mok_gated_norm_backward(const void* dh, const void* dn, const void* y, const
  * of 32, 64 or 128 neighbours along K:
  *   W[n,k] = (q[n,k] - z[n, k / group]) s[n, k / group]
  *   codes [N, K / 2]: two a byte, element 2i in the low nibble of byte i
- *   scales [N, K / group] bf16;  zeros [N, K / group] uint8, NULL: 8 throughout
+ *   scales [N, K / group] bf16;  zeros [N, K / group] uint8, 0 .. 15 (larger ones: unspecified
+ *   results); NULL: 8 throughout
  *
  * mok_quantize_int4: rows of bf16 (16-byte aligned), in float32 arithmetic, each operation rounded to
  * nearest even. Without zeros: s = bf16(max |w| / 7), q = clamp(rint(w / s) + 8, 0, 15). With zeros,
@@ -562,8 +565,10 @@ int mok_quantize_int4(const void* src_bf16, int64_t rows, int32_t K, int32_t gro
                       void* scales, uint8_t* zeros, void* stream);
 
 /* C[m,n] = sum_k x[m,k] W[n,k]: x [M, K] bf16, C [M, N] bf16 or float32 (out_dtype), rounded once.
- * Made for few rows: the weight is streamed once for every 16. The products x (q - z) are exact,
- * their sums and the scaling float32. An infinite or NaN x[m,k] makes row m NaN.
+ * Made for few rows: the weight is streamed once for every 16. Sums and the scaling are float32. x enters as
+ * it is for more than 4 rows. Up to 4 take integers: a row's group of x has one exponent and 22 bits, so that
+ * values within 2^-14 of its largest are exact and smaller ones off by at most 2^-22 of the largest; a group's
+ * sum is exact then. An infinite or NaN x[m,k] makes row m NaN.
  * K % group == 0, K <= 2^22, M <= 2^20, N <= 2^26 (MOK_EUNSUPPORTED past the last two, below 2^31).
  * x and codes start on 16 bytes. Bit-identical reruns; no workspace. */
 int mok_w4_gemm(const void* x, const uint8_t* codes, const void* scales, const uint8_t* zeros,
@@ -576,8 +581,10 @@ int mok_w4_gemm(const void* x, const uint8_t* codes, const void* scales, const u
  *   y[t] = y_in[t] + sum_{j: local} w[t,j] W_down[e] (silu(W_gate[e] x[t]) * (W_up[e] x[t])),
  *   e = topk_idx[t,j], local: e0 <= e < e0 + E_l, j ascending
  * A share of the experts (E_l < E) gives its part of the sum. y_in: the shared experts' output or the
- * residual stream (NULL: none). The hidden values stay float32 between the products (the down
- * projection reads 16 bits of their significand), sums are float32, y is rounded once. Every route is
+ * residual stream (NULL: none). Where n_routes = T k gives an expert of E at most 2 on
+ * average, or T <= 4, the products are mok_w4_gemm's of up to 4 rows, x and the hidden values as such
+ * integers; else x enters as it is and the hidden values with 16 bits of their significand. Between the
+ * products they are float32, sums are float32, y is rounded once. Every route is
  * computed; ids outside the local experts are skipped, an expert named twice counts twice. */
 typedef struct mok_moe_w4_args {
   int64_t T;               /* tokens                                                        */

@@ -11,6 +11,11 @@
 // neighbours of that order lie closer than the bound allows, c of those up to the next clear step (16 at
 // most) is formed in float64 and they are ordered by it; rows with groups that close, with NaN, with scores
 // at float64's ends or with nothing left are done in float64 from the start by their wave (row_exact).
+//
+// Bound by the vector unit for many rows (T 65,536, E 256, 8 groups: 44 us against 13 for reading the logits;
+// a row's sort, rounds and float64 weights; the whole row in float64 took 537) and by latency for few (one
+// row: 7 us with its launch). 16 lanes a row and not 64: four rows share the rounds' instructions. The gradient
+// is a stream of dlogits (30 us there against 27 for its bytes).
 #include <algorithm>
 
 #include "device_common.h"
@@ -22,6 +27,7 @@ namespace {
 
 constexpr int RS_NT = 256, RS_LPR = 16;          // lanes of a row: one DPP row
 constexpr int RS_MAXE = 1024, RS_MAXK = 64;
+constexpr int64_t RS_MAXT = 1 << 25;             // a launch's 2^32 threads, 64 a row
 
 struct RsArgs {
   const float* logits;
@@ -607,7 +613,7 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored_bwd_full(const RsBwd a) {
 
 int rs_check(int64_t T, int32_t E, int32_t k, int32_t score) {
   if (T < 0 || E < 1 || E > RS_MAXE || k < 1 || k > E || k > RS_MAXK) return MOK_EINVAL;
-  if (T * (int64_t)k >= (int64_t)1 << 31) return MOK_EINVAL;
+  if (T >= (int64_t)1 << 31 || T * (int64_t)k >= (int64_t)1 << 31) return MOK_EINVAL;
   return score == MOK_SCORE_SOFTMAX || score == MOK_SCORE_SIGMOID ? MOK_OK : MOK_EINVAL;
 }
 int rs_check_groups(int32_t E, int32_t k, int32_t G, int32_t Gk, int32_t top, float scale) {
@@ -645,6 +651,7 @@ int mok_topk_scored(const float* logits, int64_t T, int32_t E, int32_t k, int32_
   if (st != MOK_OK) return st;
   if (T == 0) return MOK_OK;
   if (!logits || !topk_idx || !topk_w) return MOK_EINVAL;
+  if (T > RS_MAXT) return MOK_EUNSUPPORTED;
   const RsArgs a = {logits, bias, topk_idx, topk_w, T, E, k, n_groups, topk_groups, group_top,
                     score == MOK_SCORE_SIGMOID, renorm != 0, scale};
   return launch_scored(a, (hipStream_t)stream) == hipSuccess ? MOK_OK : MOK_EHIP;
@@ -660,6 +667,7 @@ int mok_route_scored(const void* x, const void* w_router, int64_t T, int32_t d, 
   if (d < 1 || (io_dtype != MOK_FP32 && io_dtype != MOK_BF16)) return MOK_EINVAL;
   if (T == 0) return MOK_OK;
   if (!x || !w_router || !logits || !topk_idx || !topk_w) return MOK_EINVAL;
+  if (T > RS_MAXT) return MOK_EUNSUPPORTED;
   const hipError_t e = launch_router_logits(x, w_router, T, d, E, io_dtype == MOK_BF16, logits,
                                             (hipStream_t)stream);
   if (e != hipSuccess) return MOK_EHIP;
@@ -676,6 +684,7 @@ int mok_topk_scored_backward(const float* logits, const int32_t* topk_idx, const
   if (!(fabsf(scale) < INFINITY)) return MOK_EINVAL;
   if (T == 0) return MOK_OK;
   if (!logits || !topk_idx || !dtopk_w || !dlogits) return MOK_EINVAL;
+  if (T > RS_MAXT) return MOK_EUNSUPPORTED;
   RsBwd a = {logits, topk_idx, dtopk_w, dlogits_in, dlogits, T, E, k, score == MOK_SCORE_SIGMOID,
              renorm != 0, 0, scale};
   // rows of a workgroup: at most 16 KB of their place in LDS, 64, and what leaves 1024 workgroups

@@ -202,3 +202,15 @@ def test_workspace_queries(mok):
         with pytest.raises(mok.MokError) as e:
             call()
         assert e.value.status == EINVAL
+
+
+def test_more_tokens_than_a_launch(lib):
+    """Past 2^25 tokens the choice and its gradient are refused, not launched."""
+    T = (1 << 25) + 1
+    rule = dict(score=1, bias=None, G=4, Gk=2, top=2, renorm=1, scale=1.0)
+    refuse(lib.mok_topk_scored, dict(logits=16, T=T, E=16, k=1, **rule, idx=16, w=16), EUNSUPPORTED)
+    refuse(lib.mok_route_scored, dict(x=16, wr=16, T=T, d=64, E=16, k=1, io=1, **rule, logits=16, idx=16, w=16),
+           EUNSUPPORTED)
+    refuse(lib.mok_topk_scored_backward, dict(logits=16, idx=16, dw=16, din=None, T=T, E=16, k=1, score=0, renorm=0,
+                                              scale=1.0, dl=16), EUNSUPPORTED)
+    refuse(lib.mok_topk_scored, dict(logits=16, T=1 << 62, E=16, k=4, **rule, idx=16, w=16), EINVAL)
