@@ -7,7 +7,9 @@ loudly (ImportError) if it has not been built: there is no fallback of any kind.
 Entry points carry the C names: mok_route, mok_topk, mok_dispatch_plan,
 mok_dispatch_plan_workspace_bytes, mok_moe_workspace_bytes, mok_moe_forward,
 mok_quantize_mxfp8, mok_quantize_mxfp8_f32, mok_quantize_mxfp4_f32, mok_get_device_error,
-mok_status_string, mok_version.
+mok_status_string, mok_version. Around the layer: mok_topk_scored, mok_route_scored and
+mok_topk_scored_backward (routing by scores), mok_gated_norm and mok_gated_norm_backward, mok_quantize_int4,
+mok_w4_gemm and MoeW4Layer (mok_moe_w4_forward: the experts on 4-bit weights).
 """
 from __future__ import annotations
 

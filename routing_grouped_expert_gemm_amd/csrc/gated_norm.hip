@@ -17,7 +17,8 @@
 // shares a second launch adds in a fixed order: no atomics. Rows that are not whole 16-byte pieces, or lie
 // at other addresses, take the same kernels with loads and stores of single values' alignment and a last
 // piece value by value (float32, T 1001, d 1111 both ways: one value a thread and step, three passes over
-// memory and four launches, 38 us; so 27 us).
+// memory and four launches, 38 us; so 27 us). bf16, T 8192: forward d 7168 102 us for 470 MB,
+// both directions d 2048 90 us for 436 MB, 4.6 and 4.9 TB/s.
 #include <algorithm>
 
 #include "device_common.h"
