@@ -4,15 +4,16 @@
 //   W[n,k] = (q[n,k] - z[n,k / g]) s[n,k / g],  q 0 .. 15, two codes a byte, 2i in the low nibble
 //   C[m,n] = sum_groups s (sum_{k in group} x[m,k] (q - z))
 //
-// Bound by streaming the codes once, and close behind by the vector unit, which has to take every code
-// apart. A weight's 16 rows and 128 columns are one 16-byte load a lane (lane (kq, n): row n, 32 codes).
+// Bound by streaming the codes once, and by the start of each workgroup; the vector unit, which has to take
+// every code apart, is busy for a third to a half of the time. A weight's 16 rows and 128 columns are one 16-byte load a lane (lane (kq, n): row n, 32 codes).
 // A wave takes one tile (16 weight rows; of the MoE's first product gate and up tiles in turn) and one of
 // KS parts of K and streams it in bodies of 512 columns: the loads of the next body are in flight while
 // this one's are used, each issued as its register becomes free. A workgroup is 8 waves: 8 / KS tiles by
 // KS parts, whose sums meet in LDS in a fixed order. (Streamed alone, the codes of T 1, d 7168, I 2048, k 8
 // come at 5.3 TB/s with one wave a tile and 32 KB a CU in flight, 4.7 with two and 64 KB.) T 1, d 7168, I 2048,
 // k 8 of 256 experts: 49 us for 182 MB, where each of the two launches starts up for 5 to 7 us (x to LDS, the
-// first codes); 48 tokens there on 32 of the experts with zero points: 186 us for 602 MB.
+// first codes); 48 tokens there on 32 of the experts with zero points: 186 us for 602 MB. (Fewer
+// operations for the zero points, -z times the sums of x's bytes as the accumulators' start, changed nothing.)
 //
 //  k_w4_few   up to 4 rows of x a pass: integers. x is cut into 22-bit integers with one exponent for a
 //    row's group (what is lost is below 2^-22 of the group's largest value; bf16 values within 2^-14 of it
