@@ -12,7 +12,8 @@
 // KS parts, whose sums meet in LDS in a fixed order. (Streamed alone, the codes of T 1, d 7168, I 2048, k 8
 // come at 5.3 TB/s with one wave a tile and 32 KB a CU in flight, 4.7 with two and 64 KB.) T 1, d 7168, I 2048,
 // k 8 of 256 experts: 49 us for 182 MB, where each of the two launches starts up for 5 to 7 us (x to LDS, the
-// first codes); 48 tokens there on 32 of the experts with zero points: 186 us for 602 MB. (Fewer
+// first codes); 48 tokens there on 32 of the experts with zero points: 186 to 204 us, by
+// the routing, for 602 MB. (Fewer
 // operations for the zero points, -z times the sums of x's bytes as the accumulators' start, changed nothing.)
 //
 //  k_w4_few   up to 4 rows of x a pass: integers. x is cut into 22-bit integers with one exponent for a
