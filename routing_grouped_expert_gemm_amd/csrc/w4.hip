@@ -37,16 +37,14 @@
 #include "device_common.h"
 #include "launch.h"
 #include "mok.h"
+#include "w4_shape.h"
 
 namespace mok {
 namespace {
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
-constexpr int W4_BODY = 512;         // columns of a wave's step
 constexpr int W4_LOADS = W4_BODY / 128;
-constexpr int W4_MAXW = 8;           // waves of a workgroup
-constexpr int W4_LDS_FEW = 52 * 1024, W4_LDS_ROWS = 72 * 1024;   // for x: two workgroups a CU
 constexpr int W4_STEP = 256, W4_PARTS = 16;   // k_w4_split: columns of a wave's step, most parts of K
 constexpr int W4_SCAN = 1024;        // routes up to which a workgroup finds its rows by itself
 enum { W4_DENSE = 0, W4_UP = 1, W4_DOWN = 2 };
@@ -326,9 +324,6 @@ struct W4Tile {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-// LDS of a body's columns of one row of x: three bytes each, and a float32 exponent a group.
-MOK_HOSTDEV int w4_few_bytes(int g) { return 3 * W4_BODY + W4_BODY / g * 4; }
-
 // 8 codes of a word less their zero point as bytes, the even ones, then the odd ones; without zero points
 // (z the constant 8) times 16.
 template <bool Z>
@@ -494,7 +489,7 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_few(const W4Args p) {
     const int n_rows = (int)min((int64_t)MR, m_end - m0);
     // bodies of a chunk and part; chunks
     const int bodies = (p.K + W4_BODY - 1) / W4_BODY, bw = W4_BODY * p.ks;
-    const int bpc = min((bodies + p.ks - 1) / p.ks, max(1, p.cap / (w4_few_bytes(G) * n_rows * p.ks)));
+    const int bpc = w4_bodies(bodies, p.ks, p.cap, w4_body_bytes(true, G, 1), n_rows);
     const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck;
     auto column = [&](int c, int b) { return min(c * ck + (part * bpc + b) * W4_BODY, p.K); };
     auto row_of = [&](int r) { return w4_x_row<MODE>(p, rows, m0 + r); };
@@ -557,7 +552,7 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_token(const W4Args p) {
   const int n0 = blockIdx.x * 16;
   // bodies of a chunk and part; chunks
   const int bodies = (p.K + W4_BODY - 1) / W4_BODY, bw = W4_BODY * p.ks;
-  const int bpc = min((bodies + p.ks - 1) / p.ks, max(1, p.cap / (w4_few_bytes(G) * p.k * p.ks)));
+  const int bpc = w4_bodies(bodies, p.ks, p.cap, w4_body_bytes(true, G, 1), p.k);
   const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck;
   auto column = [&](int c, int b) { return min(c * ck + (part * bpc + b) * W4_BODY, p.K); };
   auto row_of = [&](int r) { return t * p.k + r; };
@@ -625,10 +620,10 @@ __global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
   const int64_t m_first = MODE == W4_DENSE ? (int64_t)blockIdx.y * MR : 0;
   const int64_t m_end = MODE == W4_DENSE ? min(rows.count, m_first + MR) : rows.count;
   for (int64_t m0 = m_first; m0 < m_end; m0 += MR) {
-    const int n_rows = (int)min((int64_t)MR, m_end - m0), n_xr = n_rows * PL;
+    const int n_rows = (int)min((int64_t)MR, m_end - m0);
     // bodies of a chunk and part; chunks
     const int bodies = (p.K + W4_BODY - 1) / W4_BODY, bw = W4_BODY * p.ks;
-    const int bpc = min((bodies + p.ks - 1) / p.ks, max(1, p.cap / (2 * bw * n_xr)));
+    const int bpc = w4_bodies(bodies, p.ks, p.cap, w4_body_bytes(false, G, PL), n_rows);
     const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck, ld = ck + 8;
     auto column = [&](int c, int b) { return c * ck + (part * bpc + b) * W4_BODY; };
     // x's columns c ck .. to LDS, 8 at a time, in unpack8's order: XU loads of a thread in flight
@@ -883,33 +878,25 @@ hipError_t launch_w4_split(W4Args a, int g, int64_t slots, hipStream_t s) {
   return hipGetLastError();
 }
 
-// most: the rows that an expert (or the product) can have; mean: how many it has on average.
+// tokens: the rows of an expert (or the product) whose tokens name it once; most: those that it can have; mean:
+// how many it has on average.
 template <int MODE>
-hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t most, double mean, hipStream_t s) {
+hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t tokens, int64_t most, double mean, hipStream_t s) {
   constexpr int S = MODE == W4_UP ? 2 : 1, PL = MODE == W4_DOWN ? 2 : 1;
-  const bool few = most <= 4 || mean <= 2.0;      // one in twenty experts of 2 rows has a second pass
+  const bool few = tokens <= 4 || mean <= 2.0;    // one in twenty experts of 2 rows has a second pass
   a.tiles = (a.N + 15) / 16;
-  const int bodies = (a.K + W4_BODY - 1) / W4_BODY, mr = few ? 4 : 16 / PL;
-  const int xr = (int)std::min<int64_t>(most, mr);
+  const int mr = few ? 4 : 16 / PL;
   if (MODE == W4_DENSE) slots = (a.M + mr - 1) / mr;
   // at most a tile a CU (13 and 5 rows, N 4096, K 7168, groups of 32 with zero points: 20.5 -> 12.2 and 11.1 ->
   // 9.4 us; 13 rows, N 8192, with two: 21.8 -> 22.4, groups of 128 16.4 -> 19.3)
   if (MODE == W4_DENSE && !few && a.tiles * slots <= 256) return launch_w4_split(a, g, slots, s);
-  // LDS of a body's columns in all rows; the parts of K have to fit, and gate and up tiles come in pairs
-  const int bytes = few ? w4_few_bytes(g) * xr : 2 * W4_BODY * PL * xr;
-  const int lds_x = few ? W4_LDS_FEW : W4_LDS_ROWS, pair = few ? S : 1;
-  const int parts = std::min(std::min(W4_MAXW / pair, bodies), lds_x / bytes);
-  // as many parts of K as give every SIMD two waves
-  const int64_t waves = std::max<int64_t>(1, (int64_t)a.tiles * pair * slots);
-  a.ks = (int)std::min<int64_t>(parts, (2048 + waves - 1) / waves);
-  a.ks = (bodies + (bodies + a.ks - 1) / a.ks - 1) / ((bodies + a.ks - 1) / a.ks);
-  a.tpw = W4_MAXW / a.ks / pair * pair;
-  a.cap = bytes * a.ks * std::min((bodies + a.ks - 1) / a.ks, std::max(1, lds_x / (bytes * a.ks)));
-  // 16 bytes lie between rows (of each byte's plane)
-  const size_t lds = std::max((size_t)a.cap + 48 * xr, few ? (size_t)0 : (size_t)a.tpw * a.ks * S * 1024);
+  const int pair = few ? S : 1;                   // gate and up tiles come in pairs of waves
+  const W4Shape f = w4_shape(few, g, PL, a.K, (int64_t)a.tiles * pair * slots, pair, few ? 0 : S * 1024,
+                             (int)std::min<int64_t>(tokens, mr), (int)std::min<int64_t>(most, mr));
+  a.ks = f.ks; a.tpw = f.tpw; a.cap = f.cap;
   const dim3 grid((unsigned)((a.tiles * pair + a.tpw - 1) / a.tpw), (unsigned)slots), block(64 * a.tpw * a.ks);
   auto go = [&](auto G, auto Z) {
-    launch_k(few ? k_w4_few<G(), Z(), MODE> : k_w4_rows<G(), Z(), MODE>, grid, block, (uint32_t)lds, s, nullptr,
+    launch_k(few ? k_w4_few<G(), Z(), MODE> : k_w4_rows<G(), Z(), MODE>, grid, block, (uint32_t)f.lds, s, nullptr,
              nullptr, a);
   };
   auto pick = [&](auto G) {
@@ -924,14 +911,12 @@ hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t most, double mean, 
 
 hipError_t launch_w4_token(W4Args a, int g, int64_t T, hipStream_t s) {
   a.tiles = (a.N + 15) / 16;
-  const int bodies = (a.K + W4_BODY - 1) / W4_BODY, bytes = w4_few_bytes(g) * a.k;
-  a.ks = std::min(std::min(W4_MAXW / a.k, bodies), std::max(1, W4_LDS_FEW / bytes));
-  a.ks = (bodies + (bodies + a.ks - 1) / a.ks - 1) / ((bodies + a.ks - 1) / a.ks);
-  a.cap = bytes * a.ks * std::min((bodies + a.ks - 1) / a.ks, std::max(1, W4_LDS_FEW / (bytes * a.ks)));
+  const W4Shape f = w4_token_shape(g, a.K, a.k);
+  a.ks = f.ks; a.cap = f.cap;
   const dim3 grid((unsigned)a.tiles, (unsigned)T), block(64 * a.k * a.ks);
   auto go = [&](auto G) {
-    launch_k(a.w[0].zeros ? k_w4_token<G(), true> : k_w4_token<G(), false>, grid, block, (uint32_t)(a.cap + 48 * a.k), s,
-             nullptr, nullptr, a);
+    launch_k(a.w[0].zeros ? k_w4_token<G(), true> : k_w4_token<G(), false>, grid, block, (uint32_t)f.lds, s, nullptr,
+             nullptr, a);
   };
   if (g == 32) go(std::integral_constant<int, 32>{});
   else if (g == 64) go(std::integral_constant<int, 64>{});
@@ -1007,7 +992,7 @@ int mok_w4_gemm(const void* x, const uint8_t* codes, const void* scales, const u
   a.w[0] = {codes, (const uint16_t*)scales, zeros};
   a.x = x; a.out = c; a.M = M; a.N = (int)N; a.K = K; a.out_f32 = out_dtype == MOK_FP32;
   if (M > 1 << 20 || N > 1 << 26) return MOK_EUNSUPPORTED;
-  return launch_w4<W4_DENSE>(a, group, 0, M, (double)M, (hipStream_t)stream) == hipSuccess ? MOK_OK : MOK_EHIP;
+  return launch_w4<W4_DENSE>(a, group, 0, M, M, (double)M, (hipStream_t)stream) == hipSuccess ? MOK_OK : MOK_EHIP;
 }
 
 int mok_moe_w4_workspace_bytes(const mok_moe_w4_args* args, size_t* bytes) {
@@ -1052,7 +1037,7 @@ int mok_moe_w4_forward(const mok_moe_w4_args* args, void* stream) {
   w.w[0] = {a.gate_codes, (const uint16_t*)a.gate_scales, a.gate_zeros};
   w.w[1] = {a.up_codes, (const uint16_t*)a.up_scales, a.up_zeros};
   w.x = a.x; w.out = ws + p.H; w.N = a.I; w.K = a.d;
-  if (launch_w4<W4_UP>(w, a.group, slots, a.T, mean, s) != hipSuccess) return MOK_EHIP;
+  if (launch_w4<W4_UP>(w, a.group, slots, a.T, n, mean, s) != hipSuccess) return MOK_EHIP;
   w.w[0] = {a.down_codes, (const uint16_t*)a.down_scales, a.down_zeros};
   w.x = ws + p.H; w.N = a.d; w.K = a.I;
   // few routes an expert: nearly all of its tokens' products would be one row (mean 0.25: one in eight
@@ -1063,7 +1048,7 @@ int mok_moe_w4_forward(const mok_moe_w4_args* args, void* stream) {
     return launch_w4_token(w, a.group, a.T, s) == hipSuccess ? MOK_OK : MOK_EHIP;
   }
   w.out = ws + p.P;
-  if (launch_w4<W4_DOWN>(w, a.group, slots, a.T, mean, s) != hipSuccess) return MOK_EHIP;
+  if (launch_w4<W4_DOWN>(w, a.group, slots, a.T, n, mean, s) != hipSuccess) return MOK_EHIP;
   launch_k(k_w4_combine, dim3((unsigned)blocks), dim3(256), 0, s, nullptr, nullptr,
            (const float*)(ws + p.P), a.topk_idx, (const uint2*)a.y_in, a.T, a.k, a.e0, a.E_l, a.d / 4,
            (uint2*)a.y);
