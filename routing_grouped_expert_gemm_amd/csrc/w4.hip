@@ -951,7 +951,7 @@ MoeW4Plan moe_w4_plan(const mok_moe_w4_args& a) {
 }
 
 int moe_w4_check(const mok_moe_w4_args* a) {
-  if (!a || a->T < 0 || a->d < 1 || a->I < 1 || !group_ok(a->group)) return MOK_EINVAL;
+  if (!a || a->T < 0 || a->T >= (int64_t)1 << 31 || a->d < 1 || a->I < 1 || !group_ok(a->group)) return MOK_EINVAL;
   if (a->d % a->group || a->I % a->group || a->d > (1 << 22) || a->I > (1 << 22)) return MOK_EINVAL;
   if (a->E < 1 || a->k < 1 || a->k > a->E || a->k > 64 || a->e0 < 0 || a->E_l < 1 || a->E_l > 1024 ||
       a->E_l > a->E - a->e0)
@@ -970,6 +970,7 @@ int mok_quantize_int4(const void* src_bf16, int64_t rows, int32_t K, int32_t gro
                       void* scales, uint8_t* zeros, void* stream) {
   if (rows < 0 || K < 1 || !group_ok(group) || K % group) return MOK_EINVAL;
   if (rows == 0) return MOK_OK;
+  if (rows >= (int64_t)1 << 32) return MOK_EUNSUPPORTED;
   if (!src_bf16 || !codes || !scales || !al16(src_bf16) || (uintptr_t)codes % 4) return MOK_EINVAL;
   const int64_t groups = rows * (K / group), blocks = (groups + 255) / 256;
   if (blocks * 256 >= (int64_t)1 << 32) return MOK_EUNSUPPORTED;
