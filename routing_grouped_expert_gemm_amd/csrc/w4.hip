@@ -325,7 +325,7 @@ struct W4Tile {
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 // 8 codes of a word less their zero point as bytes, the even ones, then the odd ones; without zero points
-// (z the constant 8) times 16.
+// (z the constant 8) times 16, which x's exponents take off.
 template <bool Z>
 MOK_DEV void code_bytes(uint32_t w, uint32_t zc, int& even, int& odd) {
   if constexpr (Z) {                                   // 0x80 + q - z carries into no other byte
@@ -340,9 +340,10 @@ MOK_DEV void code_bytes(uint32_t w, uint32_t zc, int& even, int& odd) {
 
 // x's rows in LDS, as bytes: [rows][3][ck + 16], then the groups' exponents [rows][ck / G]. XF: 16 bytes that
 // 8 values take (bf16: 1, float32: 2).
-template <int G, int XF>
+template <int G, bool Z, int XF>
 struct W4Bytes {
   static constexpr int XU = 2;         // units of 8 values that a thread has in flight
+  static constexpr int SHIFT = (Z ? 148 : 152) - 8;    // of an exponent: the integers' place, 16, the sums' 256
   int8_t* xb;
   const void* x;
   int K, n_rows, ck, ld, ng, cw, units;
@@ -393,7 +394,7 @@ struct W4Bytes {
       for (int m = 1; m < G / 8; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, kWave));
       const int e = max((int)(top >> 23), 1);
       if (u % (G / 8) == 0)
-        ex[r * ng + o / G] = e == 255 ? NAN : __builtin_amdgcn_ldexpf(1.0f, e - 148);
+        ex[r * ng + o / G] = e == 255 ? NAN : __builtin_amdgcn_ldexpf(1.0f, e - SHIFT);
       uint32_t d[3][2] = {};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {                  // |v| < 2^22; bytes from the least, rounded to nearest
@@ -427,8 +428,9 @@ struct W4Bytes {
   MOK_DEV const float* exponents(int first) const { return ex + min(first + (lane_id() >> 4), n_rows - 1) * ng; }
 };
 
-// total += a body's products (for zero-point-less codes 16 times); xl, xe: x's place at its first column. The
-// registers q take the codes of the body at column kn of tile w as they become free.
+// total += a body's products; xl, xe: x's place at its first column. The registers q take the codes of the body at
+// column kn of tile w as they become free. A group's sum times its exponent is exact (short of float32's largest
+// value), so that a large scale of small values, or a small one, loses nothing.
 template <int G, bool Z>
 MOK_DEV void w4_few_body(uint4 (&q)[W4_LOADS], const W4Groups<G, Z>& gr, const int8_t* xl, const float* xe,
                          const W4Tile<1>& w, int kn, float& total) {
@@ -460,8 +462,8 @@ MOK_DEV void w4_few_body(uint4 (&q)[W4_LOADS], const W4Groups<G, Z>& gr, const i
     q[l] = w.load(0, l, kn);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const float v = fmaf((float)acc[g][0], 65536.0f, (float)((acc[g][1] << 8) + acc[g][2]));
-      total = fmaf(v * gr.scale(l * NG + g), xe[l * NG + g], total);
+      const float v = fmaf((float)((acc[g][1] << 8) + acc[g][2]), 1.0f / 256, (float)acc[g][0] * 256.0f);
+      total = fmaf(v * xe[l * NG + g], gr.scale(l * NG + g), total);
     }
   }
 }
@@ -493,7 +495,7 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_few(const W4Args p) {
     const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck;
     auto column = [&](int c, int b) { return min(c * ck + (part * bpc + b) * W4_BODY, p.K); };
     auto row_of = [&](int r) { return w4_x_row<MODE>(p, rows, m0 + r); };
-    W4Bytes<G, MODE == W4_DOWN ? 2 : 1> x(xb, p.x, p.K, n_rows, ck);
+    W4Bytes<G, Z, MODE == W4_DOWN ? 2 : 1> x(xb, p.x, p.K, n_rows, ck);
     uint4 q[W4_LOADS];
     W4Groups<G, Z> gr;
     x.load(0, tid, row_of);                            // x first: waiting for it must not wait for the codes
@@ -531,7 +533,6 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_few(const W4Args p) {
       for (int s = 0; s < S; ++s) {
         v[s] = 0.0f;
         for (int j = 0; j < p.ks; ++j) v[s] += red[((t * S + s) * p.ks + j) * 64 + m * 16 + (c & 15)];
-        if (!Z) v[s] *= 0.0625f;
       }
       if (n < p.N) w4_store<MODE, S>(p, rows, m0 + m, n, v);
     }
@@ -558,7 +559,7 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_token(const W4Args p) {
   auto row_of = [&](int r) { return t * p.k + r; };
   const int e = uniform(p.idx[t * p.k + j]) - p.e0;
   const bool idle = e < 0 || e >= p.El;
-  W4Bytes<G, 2> x(xb, p.x, p.K, p.k, ck);
+  W4Bytes<G, Z, 2> x(xb, p.x, p.K, p.k, ck);
   x.load(0, tid, row_of);                              // (rows of routes to other experts hold anything)
   __builtin_amdgcn_sched_barrier(0);
   uint4 q[W4_LOADS];
@@ -587,7 +588,7 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_token(const W4Args p) {
     }
   }
   // the wave's route is row 0 of its MFMA: lanes 0 .. 15 have its columns
-  if (lane < 16) red[wv * 16 + lane] = idle ? 0.0f : Z ? total : total * 0.0625f;
+  if (lane < 16) red[wv * 16 + lane] = idle ? 0.0f : total;
   __syncthreads();
   const int n = n0 + tid;
   if (tid < 16 && n < p.N) {
