@@ -566,9 +566,9 @@ int mok_quantize_int4(const void* src_bf16, int64_t rows, int32_t K, int32_t gro
 
 /* C[m,n] = sum_k x[m,k] W[n,k]: x [M, K] bf16, C [M, N] bf16 or float32 (out_dtype), rounded once.
  * Made for few rows: the weight is streamed once for every 16. Sums and the scaling are float32. x enters as
- * it is for more than 4 rows. Up to 4 take integers: a row's group of x has one exponent and 22 bits, so that
- * values within 2^-14 of its largest are exact and smaller ones off by at most 2^-22 of the largest; a group's
- * sum is exact then. An infinite or NaN x[m,k] makes row m NaN. A group's sum of x and its codes (up to 15) is
+ * it is for more than 4 rows. Up to 4 take integers: a row's group of x has one exponent and 30 bits, so that
+ * values within 2^-22 of its largest are exact and smaller ones off by at most 2^-30 of the largest, less than a
+ * float32 sum loses. An infinite or NaN x[m,k] makes row m NaN. A group's sum of x and its codes (up to 15) is
  * formed before its scale: values of x from 1e35 on may make it an infinity or NaN where C[m,n] would fit.
  * K % group == 0, K <= 2^22, M <= 2^20, N <= 2^26 (MOK_EUNSUPPORTED past the last two, below 2^31).
  * x and codes start on 16 bytes. Bit-identical reruns; no workspace. */

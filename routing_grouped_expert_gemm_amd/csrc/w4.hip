@@ -16,12 +16,12 @@
 // the routing, for 602 MB. (Fewer
 // operations for the zero points, -z times the sums of x's bytes as the accumulators' start, changed nothing.)
 //
-//  k_w4_few   up to 4 rows of x a pass: integers. x is cut into 22-bit integers with one exponent for a
-//    row's group (what is lost is below 2^-22 of the group's largest value; bf16 values within 2^-14 of it
-//    are exact) and those into three signed bytes, which are rows 4 m, 4 m + 1, 4 m + 2 of the 16-row int8
-//    MFMA. A code less its zero point is a byte: 4 (with zero points 7) vector operations for 8 codes.
-//    The group's sums are exact; a lane's accumulators are the three bytes' sums of row kq and column n, so
-//    that scale and exponent are one fused multiply-add a group.
+//  k_w4_few   up to 4 rows of x a pass: integers. x is cut into 30-bit integers with one exponent for a
+//    row's group (what is lost is below 2^-30 of the group's largest value, less than a float32 sum of the
+//    group loses; bf16 values within 2^-22 of it, and float32 values within 2^-6, are exact) and those into four
+//    signed bytes, which are rows 4 m .. 4 m + 3 of the 16-row int8 MFMA. A code less its zero point is a
+//    byte: 4 (with zero points 7) vector operations for 8 codes. The bytes' sums are exact; a lane's
+//    accumulators are those of row kq and column n, joined to the group's sum in float32.
 //  k_w4_token the same, of all the experts of one token.
 //  k_w4_rows  up to 16 rows: the bf16 MFMA. A nibble 0 .. 15 is, as an E4M3 byte, q 2^-9 (its first two
 //    binades are evenly spaced), so one AND for four codes and a conversion for two give exact bf16
@@ -338,12 +338,26 @@ MOK_DEV void code_bytes(uint32_t w, uint32_t zc, int& even, int& odd) {
   }
 }
 
-// x's rows in LDS, as bytes: [rows][3][ck + 16], then the groups' exponents [rows][ck / G]. XF: 16 bytes that
+// The bytes of n as signed digits, -128 .. 127 each: half a place's worth goes to every place but the highest.
+MOK_DEV uint32_t signed_bytes(int n) { return ((uint32_t)n + 0x00808080u) ^ 0x00808080u; }
+
+// The least bytes of four words (the first's lowest), .., their highest.
+MOK_DEV void bytes_by_place(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t& p0, uint32_t& p1, uint32_t& p2,
+                            uint32_t& p3) {
+  const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x05010400u), AB = __builtin_amdgcn_perm(b, a, 0x07030602u);
+  const uint32_t cd = __builtin_amdgcn_perm(d, c, 0x05010400u), CD = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  p0 = __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+  p1 = __builtin_amdgcn_perm(cd, ab, 0x07060302u);
+  p2 = __builtin_amdgcn_perm(CD, AB, 0x05040100u);
+  p3 = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
+}
+
+// x's rows in LDS, as bytes: [rows][4][ck + 16], then the groups' exponents [rows][ck / G]. XF: 16 bytes that
 // 8 values take (bf16: 1, float32: 2).
 template <int G, bool Z, int XF>
 struct W4Bytes {
   static constexpr int XU = 2;         // units of 8 values that a thread has in flight
-  static constexpr int SHIFT = (Z ? 148 : 152) - 8;    // of an exponent: the integers' place, 16, the sums' 256
+  static constexpr int SHIFT = (Z ? 156 : 160) - 16;   // of an exponent: the integers' place, 16, the sums' 65536
   int8_t* xb;
   const void* x;
   int K, n_rows, ck, ld, ng, cw, units;
@@ -351,7 +365,7 @@ struct W4Bytes {
   uint4 xv[XU][XF];
   MOK_DEV W4Bytes(int8_t* lds, const void* x_, int K_, int rows, int ck_)
       : xb(lds), x(x_), K(K_), n_rows(rows), ck(ck_), ld(ck_ + 16), ng(ck_ / G), cw(ck_ / 8), units(rows * (ck_ / 8)),
-        ex((float*)(lds + rows * 3 * (ck_ + 16))) {}
+        ex((float*)(lds + rows * 4 * (ck_ + 16))) {}
   // the columns c ck .. : row_of(r) is where row r lies in x, in rows
   template <class Row> MOK_DEV void load(int c, int u0, Row&& row_of) {
 #pragma unroll
@@ -395,18 +409,14 @@ struct W4Bytes {
       const int e = max((int)(top >> 23), 1);
       if (u % (G / 8) == 0)
         ex[r * ng + o / G] = e == 255 ? NAN : __builtin_amdgcn_ldexpf(1.0f, e - SHIFT);
-      uint32_t d[3][2] = {};
+      uint32_t n[8], d[4][2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {                  // |v| < 2^22; bytes from the least, rounded to nearest
-        const int n0 = e == 255 ? 0 : (int)rintf(__builtin_amdgcn_ldexpf(v[i], 148 - e));
-        const int n1 = (n0 + 128) >> 8, n2 = (n1 + 128) >> 8;
-        const int h = i & 1, b = 8 * (i >> 1);       // the even ones, then the odd ones
-        d[2][h] |= (uint32_t)(n0 & 0xFF) << b;
-        d[1][h] |= (uint32_t)(n1 & 0xFF) << b;
-        d[0][h] |= (uint32_t)(n2 & 0xFF) << b;
-      }
+      for (int i = 0; i < 8; ++i)                    // |v| < 2^30
+        n[i] = e == 255 ? 0 : signed_bytes((int)rintf(__builtin_amdgcn_ldexpf(v[i], 156 - e)));
 #pragma unroll
-      for (int q = 0; q < 3; ++q) *(uint2*)(xb + (r * 3 + q) * ld + o) = make_uint2(d[q][0], d[q][1]);
+      for (int h = 0; h < 2; ++h) bytes_by_place(n[h], n[2 + h], n[4 + h], n[6 + h], d[3][h], d[2][h], d[1][h], d[0][h]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *(uint2*)(xb + (r * 4 + q) * ld + o) = make_uint2(d[q][0], d[q][1]);
     }
   }
   // Chunk c into LDS; loaded: the first units are in xv.
@@ -418,11 +428,11 @@ struct W4Bytes {
       if (u - (int)threadIdx.x >= units) break;
     }
   }
-  // Where the lane's row of the MFMA lies: byte ln % 4 of row first + ln / 4 (a fourth byte, and rows past the
-  // last, are not looked at), with its columns' place in 128; and the exponents of row first + kq.
+  // Where the lane's row of the MFMA lies: byte ln % 4 of row first + ln / 4 (rows past the last are not looked
+  // at), with its columns' place in 128; and the exponents of row first + kq.
   MOK_DEV const int8_t* fragment(int first) const {
     const int kq = lane_id() >> 4, ln = lane_id() & 15;
-    return xb + (min(first + (ln >> 2), n_rows - 1) * 3 + min(ln & 3, 2)) * ld +
+    return xb + (min(first + (ln >> 2), n_rows - 1) * 4 + (ln & 3)) * ld +
            (G == 128 ? 32 * kq : G == 64 ? 32 * (kq & 1) + 16 * (kq >> 1) : 8 * kq);
   }
   MOK_DEV const float* exponents(int first) const { return ex + min(first + (lane_id() >> 4), n_rows - 1) * ng; }
@@ -462,7 +472,7 @@ MOK_DEV void w4_few_body(uint4 (&q)[W4_LOADS], const W4Groups<G, Z>& gr, const i
     q[l] = w.load(0, l, kn);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const float v = fmaf((float)((acc[g][1] << 8) + acc[g][2]), 1.0f / 256, (float)acc[g][0] * 256.0f);
+      const float v = fmaf((float)((acc[g][2] << 8) + acc[g][3]), 1.0f / 65536, (float)((acc[g][0] << 8) + acc[g][1]));
       total = fmaf(v * xe[l * NG + g], gr.scale(l * NG + g), total);
     }
   }

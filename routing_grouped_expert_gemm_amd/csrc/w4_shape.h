@@ -12,12 +12,12 @@ namespace mok {
 
 constexpr int W4_BODY = 512;         // columns of a wave's step
 constexpr int W4_MAXW = 8;           // waves of a workgroup
-constexpr int W4_LDS_FEW = 52 * 1024, W4_LDS_ROWS = 72 * 1024;   // for x: two workgroups a CU
+constexpr int W4_LDS_FEW = 70 * 1024, W4_LDS_ROWS = 72 * 1024;   // for x: two workgroups a CU
 
-// LDS of a body's columns of one row of x. few: three bytes a value and a float32 exponent a group; else bf16,
+// LDS of a body's columns of one row of x. few: four bytes a value and a float32 exponent a group; else bf16,
 // pl planes of it. Behind each plane's columns lie 16 bytes more.
-MOK_HOSTDEV int w4_body_bytes(bool few, int g, int pl) { return few ? 3 * W4_BODY + W4_BODY / g * 4 : 2 * pl * W4_BODY; }
-MOK_HOSTDEV int w4_pad_bytes(bool few, int pl) { return 16 * (few ? 3 : pl); }
+MOK_HOSTDEV int w4_body_bytes(bool few, int g, int pl) { return few ? 4 * W4_BODY + W4_BODY / g * 4 : 2 * pl * W4_BODY; }
+MOK_HOSTDEV int w4_pad_bytes(bool few, int pl) { return 16 * (few ? 4 : pl); }
 
 // Bodies of a chunk and part that a workgroup takes at a time: cap bytes (which hold one body of every row and
 // part at least) over rows of body_bytes, ks parts.
