@@ -584,9 +584,8 @@ int mok_w4_gemm(const void* x, const uint8_t* codes, const void* scales, const u
  * A share of the experts (E_l < E) gives its part of the sum. y_in: the shared experts' output or the
  * residual stream (NULL: none). Where n_routes = T k gives an expert of E at most 2 on
  * average, or T <= 4, the products are mok_w4_gemm's of up to 4 rows, x and the hidden values as such
- * integers; else x enters as it is and the hidden values with 16 bits of their significand. Between the
- * products they are float32, sums are float32, y is rounded once. Every route is
- * computed; ids outside the local experts are skipped, an expert named twice counts twice. */
+ * integers; else both enter as they are. Between the products the hidden values are float32, sums are
+ * float32, y is rounded once. Every route is computed; ids outside the local experts are skipped, an expert named twice counts twice. */
 typedef struct mok_moe_w4_args {
   int64_t T;               /* tokens                                                        */
   int32_t d, I;            /* model dim and expert intermediate: multiples of group         */

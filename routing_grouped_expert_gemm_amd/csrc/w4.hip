@@ -29,9 +29,8 @@
 //    the zero point off; the sum is scaled in float32.
 //  k_w4_split the same for at most a tile a CU: x from the caches, up to 16 parts of K.
 //
-// The MoE's first launch writes H = silu(gate) up in float32, its second reads it (k_w4_rows: as two bf16
-// planes, 16 significant bits, in two rows of the MFMA); a third adds a token's experts in the order of
-// its picks.
+// The MoE's first launch writes H = silu(gate) up in float32, its second reads it (k_w4_rows: as three bf16
+// planes, all of its bits); a third adds a token's experts in the order of its picks.
 #include <algorithm>
 
 #include "device_common.h"
@@ -169,9 +168,9 @@ struct W4Groups {
   MOK_DEV float zero(int g) const { return Z ? (float)zero_byte(g) : 8.0f; }
 };
 
-// total += the products of 128 columns (load i of a body), whose x are a[0 .. 3].
-template <int G, bool Z, int S, int BODY>
-MOK_DEV void w4_step(const uint4 (&q)[S], const W4Groups<G, Z, BODY> (&gr)[S], int i, const bf16x8_t (&a)[4],
+// total += the products of 128 columns (load i of a body), whose x are the sums of a[0 .. A)[0 .. 3].
+template <int G, bool Z, int S, int A, int BODY>
+MOK_DEV void w4_step(const uint4 (&q)[S], const W4Groups<G, Z, BODY> (&gr)[S], int i, const bf16x8_t (&a)[A][4],
                      f32x4_t (&total)[S]) {
   constexpr int J = G < 128 ? G / 32 : 4;            // instructions of a group
   const uint32_t c = Z ? 0x3F803F80u : 0xC100C100u;  // 1 or -8
@@ -187,14 +186,19 @@ MOK_DEV void w4_step(const uint4 (&q)[S], const W4Groups<G, Z, BODY> (&gr)[S], i
     const int g = (128 * i + 32 * j0) / G;
     f32x4_t x = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = j0; j < j0 + J; ++j) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], cv, x, 0, 0, 0);
+    for (int j = j0; j < j0 + J; ++j)
+#pragma unroll
+      for (int n = 0; n < A; ++n) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[n][j], cv, x, 0, 0, 0);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       f32x4_t acc = x;
       if constexpr (Z) acc *= -gr[s].zero(g);
 #pragma unroll
-      for (int j = j0; j < j0 + J; ++j)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], unpack8(w[s][j]), acc, 0, 0, 0);
+      for (int j = j0; j < j0 + J; ++j) {
+        const bf16x8_t b = unpack8(w[s][j]);
+#pragma unroll
+        for (int n = 0; n < A; ++n) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[n][j], b, acc, 0, 0, 0);
+      }
       const float sc = gr[s].scale(g);
 #pragma unroll
       for (int e = 0; e < 4; ++e) total[s][e] = fmaf(acc[e], sc, total[s][e]);
@@ -282,7 +286,8 @@ MOK_DEV void w4_store(const W4Args& p, const W4Rows& rows, int64_t m, int n, con
   }
 }
 
-// The parts' sums of the workgroup's tiles, in order: red [wave][S][16 rows][16 columns].
+// The parts' sums of the workgroup's tiles, in order: red [wave][S][16 rows][16 columns]. PL > 1: row m's are those
+// of row m and of row lo_row + m.
 template <int MODE, int S, int PL>
 MOK_DEV void w4_join(const W4Args& p, const W4Rows& rows, const float* red, int64_t m0, int n_rows,
                      int lo_row, int t0, int nt) {
@@ -295,7 +300,7 @@ MOK_DEV void w4_join(const W4Args& p, const W4Rows& rows, const float* red, int6
       for (int w = 0; w < p.ks; ++w) {
         const float* r = red + (((c >> 4) * p.ks + w) * S + s) * 256 + m * 16 + (c & 15);
         v[s] += r[0];
-        if constexpr (PL == 2) v[s] += r[lo_row * 16];
+        if constexpr (PL > 1) v[s] += r[lo_row * 16];
       }
     }
     if (n < p.N) w4_store<MODE, S>(p, rows, m0 + m, n, v);
@@ -614,10 +619,13 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_token(const W4Args p) {
   }
 }
 
-// The same for up to 16 rows of the MFMA, x in LDS for the whole workgroup.
+// The same for up to 16 rows of the MFMA, x in LDS for the whole workgroup. H, which is float32, is three bf16
+// values, the bits of its significand in order: 8 rows of H are the MFMA's rows m (first) and 8 + m (second),
+// and of another MFMA on the same codes half the third in both. The accumulators' rows m and 8 + m add up.
 template <int G, bool Z, int MODE>
 __global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
-  constexpr int S = MODE == W4_UP ? 2 : 1, PL = MODE == W4_DOWN ? 2 : 1, MR = 16 / PL;
+  constexpr int S = MODE == W4_UP ? 2 : 1, PL = MODE == W4_DOWN ? 3 : 1;
+  constexpr int MR = PL == 1 ? 16 : 8, A = PL == 1 ? 1 : 2;          // rows of a pass, MFMAs of a fragment
   extern __shared__ __attribute__((aligned(16))) bf16_t xs[];   // [rows PL][ck + 8]; then the waves' sums
   __shared__ int16_t list[MODE == W4_DENSE ? 1 : W4_SCAN];
   const int tid = threadIdx.x, lane = lane_id(), wv = uniform(tid >> 6), kq = lane >> 4, ln = lane & 15;
@@ -638,16 +646,16 @@ __global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
     const int ck = bpc * bw, chunks = (p.K + ck - 1) / ck, ld = ck + 8;
     auto column = [&](int c, int b) { return c * ck + (part * bpc + b) * W4_BODY; };
     // x's columns c ck .. to LDS, 8 at a time, in unpack8's order: XU loads of a thread in flight
-    constexpr int XU = 4 / PL;
+    constexpr int XU = PL == 1 ? 4 : 2, XF = PL == 1 ? 1 : 2;          // XF: 16 bytes of 8 values
     const int cw = ck / 8, units = n_rows * cw;
-    uint4 xv[XU][PL];
+    uint4 xv[XU][XF];
     auto x_load = [&](int c, int u0) {
 #pragma unroll
       for (int j = 0; j < XU; ++j) {
         const int u = u0 + j * (int)blockDim.x, r = min(u / cw, n_rows - 1), k = c * ck + (u - r * cw) * 8;
         const int64_t at = w4_x_row<MODE>(p, rows, m0 + r) * p.K + min(k, p.K - 8);
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
+        for (int i = 0; i < XF; ++i) {
           const uint4 v = PL == 1 ? *(const uint4*)((const bf16_t*)p.x + at) : *(const uint4*)((const float*)p.x + at + 4 * i);
           xv[j][i] = k < p.K ? v : make_uint4(0, 0, 0, 0);
         }
@@ -662,21 +670,32 @@ __global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
         if constexpr (PL == 1) {
           *(bf16x8_t*)to = order8(xv[j][0]);
         } else {
-          const uint4 a = xv[j][0], b = xv[j][PL - 1];
+          const uint4 a = xv[j][0], b = xv[j][XF - 1];
           const uint32_t w[8] = {a.x, a.z, b.x, b.z, a.y, a.w, b.y, b.w};
-          bf16x8_t hi, lo;
+          uint32_t p[3][4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            hi[i] = (__bf16)__uint_as_float(w[i]);
-            lo[i] = (__bf16)(__uint_as_float(w[i]) - (float)hi[i]);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t t[3][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {              // cut off, not rounded: the rest fits the next, exactly
+              float v = __uint_as_float(w[2 * i + h]);
+              t[0][h] = __float_as_uint(v) >> 16;
+              v -= __uint_as_float(t[0][h] << 16);
+              t[1][h] = __float_as_uint(v) >> 16;
+              v -= __uint_as_float(t[1][h] << 16);
+              t[2][h] = __float_as_uint(0.5f * v) >> 16;
+            }
+#pragma unroll
+            for (int q = 0; q < 3; ++q) p[q][i] = t[q][0] | (t[q][1] << 16);
           }
-          *(bf16x8_t*)to = hi;
-          *(bf16x8_t*)(to + n_rows * ld) = lo;
+#pragma unroll
+          for (int q = 0; q < 3; ++q) *(uint4*)(to + q * n_rows * ld) = make_uint4(p[q][0], p[q][1], p[q][2], p[q][3]);
         }
       }
     };
     // the row of xs that is this lane's of the MFMA's 16 (those past the rows are not looked at)
-    const bf16_t* const xl = xs + (PL == 2 ? min(ln & 7, n_rows - 1) + (ln >> 3) * n_rows : min(ln, n_rows - 1)) * ld;
+    const bf16_t* const xl = xs + (PL > 1 ? min(ln & 7, n_rows - 1) + (ln >> 3) * n_rows : min(ln, n_rows - 1)) * ld;
+    const int third = (PL > 1 ? 2 - (ln >> 3) : 0) * n_rows * ld;      // from there to H's third part
     uint4 q[W4_LOADS][S];
     W4Groups<G, Z> gr[S];
     f32x4_t total[S];
@@ -709,17 +728,19 @@ __global__ __launch_bounds__(64 * W4_MAXW) void k_w4_rows(const W4Args p) {
 #pragma unroll
         for (int s = 0; s < S; ++s) gn[s].load(p.w[s], w.row, p.K, kn);
         const bf16_t* const xb = xl + (part * bpc + b) * W4_BODY;
-        bf16x8_t a[2][4];
+        bf16x8_t a[2][A][4];
         auto read = [&](int l) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            a[l & 1][j] = *(const bf16x8_t*)(xb + 128 * l + (G < 128 ? 32 * j + 8 * kq : 32 * kq + 8 * j));
+          for (int n = 0; n < A; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              a[l & 1][n][j] = *(const bf16x8_t*)(xb + n * third + 128 * l + (G < 128 ? 32 * j + 8 * kq : 32 * kq + 8 * j));
         };
         read(0);
 #pragma unroll
         for (int l = 0; l < W4_LOADS; ++l) {
           if (l + 1 < W4_LOADS) read(l + 1);
-          w4_step<G, Z, S, W4_BODY>(q[l], gr, l, a[l & 1], total);
+          w4_step<G, Z, S, A, W4_BODY>(q[l], gr, l, a[l & 1], total);
 #pragma unroll
           for (int s = 0; s < S; ++s) q[l][s] = w.load(s, l, kn);
         }
@@ -778,10 +799,10 @@ __global__ __launch_bounds__(64 * W4_PARTS) void k_w4_split(const W4Args p) {
     load(next, i + 1);
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-      bf16x8_t a[4];
+      bf16x8_t a[1][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = order8(v[l][j]);
-      w4_step<G, Z, 1, W4_STEP>(now.q[l], now.gr, l, a, total);
+      for (int j = 0; j < 4; ++j) a[0][j] = order8(v[l][j]);
+      w4_step<G, Z, 1, 1, W4_STEP>(now.q[l], now.gr, l, a, total);
     }
     now = next;
   }
@@ -893,10 +914,10 @@ hipError_t launch_w4_split(W4Args a, int g, int64_t slots, hipStream_t s) {
 // how many it has on average.
 template <int MODE>
 hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t tokens, int64_t most, double mean, hipStream_t s) {
-  constexpr int S = MODE == W4_UP ? 2 : 1, PL = MODE == W4_DOWN ? 2 : 1;
+  constexpr int S = MODE == W4_UP ? 2 : 1, PL = MODE == W4_DOWN ? 3 : 1;
   const bool few = tokens <= 4 || mean <= 2.0;    // one in twenty experts of 2 rows has a second pass
   a.tiles = (a.N + 15) / 16;
-  const int mr = few ? 4 : 16 / PL;
+  const int mr = few ? 4 : PL > 1 ? 8 : 16;
   if (MODE == W4_DENSE) slots = (a.M + mr - 1) / mr;
   // at most a tile a CU (13 and 5 rows, N 4096, K 7168, groups of 32 with zero points: 20.5 -> 12.2 and 11.1 ->
   // 9.4 us; 13 rows, N 8192, with two: 21.8 -> 22.4, groups of 128 16.4 -> 19.3)

@@ -44,15 +44,19 @@ inline W4Shape w4_shape(bool few, int g, int pl, int K, int64_t waves, int pair,
   W4Shape s;
   const int bodies = (K + W4_BODY - 1) / W4_BODY, b = w4_body_bytes(few, g, pl);
   const int lds_x = few ? W4_LDS_FEW : W4_LDS_ROWS;
-  int parts = W4_MAXW / pair;
-  if (parts > bodies) parts = bodies;
-  if (parts > lds_x / (b * most)) parts = lds_x / (b * most);       // one body of every row and part has to fit
-  // as many parts of K as give every SIMD two waves
-  if (waves < 1) waves = 1;
-  const int64_t want = (2048 + waves - 1) / waves;
-  s.ks = want < parts ? (int)want : parts;
-  s.ks = (bodies + (bodies + s.ks - 1) / s.ks - 1) / ((bodies + s.ks - 1) / s.ks);
-  s.tpw = W4_MAXW / s.ks / pair * pair;
+  // twice as much for the bf16 rows of few workgroups, which have a CU each
+  for (int room = few ? lds_x : 2 * lds_x;; room = lds_x) {
+    int parts = W4_MAXW / pair;
+    if (parts > bodies) parts = bodies;
+    if (parts > room / (b * most)) parts = room / (b * most);       // one body of every row and part has to fit
+    // as many parts of K as give every SIMD two waves
+    if (waves < 1) waves = 1;
+    const int64_t want = (2048 + waves - 1) / waves;
+    s.ks = want < parts ? (int)want : parts;
+    s.ks = (bodies + (bodies + s.ks - 1) / s.ks - 1) / ((bodies + s.ks - 1) / s.ks);
+    s.tpw = W4_MAXW / s.ks / pair * pair;
+    if (room == lds_x || waves <= (int64_t)256 * s.tpw) break;
+  }
   s.cap = b * rows * s.ks * w4_bodies(bodies, s.ks, lds_x, b, rows);
   if (s.cap < b * most * s.ks) s.cap = b * most * s.ks;
   const size_t x = (size_t)s.cap + (size_t)w4_pad_bytes(few, pl) * most, sums = (size_t)s.tpw * s.ks * red;

@@ -42,22 +42,26 @@ def pack(v):
 HIDDEN = [(1, 4, 2, 128), (1, 64, 4, 64), (3, 8, 2, 32), (4, 2, 1, 128)]          # T, E, k, group: integers
 
 
-@pytest.mark.parametrize("T,E,k,group", HIDDEN)
+ROWS = [(5, 2, 1, 128), (8, 1, 1, 64), (20, 4, 2, 32), (70, 8, 2, 128), (600, 4, 2, 64)]      # bf16
+
+
+@pytest.mark.parametrize("T,E,k,group", HIDDEN + ROWS)
 def test_hidden_values_that_cancel(T, E, k, group):
-    """H = [2^18 + 2, 2^18, 2^25 (code: the zero point)] 2^j, for token j; weights 1, -1, 0: y is 2^(j + 1)."""
+    """H = [2^18 + 2^9 + 2, 2^18 + 2^9, 2^25 (code: the zero point)] 2^j, for token j; weights 1, -1, 0: y is 2^(j + 1)."""
     import routing_grouped_expert_gemm_amd as mok
     d, I = 2 * group, 2 * group
     up, gate, down = (torch.zeros(E, *s, dtype=torch.int64) for s in ((I, d), (I, d), (d, I)))
     for c in range(0, I, group):                           # in each group of H
         up[:, c, 0], up[:, c, 1], up[:, c + 1, 0], up[:, c + 5, 0] = 1, 1, 1, 1
+        up[:, c:c + 2, 4] = 1
         gate[:, c:c + 2, 2], gate[:, c + 5, 3] = 1, 1
     down[:, :, 0], down[:, :, 1] = 1, -1
     if T > 4:
         gate[:, 5::group] = 0                              # the integers' case alone
     x = torch.zeros(T, d)
     for t in range(T):
-        x[t, :4] = torch.tensor([2.0 ** 11, 2.0 ** -6, 2.0 ** 7, 2.0 ** 14])
-        x[t, 0:2] *= 2.0 ** (t % 8)
+        x[t, :5] = torch.tensor([2.0 ** 11, 2.0 ** -6, 2.0 ** 7, 2.0 ** 14, 4.0])
+        x[t, [0, 1, 4]] *= 2.0 ** (t % 8)
     one = lambda a: torch.ones(*a.shape[:-1], a.shape[-1] // group, device=DEV).bfloat16()  # noqa: E731
     L = [(pack(a).to(DEV), one(a), None) for a in (gate, up, down)]
     layer = mok.MoeW4Layer(*L, E=E, k=k, max_tokens=T)

@@ -17,7 +17,7 @@ using namespace mok;
 static long bad = 0, seen = 0;
 // rows: with the tokens' one route each; most: of all routes
 static void one(bool few, int g, int pl, int K, long long waves, int pair, int red, long long T, long long routes) {
-  const int mr = few ? 4 : 16 / pl, bodies = (K + W4_BODY - 1) / W4_BODY;
+  const int mr = few ? 4 : pl > 1 ? 8 : 16, bodies = (K + W4_BODY - 1) / W4_BODY;
   const int rows = (int)(T < mr ? T : mr), most = (int)(routes < mr ? routes : mr);
   const W4Shape s = w4_shape(few, g, pl, K, waves, pair, red, rows, most);
   bool ok = s.ks >= 1 && s.ks <= bodies && s.tpw >= pair && s.tpw * s.ks <= W4_MAXW && s.tpw % pair == 0 &&
