@@ -206,6 +206,24 @@ MOK_DEV double row_sum(double v) {
   return v;
 }
 
+// exp(x) for x <= 0 within 2^-35 of itself, 0 below -700 (float32 holds none of it): 2^n e^r, |r| <= ln 2 / 2, by
+// the series up to r^9. A softmax that is not renormalised takes one of every expert.
+MOK_DEV double exp_down(double x) {
+  const double n = rint(x * 1.4426950408889634);
+  const double r = fma(n, -0.6931471805599453, x);
+  double p = 1.0 / 362880;
+  p = fma(p, r, 1.0 / 40320);
+  p = fma(p, r, 1.0 / 5040);
+  p = fma(p, r, 1.0 / 720);
+  p = fma(p, r, 1.0 / 120);
+  p = fma(p, r, 1.0 / 24);
+  p = fma(p, r, 1.0 / 6);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return x > -700.0 ? __builtin_amdgcn_ldexp(p, (int)n) : 0.0;
+}
+
 MOK_DEV uint32_t key_of(float v) {
   const uint32_t u = __float_as_uint(v);
   return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
@@ -279,10 +297,10 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_l
     for (int q = 0; q < Q; ++q) top = fmaxf(top, v[q]);
     top = row_maxf(top);
     if (!a.renorm && top > -INFINITY) {
-      float s = 0.0f;
+      double s = 0.0;                              // (the weights are float64's, rounded once)
 #pragma unroll
-      for (int q = 0; q < Q; ++q) s += expf(v[q] - top);
-      sum = row_sum((double)s);
+      for (int q = 0; q < Q; ++q) s += exp_down((double)v[q] - (double)top);
+      sum = row_sum(s);
     }
   }
   // margin of a value x, m0 + m1 |x|: pairs further apart than this are in the order of float64. The bits
