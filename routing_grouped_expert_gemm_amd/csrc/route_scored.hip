@@ -378,8 +378,11 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_l
     }
     const bool in = g < a.G && rank < a.Gk, out = g < a.G && !in;
     const float least = -row_maxf(in ? -w : -INFINITY), most = row_maxf(out ? w : -INFINITY);
-    // (worths carry no places: m0 of each member, and roundings; by_logit they are logits themselves)
-    const float near = by_logit ? m0 * fmaxf(1.0f, fabsf(least)) : 2.0f * m0 + (m0 == 0.0f ? 9e-5f : 4e-7f) * fabsf(least);
+    // (worths carry no places: m0 of each member, and roundings; by_logit they are logits themselves. A bias
+    // may be any number, and members of other signs leave a worth far smaller than what was rounded)
+    const float size = a.bias ? row_maxf((w1 > -INFINITY ? fabsf(w1) : 0.0f) + (w2 > -INFINITY ? fabsf(w2) : 0.0f))
+                              : fabsf(least);
+    const float near = by_logit ? m0 * fmaxf(1.0f, fabsf(least)) : 2.0f * m0 + (m0 == 0.0f ? 9e-5f : 4e-7f) * size;
     redo |= most > -INFINITY && least - most < near;
     if (by_logit && most > -INFINITY)              // where float64 scores may be equal
       redo |= a.sigmoid ? most > 20.0f || least < -700.0f : least - top < -700.0f;
