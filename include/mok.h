@@ -482,7 +482,8 @@ int mok_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_dtype
  * The experts form n_groups groups of E / n_groups neighbours. A group's worth is the sum of its
  * group_top (1 or 2) largest c; the topk_groups groups of most worth are kept, and the picks are the
  * k largest c in them, in descending order. Ties, of groups as of experts, go to the lower id.
- *   w[j] = scale s[idx[j]]            renorm: scale s[idx[j]] / sum_i s[idx[i]] (0 where the sum is 0)
+ *   w[j] = scale s[idx[j]]            renorm: scale s[idx[j]] / sum_i s[idx[i]] (0 where the sum is 0; of a
+ *                                     softmax exp(l[idx[j]]) / sum_i exp(l[idx[i]]), however small the scores)
  * Scores, c and worths are those of float64 arithmetic; w is rounded once. An expert with l or bias
  * -inf is left out: it adds nothing to its group's worth and is picked only where fewer than k others
  * are left in the kept groups (a row that leaves nothing picks the lowest ids, with weights 0 where l
@@ -507,7 +508,7 @@ int mok_route_scored(const void* x, const void* w_router, int64_t T, int32_t d, 
  *   dlogits[t,e] = dlogits_in[t,e] + sum_j dtopk_w[t,j] d w[t,j] / d l[t,e]
  * dlogits_in [T, E] (NULL: zeros; the balance loss's gradient): dlogits may be the same buffer, and
  * overlaps nothing else. Picks outside [0, E) take no part, neither in a renormalising sum; an expert
- * named twice adds up. A row whose scores sum to 0 has a zero gradient. Feed the result to
+ * named twice adds up. A row whose sum of scores is 0 has a zero gradient. Feed the result to
  * mok_route_backward as its dlogits, without picks. No atomics: bit-identical reruns. */
 int mok_topk_scored_backward(const float* logits, const int32_t* topk_idx, const float* dtopk_w,
                              const float* dlogits_in, int64_t T, int32_t E, int32_t k,

@@ -166,6 +166,13 @@ MOK_DEV void row_exact(const RsArgs& a, int64_t t, uint64_t* key, uint64_t* wort
   if (lane < a.k) s = score(l[mine]);
   if (a.renorm) {
     double sum = 0.0;
+    if (!a.sigmoid && inv == inv) {                // from the picks' largest, as it may be far below the row's
+      const double x = lane < a.k ? (double)l[mine] : -INFINITY;
+      double most = x;
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) most = fmax(most, __shfl_xor(most, m, kWave));
+      s = most > -INFINITY ? exp(x - most) : 0.0;
+    }
     for (int j = 0; j < a.k; ++j) sum += __shfl(s, j, kWave);
     s = sum == 0.0 ? 0.0 : s / sum;
   }
