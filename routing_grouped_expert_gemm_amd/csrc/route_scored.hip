@@ -549,6 +549,7 @@ MOK_DEV void scatter_picks(const RsBwd& a, int64_t t0, int n, float* st, const f
         const double x = exp(-fabs((double)lg)), y = 1.0 / (1.0 + x);
         s = lg < 0.0f ? x * y : y;
         one = lg < 0.0f ? y : x * y;
+        if (lg < 0.0f && x < 0x1p-1024) s = 0.0;   // the forward's, where exp(-l) is past float64
       } else {
         const float m = pick_max<LK>(lg);
         s = m > -INFINITY ? exp((double)lg - (double)m) : 0.0;
