@@ -540,10 +540,8 @@ hipError_t run_gated_bwd(GnBwd a, float* dgate_all, float* dw_post, float* dw_pr
   };
   if (a.rows == 0) {
   } else if (d > 8192) {
-    const bool wide = d > 2048;
     for (int64_t r = 0; r < a.rows; r += kMaxLaunchRows)
-      launch_k(wide ? k_gated_norm_bwd_any<T, 1024> : k_gated_norm_bwd_any<T, 256>,
-               dim3((unsigned)std::min(a.rows - r, kMaxLaunchRows)), dim3(wide ? 1024 : 256), 0, s,
+      launch_k(k_gated_norm_bwd_any<T, 1024>, dim3((unsigned)std::min(a.rows - r, kMaxLaunchRows)), dim3(1024), 0, s,
                nullptr, nullptr, a, r);
     if (n_sums)
       launch_k(k_gated_norm_cols_any<T>, dim3((d + NORM_NT - 1) / NORM_NT, blocks), dim3(NORM_NT),
