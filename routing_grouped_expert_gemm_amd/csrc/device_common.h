@@ -75,6 +75,13 @@ MOK_DEV int32_t block_excl_scan_1024(int32_t v, int32_t* sh, int32_t* total) {
   return r;
 }
 
+// Orders the wave's LDS accesses before this point against those behind it.
+MOK_DEV void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Values every lane of the wave holds identically, moved to scalar registers.
 MOK_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 template <class T>

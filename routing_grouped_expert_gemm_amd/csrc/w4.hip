@@ -72,13 +72,6 @@ struct W4Args {
   const void* y_in;                  // k_w4_token: bf16 [T, N] or NULL; out: y bf16 [T, N]
 };
 
-// Orders the wave's LDS accesses before this point against those behind it.
-MOK_DEV void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // Lane groups of 16 <-> registers: afterwards w[j] of lane group q is what w[q] of group j was.
 MOK_DEV void transpose4(uint32_t (&w)[4]) {
   auto s32 = [](uint32_t& a, uint32_t& b) {
