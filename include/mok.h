@@ -566,7 +566,7 @@ int mok_quantize_int4(const void* src_bf16, int64_t rows, int32_t K, int32_t gro
                       void* scales, uint8_t* zeros, void* stream);
 
 /* C[m,n] = sum_k x[m,k] W[n,k]: x [M, K] bf16, C [M, N] bf16 or float32 (out_dtype), rounded once.
- * Made for few rows: the weight is streamed once for every 16. Sums and the scaling are float32. x enters as
+ * Made for few rows: the weight is streamed once for up to 4 of them, or for every 16. Sums and the scaling are float32. x enters as
  * it is for more than 4 rows. Up to 4 take integers: a row's group of x has one exponent and 30 bits, so that
  * values within 2^-22 of its largest are exact and smaller ones off by at most 2^-30 of the largest, less than a
  * float32 sum loses. An infinite or NaN x[m,k] makes row m NaN. A group's sum of x and its codes (up to 15) is
@@ -577,16 +577,19 @@ int mok_w4_gemm(const void* x, const uint8_t* codes, const void* scales, const u
                 int64_t M, int64_t N, int32_t K, int32_t group, int32_t out_dtype, void* c,
                 void* stream);
 
-/* The routed experts' FFNs of the layer on such weights, for the few tokens of a decoding step (each
- * weight that some token picks is streamed once for every 16 of its tokens, 8 for the down
- * projection; the others are not read):
+/* The routed experts' FFNs of the layer on such weights, for the few tokens of a decoding step (weights
+ * that no token picks are not read):
  *   y[t] = y_in[t] + sum_{j: local} w[t,j] W_down[e] (silu(W_gate[e] x[t]) * (W_up[e] x[t])),
  *   e = topk_idx[t,j], local: e0 <= e < e0 + E_l, j ascending
  * A share of the experts (E_l < E) gives its part of the sum. y_in: the shared experts' output or the
- * residual stream (NULL: none). Where n_routes = T k gives an expert of E at most 2 on
- * average, or T <= 4, the products are mok_w4_gemm's of up to 4 rows, x and the hidden values as such
- * integers; else both enter as they are. Between the products the hidden values are float32, sums are
- * float32, y is rounded once. Every route is computed; ids outside the local experts are skipped, an expert named twice counts twice. */
+ * residual stream (NULL: none). Where T k gives an expert of E at most 2 routes on average, or T <= 4, the
+ * products are mok_w4_gemm's of up to 4 rows, x and the hidden values as such integers, and an expert's weights
+ * are streamed once for every 4 of its routes; else both enter as they are, and the weights are streamed
+ * once for every 16 routes, of the down projection for every 8. (With k <= 8, all experts here, at most 0.25
+ * routes an expert on average and T k <= 1024 the down projection is streamed once a route.) A routing
+ * that sends most tokens to few experts takes the form of its average, and with it more passes.
+ * Between the products the hidden values are float32, sums are float32, y is rounded once. Every route is
+ * computed; ids outside the local experts are skipped, an expert named twice counts twice. */
 typedef struct mok_moe_w4_args {
   int64_t T;               /* tokens                                                        */
   int32_t d, I;            /* model dim and expert intermediate: multiples of group         */

@@ -17,8 +17,10 @@
 // shares a second launch adds in a fixed order: no atomics. Rows that are not whole 16-byte pieces, or lie
 // at other addresses, take the same kernels with loads and stores of single values' alignment and a last
 // piece value by value (float32, T 1001, d 1111 both ways: one value a thread and step, three passes over
-// memory and four launches, 38 us; so 27 us). bf16, T 8192: forward d 7168 102 us for 470 MB,
-// both directions d 2048 90 us for 436 MB, 4.6 and 4.9 TB/s.
+// memory and four launches, 38 us; so 24). That one-value form is left for rows past 16,384 values (8,192 in
+// the backward) or, forward, 2^21 rows. Whole passes, bf16, T 8192: forward d 7168 103 us for 470 MB, both
+// directions d 2048 90 us for 436 MB, 4.6 and 4.8 TB/s (under the profiler the kernels' own times come to 108
+// and 95).
 #include <algorithm>
 
 #include "device_common.h"
@@ -145,7 +147,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm(co
   }
 }
 
-// Any d and alignment: one workgroup a row, one value a thread and step.
+// Rows that the form above does not hold, or too many for it: one workgroup a row, one value a thread and step.
 template <class T, int NT>
 __global__ __launch_bounds__(NT) void k_gated_norm_any(const GnArgs a, int64_t row0) {
   __shared__ double sh[2][NT / 64];
@@ -372,7 +374,7 @@ __global__ __launch_bounds__(TPR > NORM_NT ? TPR : NORM_NT) void k_gated_norm_bw
   share(a.p_pre, ab);
 }
 
-// Any d and alignment. First launch: a workgroup a row; what its columns' sums need of the row
+// The same for rows that it does not hold. First launch: a workgroup a row; what its columns' sums need of the row
 // (both rstd and their scales, the mean of g nh) goes to stat.
 template <class T, int NT>
 __global__ __launch_bounds__(NT) void k_gated_norm_bwd_any(const GnBwd a, int64_t row0) {
@@ -507,7 +509,7 @@ hipError_t run_gated(const GnArgs& a, hipStream_t s) {
   else if (d <= 1024) go(Form<64, 2>{});
   else if (a.rows <= 256 && d <= 8192) go(Form<1024, 1>{});
   else if (d <= 4096) go(Form<256, 2>{});
-  // (bf16 T 8192, d 7168: 108 us, with 512 threads a row 109, with 1024 145)
+  // (bf16 T 8192, d 7168, under the profiler: 108 us, with 512 threads a row 109, with 1024 145)
   else if (d <= 8192) go(Form<256, 4>{});
   else go(Form<1024, 2>{});
   return hipGetLastError();

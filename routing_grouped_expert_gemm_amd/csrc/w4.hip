@@ -4,16 +4,17 @@
 //   W[n,k] = (q[n,k] - z[n,k / g]) s[n,k / g],  q 0 .. 15, two codes a byte, 2i in the low nibble
 //   C[m,n] = sum_groups s (sum_{k in group} x[m,k] (q - z))
 //
-// Bound by streaming the codes once, and by the start of each workgroup; the vector unit, which has to take
-// every code apart, is busy for a third to a half of the time. A weight's 16 rows and 128 columns are one 16-byte load a lane (lane (kq, n): row n, 32 codes).
-// A wave takes one tile (16 weight rows; of the MoE's first product gate and up tiles in turn) and one of
-// KS parts of K and streams it in bodies of 512 columns: the loads of the next body are in flight while
-// this one's are used, each issued as its register becomes free. A workgroup is 8 waves: 8 / KS tiles by
-// KS parts, whose sums meet in LDS in a fixed order. (Streamed alone, the codes of T 1, d 7168, I 2048, k 8
-// come at 5.3 TB/s with one wave a tile and 32 KB a CU in flight, 4.7 with two and 64 KB.) T 1, d 7168, I 2048,
-// k 8 of 256 experts: 49 us for 182 MB, where each of the two launches starts up for 5 to 7 us (x to LDS, the
-// first codes); 48 tokens there on 32 of the experts with zero points: 186 to 204 us, by
-// the routing, for 602 MB. (Fewer
+// Bound by streaming the codes, and by the start of each workgroup; the vector unit, which has to take
+// every code apart, is busy for a fifth to a half of the time. A weight's 16 rows and 128 columns are one 16-byte
+// load a lane (lane (kq, n): row n, 32 codes). A wave takes one tile (16 weight rows; of the MoE's first product
+// gate and up tiles in turn) and one of KS parts of K and streams it in bodies of 512 columns: the loads of the
+// next body are in flight while this one's are used, each issued as its register becomes free. A workgroup is
+// 8 waves: 8 / KS tiles by KS parts, whose sums meet in LDS in a fixed order. (Streamed alone, the codes of T 1,
+// d 7168, I 2048, k 8 come at 5.3 TB/s with one wave a tile and 32 KB a CU in flight, 4.7 with two and 64 KB.)
+//
+// Whole passes: T 1, d 7168, I 2048, k 8 of 256 experts 49 us for 182 MB, where each of the two launches starts
+// up for 5 to 7 us (x to LDS, the first codes); 48 tokens there on 32 of the experts with zero points 190 to
+// 204 us, by the routing, for 602 MB; T 48, d 2048, I 1408, k 6 of 64 (bf16 rows) 103 us for 283 MB. (Fewer
 // operations for the zero points, -z times the sums of x's bytes as the accumulators' start, changed nothing.)
 //
 //  k_w4_few   up to 4 rows of x a pass: integers. x is cut into 30-bit integers with one exponent for a
@@ -549,8 +550,8 @@ __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_few(const W4Args p) {
 
 // The down projection of a token whose experts hardly any other token shares: workgroup (x, y) takes tile x of
 // all the k <= 8 routes of token y, a wave a route (and part of K), and writes y itself, which saves P's way
-// through memory and a launch (T 1, d 7168, I 2048, k 8 of 256 experts: 56 -> 49 us; d 2048, I 1408, k 6 of
-// 64: 22 -> 19).
+// through memory and a launch (T 1, d 7168, I 2048, k 8 of 256 experts: 51.5 -> 49 us; d 2048, I 1408, k 6 of
+// 64: 20.3 -> 18.0).
 template <int G, bool Z>
 __global__ __launch_bounds__(64 * W4_MAXW, 4) void k_w4_token(const W4Args p) {
   extern __shared__ __attribute__((aligned(16))) int8_t xb[];
@@ -908,7 +909,10 @@ hipError_t launch_w4_split(W4Args a, int g, int64_t slots, hipStream_t s) {
 template <int MODE>
 hipError_t launch_w4(W4Args a, int g, int64_t slots, int64_t tokens, int64_t most, double mean, hipStream_t s) {
   constexpr int S = MODE == W4_UP ? 2 : 1, PL = MODE == W4_DOWN ? 3 : 1;
-  const bool few = tokens <= 4 || mean <= 2.0;    // one in twenty experts of 2 rows has a second pass
+  // one in twenty experts of 2 rows has a second pass. Whole passes, bf16 rows and integers: 64 experts of d 2048,
+  // I 1408, k 6 at a mean of 1.5, 2, 2.5 and 4 rows 83 and 72, 87 and 82, 90 and 90, 102 and 113 us; 32 of 256 of
+  // d 7168, I 2048, k 8 with zero points at 1.5, 2, 2.5 and 4: 200 and 190, 225 and 214, 245 and 250, 297 and 330
+  const bool few = tokens <= 4 || mean <= 2.0;
   a.tiles = (a.N + 15) / 16;
   const int mr = few ? 4 : PL > 1 ? 8 : 16;
   if (MODE == W4_DENSE) slots = (a.M + mr - 1) / mr;
@@ -1067,7 +1071,10 @@ int mok_moe_w4_forward(const mok_moe_w4_args* args, void* stream) {
   w.w[0] = {a.down_codes, (const uint16_t*)a.down_scales, a.down_zeros};
   w.x = ws + p.H; w.N = a.d; w.K = a.I;
   // few routes an expert: nearly all of its tokens' products would be one row (mean 0.25: one in eight
-  // experts that are picked serves two); and all experts here, or waves would be idle
+  // experts that are picked serves two); and all experts here, or waves would be idle. Whole passes without and
+  // with it: 128 experts of d 512, I 256, k 8 at a mean of 0.25 17.4 and 13.2 us; 64 of d 2048, I 1408, k 6 at 0.19
+  // and 0.47 26.5 and 23.1, 40.3 and 38.2; 256 of d 7168, I 2048, k 8 at 0.03, 0.06, 0.12 and 0.25 51.5 and 48.8,
+  // 87 and 87, 148 and 154, 259 and 284, where the weights that two tokens share count for more than a launch
   if (!p.plan && a.k <= W4_MAXW && a.E_l == a.E && mean <= 0.25) {
     w.out = a.y;
     w.y_in = a.y_in;
