@@ -384,6 +384,7 @@ __global__ __launch_bounds__(RS_NT) void k_topk_scored(const RsArgs a, bool by_l
                               : fabsf(least);
     const float near = by_logit ? m0 * fmaxf(1.0f, fabsf(least)) : 2.0f * m0 + (m0 == 0.0f ? 9e-5f : 4e-7f) * size;
     redo |= most > -INFINITY && least - most < near;
+    redo |= a.bias && !(size < INFINITY);          // worths past float32
     if (by_logit && most > -INFINITY)              // where float64 scores may be equal
       redo |= a.sigmoid ? most > 20.0f || least < -700.0f : least - top < -700.0f;
     if (aligned) {

@@ -28,3 +28,15 @@ def test_worths_that_cancel(E, G, Gk, score):
             c = np.sort((scores(l, score) + bias).reshape(200, G, n), axis=2)[:, :, -2:].sum(2)
             far &= np.diff(np.sort(c, axis=1), axis=1).min(1) > 2.0 ** -50 * size
             check(l[far], min(4, Gk * n), bias, score, G, Gk)
+
+
+@pytest.mark.parametrize("E,G,Gk", [(64, 8, 3), (60, 5, 2), (256, 8, 4)])
+def test_worths_past_float32(E, G, Gk):
+    """Biases whose sum only float64 holds: the groups of largest sum have the highest ids, or the lowest sums do."""
+    rng = np.random.default_rng(E)
+    n = E // G
+    for sign in (1, -1):
+        bias = np.repeat(sign * np.linspace(1.8e38, 3.2e38, G), n).astype(np.float32)
+        bias += (1e36 * rng.random(E)).astype(np.float32)
+        check(logits(rng, 40, E), 4, bias, "sigmoid", G, Gk)
+        check(logits(rng, 40, E), 4, bias, "softmax", G, Gk, renorm=False)
